@@ -13,7 +13,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtbe.so")
 SOURCES = ["tbe_api.cu", "forward.cu", "forward_small.cu", "forward_hot.cu", "preprocess.cu",
-           "update.cu", "hot_grad.cu", "noalloc.cu"]
+           "update.cu", "hot_grad.cu", "noalloc.cu", "experts.cu", "product_fp8.cu", "grads.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "-I", INCLUDE, "-I", CSRC]
@@ -28,7 +28,7 @@ def _nvcc():
 
 def _deps():
     hdrs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
-    return hdrs + [os.path.join(INCLUDE, "tbe.h")]
+    return hdrs + [os.path.join(INCLUDE, f) for f in sorted(os.listdir(INCLUDE))]
 
 
 def _stale(target, inputs):
