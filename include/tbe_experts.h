@@ -110,7 +110,8 @@ tbe_status tbe_quantize_weights(const void* w, int32_t dtype, int64_t experts, i
  * the transposed weights [E, K, N] (quantised in the same blocks, so they
  * hold the same values).  K, a_stride and the addresses of a and w must be
  * multiples of 16 (16-byte copies).
- * offsets are clamped into [0, rows] and to rise, whatever they hold.
+ * offsets are clamped into [0, rows], whatever they hold; an expert whose end
+ * lies before its start has no rows.
  * status: device int32 word, or NULL; a bounded device wait that gave up sets
  * TBE_ERR_TIMEOUT in it (the outputs are then incomplete).
  * Errors: TBE_EINVAL, TBE_EUNSUPPORTED, TBE_ECUDA. */

@@ -1,10 +1,14 @@
 // 8-bit rows and weights with a scale for each block of 128, and the experts'
 // products on them.  The operations are specified in include/tbe_experts.h.
+#include <cuda.h>
 #include <cuda_fp8.h>
+
+#include <type_traits>
 
 #include "internal.h"
 #include "rows.cuh"
 #include "tbe_experts.h"
+#include "tcgen05.cuh"
 
 namespace tbe {
 namespace {
@@ -19,10 +23,6 @@ __device__ __forceinline__ float block_scale(float amax) {
 
 __device__ __forceinline__ uint8_t to_e4m3(float v) {
   return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
-}
-
-__device__ __forceinline__ float from_e4m3(uint8_t v) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(v, __NV_E4M3)));
 }
 
 // One warp a sorted place's source row and block of 128 columns: the row is read
@@ -106,74 +106,650 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------------- product
 //
-// A CTA owns 64 output rows x 64 columns of one expert; a thread 4 x 4 of
-// them.  A grid row of row tiles is walked over the experts by every CTA.
-constexpr int kTile = 64, kStep = 32;
+// out[token, n] = sum over blocks b of 128 columns of (a_scale[token, b] *
+// w_scale[n / 128, b]) * P_b[token, n], with P_b the block's product of 8-bit
+// values: four tcgen05 MMAs (kind::f8f6f4, 32 columns each) into a
+// tensor-memory accumulator.  While the tensor cores form the next products,
+// the epilogue warps read P_b, scale it and add it to the tile's sums in their
+// registers: a scale differs from block to block, so the sum over blocks cannot
+// stay in tensor memory.
+//
+// A tile is 128 tokens x kTileN columns of n.  kTileN = 256 has two accumulators
+// in tensor memory and is for many tokens: it reads 96 bytes of shared memory a
+// multiply-add cycle where 128 columns read 128, all that shared memory gives.
+// kTileN = 128 has four accumulators, and finer tiles.
+//
+// Warps: 0 issues the TMA copies, 1 the MMAs; 2 and 3 bring the blocks' scales
+// to shared memory ahead of their use (an epilogue warp that waits for its own
+// scales costs more than the block), and clear the rows past the last expert;
+// 4..11 are the epilogue: warp w holds tokens 32 (w % 4) .. + 31 (one a lane)
+// and half w / 8 of the columns.  A tile with few tokens copies them 32 rows at a
+// time; the other rows of the MMA hold what the buffer held before and reach
+// only results that are not stored.
+//
+// kSplit: the CTAs of a cluster each form a part of the sum over blocks of one
+// tile; the parts meet in shared memory and are added in the order of the ranks.
+constexpr int kTileM = 128;
+constexpr int kScaleRing = 8;  // blocks whose scales stand in shared memory
+constexpr int kProductThreads = 384;
+constexpr int kRowBox = 32;
+constexpr int kScaleWarps = 2;
+constexpr int kEpilogueWarps = 8;
+constexpr int kTmemColumns = 512;
+constexpr int kRingBytes = 196608;
+constexpr int kMaxStages = 6;
+constexpr int kWarpStaging = 32 * 80;  // a warp's staging: 32 rows of 64 (+16) bytes
+constexpr int kProductSmem = kRingBytes + kEpilogueWarps * kWarpStaging + 1024;
 
-__device__ __forceinline__ int clamp_offset(const int* offsets, int e, int rows) {
-  const int v = offsets[e];
-  return v < 0 ? 0 : v > rows ? rows : v;
+template <int kTileN>
+struct ProductShape {
+  static constexpr int kAccumulators = kTmemColumns / kTileN;
+  static constexpr int kStageBytes = (kTileM + kTileN) * kBlock;  // tokens, then weight rows
+  static constexpr int kStages = kRingBytes / kStageBytes;
+  static constexpr int kSums = kTileN / 2;        // of an epilogue thread
+  static constexpr int kBlocksN = kTileN / kBlock;  // scale blocks of n
+  static constexpr int kJoinStride = kTileN + 4;  // split sums meet in the ring: [128][..] floats
+};
+
+struct ProductArgs {
+  const float* a_scale;
+  const float* w_scale;
+  const int* offsets;
+  void* out;
+  int64_t out_stride;
+  int* status;
+  int rows, n, k, experts;
+  int kb, nb, n_tiles;  // blocks of k and of n, tiles of n
+  int row_tiles;        // the most row tiles that the experts can have
+  bool vector_out;      // 16-byte stores of whole vectors are aligned
+};
+
+struct ProductShared {
+  // full: a stage's copies have landed; done: the MMAs that read it are done, so the stage is
+  // free and the block's product stands in its accumulator, and the block's scales are there;
+  // taken: the accumulator has been read
+  unsigned long long full[kMaxStages], done[kMaxStages], taken[4], drain;
+  uint32_t tmem;
+  int dead;
+  float scale[kScaleRing][2][kTileM];  // [block][128 columns of n][token]
+  int warp_sum[kProductThreads / 32];
+  int tile0[TBE_MAX_EXPERTS + 1];  // first row tile of each expert
+};
+
+__device__ __forceinline__ int group_start(const ProductArgs& P, int e) {
+  if (!P.offsets) return e ? P.rows : 0;
+  const int v = P.offsets[e];
+  return v < 0 ? 0 : v > P.rows ? P.rows : v;
+}
+
+// A wait of a role: gives up at the bound, or soon after another role has.
+// The whole warp calls it and goes on or gives up as one.
+__device__ __forceinline__ bool role_wait(unsigned long long* bar, uint32_t parity,
+                                          volatile int* dead) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  bool got = false;
+  for (uint32_t i = 0; i < kSpinLimit && !got; ++i) {
+    got = mbar_try_wait(bar, parity);
+    if (i > 64 && !got) {
+      if (*dead) break;
+      __nanosleep(64);
+    }
+  }
+  if (!got) *dead = 1;
+  return __all_sync(0xffffffffu, got);
+}
+
+// Both barriers' phases are over, asked without waiting: the two questions'
+// latencies overlap.
+__device__ __forceinline__ bool both_over(unsigned long long* x, uint32_t px,
+                                          unsigned long long* y, uint32_t py) {
+  uint32_t over;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "and.pred p, p, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(over)
+      : "r"(smem_u32(x)), "r"(px), "r"(smem_u32(y)), "r"(py)
+      : "memory");
+  return __all_sync(0xffffffffu, over);
+}
+
+__device__ __forceinline__ bool elected() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y,
+                                         unsigned long long* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(unsigned long long* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Operand rows of 128 bytes, written by TMA in its 128-byte swizzle: 8-row
+// groups 1024 bytes apart (layout type 2 at bit 61).
+__device__ __forceinline__ uint64_t swizzled_desc(const void* p) {
+  return make_smem_desc(p, 16, 1024) | (2ull << 61);
+}
+
+__device__ __forceinline__ void mma_f8(uint32_t tmem, uint64_t adesc, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Starts reading 32 columns of this warp's 32 tensor-memory lanes; the values
+// are there after tmem_arrived on the same registers.
+__device__ __forceinline__ void tmem_read(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+// Two fp32 multiply-adds in one instruction: acc += v * s on a pair.  Volatile,
+// so that they stay where they are written: after the accumulator is handed back.
+__device__ __forceinline__ void fma_pair(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s) {
+  uint64_t v;
+  asm volatile("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+  asm volatile("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(s));
+}
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ float2 pair_values(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ float load_cluster(uint32_t addr, uint32_t rank) {
+  uint32_t remote;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
+  return v;
+}
+
+struct ProductTile {
+  int expert, row0, rows, n0;  // first row, rows of the tile, first column
+};
+
+// Row tiles of all experts before each, in shared memory; the whole CTA.  Sums
+// stop at P.row_tiles, which offsets that rise do not reach.
+__device__ __forceinline__ void build_tiles(const ProductArgs& P, ProductShared& S) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int carry = 0;
+  for (int e0 = 0; e0 < P.experts; e0 += kProductThreads) {
+    const int e = e0 + static_cast<int>(threadIdx.x);
+    int tiles = 0;
+    if (e < P.experts) {
+      const int c = group_start(P, e + 1) - group_start(P, e);
+      tiles = c > 0 ? min((c + kTileM - 1) / kTileM, P.row_tiles) : 0;
+    }
+    int incl = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl = min(incl + y, P.row_tiles);
+    }
+    if (lane == 31) S.warp_sum[warp] = incl;
+    __syncthreads();
+    int before = carry;
+    for (int w = 0; w < kProductThreads / 32; ++w) {
+      if (w < warp) before = min(before + S.warp_sum[w], P.row_tiles);
+      carry = min(carry + S.warp_sum[w], P.row_tiles);
+    }
+    if (e < P.experts) S.tile0[e + 1] = min(before + incl, P.row_tiles);
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) S.tile0[0] = 0;
+}
+
+// Tile t of the walk: experts in order, and in an expert its row tiles first.
+template <int kTileN>
+__device__ __forceinline__ ProductTile tile_at(const ProductArgs& P, const ProductShared& S,
+                                               int t) {
+  int lo = 0, hi = P.experts - 1;
+  while (lo < hi) {  // the last expert whose tiles start at or before t
+    const int mid = (lo + hi + 1) >> 1;
+    if (S.tile0[mid] * P.n_tiles <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  const int m_tiles = S.tile0[lo + 1] - S.tile0[lo];
+  const int at = t - S.tile0[lo] * P.n_tiles;
+  const int start = group_start(P, lo), end = group_start(P, lo + 1);
+  ProductTile T;
+  T.expert = lo;
+  T.row0 = start + at % m_tiles * kTileM;
+  T.rows = end - T.row0 < kTileM ? end - T.row0 : kTileM;
+  T.n0 = at / m_tiles * kTileN;
+  return T;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256)
-    product_kernel(const uint8_t* __restrict__ a, int64_t a_stride,
-                   const float* __restrict__ a_scale, const uint8_t* __restrict__ w,
-                   const float* __restrict__ w_scale, const int* __restrict__ offsets, int rows,
-                   int64_t n, int64_t k, int experts, T* __restrict__ out, int64_t out_stride) {
-  __shared__ float sa[kStep][kTile + 1], sw[kStep][kTile + 1];
-  const int kb = static_cast<int>((k + kBlock - 1) / kBlock);
-  const int nb = static_cast<int>((n + kBlock - 1) / kBlock);
-  const int64_t n0 = static_cast<int64_t>(blockIdx.y) * kTile;
-  const int tr = threadIdx.x / 16 * 4, tc = threadIdx.x % 16 * 4;
-  int tile = blockIdx.x, start = 0;
-  for (int e = 0; e <= experts; ++e) {  // e == experts: the rows past the last expert
-    int end = rows;
-    if (e < experts && offsets) {
-      end = clamp_offset(offsets, e + 1, rows);
-      if (e == 0) start = clamp_offset(offsets, 0, rows);
-      if (end < start) end = start;
-    }
-    const int tiles = (end - start + kTile - 1) / kTile;
-    for (; tile < tiles; tile += gridDim.x) {
-      const int r0 = start + tile * kTile;
-      float acc[4][4] = {};
-      for (int b = 0; b < kb && e < experts; ++b) {
-        float part[4][4] = {};
-        for (int64_t k0 = static_cast<int64_t>(b) * kBlock; k0 < k && k0 < (b + 1) * kBlock;
-             k0 += kStep) {
-          __syncthreads();
-          for (int i = threadIdx.x; i < kTile * kStep; i += 256) {
-            const int r = i / kStep, c = i % kStep;
-            sa[c][r] = r0 + r < end && k0 + c < k ? from_e4m3(a[(r0 + r) * a_stride + k0 + c]) : 0.f;
-            sw[c][r] = n0 + r < n && k0 + c < k ? from_e4m3(w[(e * n + n0 + r) * k + k0 + c]) : 0.f;
-          }
-          __syncthreads();
-          for (int c = 0; c < kStep; ++c)
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Stores a warp's 32 rows x kSums columns: 64 bytes of a row at a time through
+// the warp's staging buffer, so that a store instruction covers 8 rows x 64
+// contiguous bytes.  kWhole: all rows and columns count and 16-byte stores are
+// aligned.
+template <typename T, int kSums, bool kWhole>
+__device__ __forceinline__ void store_tile(const ProductArgs& P, char* staging, int row0, int rows,
+                                           int col0, const uint64_t (&acc)[kSums / 2]) {
+  constexpr int kCols = 64 / static_cast<int>(sizeof(T));  // columns of one pass
+  constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+  const int lane = threadIdx.x & 31;
+  uint4* mine = reinterpret_cast<uint4*>(staging + lane * 80);
+  const char* src = staging + lane / 4 * 80 + lane % 4 * 16;
+  const int64_t pitch = P.out_stride * 8;  // eight rows
+  T* dst = static_cast<T*>(P.out) + (static_cast<int64_t>(row0) + lane / 4) * P.out_stride + col0 +
+           lane % 4 * kVec;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+  for (int c0 = 0; c0 < kSums; c0 += kCols) {
+    if (!kWhole && col0 + c0 >= P.n) break;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) part[i][j] = fmaf(sa[c][tr + i], sw[c][tc + j], part[i][j]);
-        }
+    for (int v = 0; v < 4; ++v) {
+      uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (r0 + tr + i >= end || n0 + tc >= n) continue;
-          const float s = a_scale[static_cast<int64_t>(r0 + tr + i) * kb + b] *
-                          w_scale[(static_cast<int64_t>(e) * nb + (n0 + tc) / kBlock) * kb + b];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(s, part[i][j], acc[i][j]);
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+          const float2 f = pair_values(acc[(c0 + v * 4) / 2 + i / 2]);
+          w[i] = __float_as_uint(i % 2 ? f.y : f.x);
+        } else {
+          const float2 f = pair_values(acc[(c0 + v * 8) / 2 + i]);
+          w[i] = pack2<T>(f.x, f.y);
         }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (r0 + tr + i < end && n0 + tc + j < n)
-            out[(r0 + tr + i) * out_stride + n0 + tc + j] = from_f32<T>(acc[i][j]);
+      mine[v] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    tile -= tiles;
-    start = end;
+    __syncwarp();
+    if constexpr (kWhole) {
+      uint4 q[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) q[g] = *reinterpret_cast<const uint4*>(src + g * 8 * 80);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) *reinterpret_cast<uint4*>(dst + g * pitch + c0) = q[g];
+    } else {
+      const int col = col0 + c0 + lane % 4 * kVec;
+      for (int g = 0; g < 4; ++g) {
+        if (g * 8 + lane / 4 >= rows) break;
+        const char* from = src + g * 8 * 80;
+        T* to = dst + g * pitch + c0;
+        if (P.vector_out && col + kVec <= P.n) {
+          *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
+        } else {
+          for (int i = 0; i < kVec && col + i < P.n; ++i)
+            to[i] = reinterpret_cast<const T*>(from)[i];
+        }
+      }
+    }
+    __syncwarp();
   }
+}
+
+template <typename T, int kTileN, bool kSplit>
+__global__ void __launch_bounds__(kProductThreads, 1)
+    product_kernel(const __grid_constant__ CUtensorMap a_map,
+                   const __grid_constant__ CUtensorMap a_part_map,
+                   const __grid_constant__ CUtensorMap w_map,
+                   const __grid_constant__ ProductArgs P) {
+  using Shape = ProductShape<kTileN>;
+  constexpr int kStages = Shape::kStages, kStageBytes = Shape::kStageBytes;
+  constexpr int kSums = Shape::kSums, kAccumulators = Shape::kAccumulators;
+  constexpr int kBlocksN = Shape::kBlocksN;
+  extern __shared__ char product_smem[];
+  __shared__ ProductShared S;
+  char* ring = reinterpret_cast<char*>(
+      (reinterpret_cast<uintptr_t>(product_smem) + 1023) & ~uintptr_t(1023));
+  char* staging = ring + kRingBytes;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  volatile int* dead = &S.dead;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&S.full[i], 1);
+      mbar_init(&S.done[i], 1 + kScaleWarps);
+    }
+    for (int i = 0; i < kAccumulators; ++i)
+      mbar_init(&S.taken[i], kEpilogueWarps);
+    mbar_init(&S.drain, 1);
+    S.dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 2) tmem_alloc(&S.tmem, kTmemColumns);
+  build_tiles(P, S);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = S.tmem;
+  const int tiles = S.tile0[P.experts] * P.n_tiles;
+  const int split = kSplit ? static_cast<int>(cluster_size()) : 1;
+  const int part = kSplit ? static_cast<int>(cluster_rank()) : 0;
+  // tiles first, first + stride, ...; with kSplit a cluster has one
+  const int first = static_cast<int>(blockIdx.x) / split;
+  const int stride = kSplit ? tiles + 1 : static_cast<int>(gridDim.x);
+  const int b0 = static_cast<int>(static_cast<int64_t>(P.kb) * part / split);
+  const int b1 = static_cast<int>(static_cast<int64_t>(P.kb) * (part + 1) / split);
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0) {
+      int stage = 0, issued = 0;
+      uint32_t parity = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += stride) {
+        const ProductTile tile = tile_at<kTileN>(P, S, t);
+        const int mine = (tile.rows + kRowBox - 1) / kRowBox * kRowBox;  // rows to copy
+        const int w0 = tile.expert * P.n + tile.n0;
+        for (int b = b0; b < b1; ++b) {
+          if (!role_wait(&S.done[stage], parity ^ 1, dead)) {
+            ok = false;
+            break;
+          }
+          char* a = ring + stage * kStageBytes;
+          char* w = a + kTileM * kBlock;
+          if (elected()) {
+            unsigned long long* bar = &S.full[stage];
+            mbar_expect_tx(bar, (mine + kTileN) * kBlock);
+            tma_load(w, &w_map, b * kBlock, w0, bar);
+            if (mine == kTileM)
+              tma_load(a, &a_map, b * kBlock, tile.row0, bar);
+            else
+              for (int r = 0; r < mine; r += kRowBox)
+                tma_load(a + r * kBlock, &a_part_map, b * kBlock, tile.row0 + r, bar);
+          }
+          __syncwarp();
+          ++issued;
+          if (++stage == kStages) stage = 0, parity ^= 1;
+        }
+      }
+      if (!ok)  // let the copies in flight land before the CTA ends
+        for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+          mbar_wait(&S.full[i % kStages], (i / kStages) & 1);
+    } else if (warp == 1) {
+      const uint32_t idesc = make_idesc(0, kTileM, kTileN);  // e4m3 x e4m3 -> fp32
+      const uint64_t a_desc = swizzled_desc(ring), w_desc = swizzled_desc(ring + kTileM * kBlock);
+      int stage = 0, slot = 0;
+      uint32_t parity = 0, tparity = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += stride) {
+        for (int b = b0; b < b1; ++b) {
+          if (!both_over(&S.taken[slot], tparity ^ 1, &S.full[stage], parity) &&
+              (!role_wait(&S.taken[slot], tparity ^ 1, dead) ||
+               !role_wait(&S.full[stage], parity, dead))) {
+            ok = false;
+            break;
+          }
+          fence_after_sync();
+          const uint64_t at = static_cast<uint64_t>(stage * (kStageBytes >> 4));
+          if (elected()) {
+#pragma unroll
+            for (int i = 0; i < kBlock / 32; ++i)  // 32 columns are 32 bytes: 2 in the address
+              mma_f8(tmem + slot * kTileN, a_desc + at + i * 2, w_desc + at + i * 2, idesc, i > 0);
+            mma_commit(&S.done[stage]);
+          }
+          __syncwarp();
+          if (++stage == kStages) stage = 0, parity ^= 1;
+          if (++slot == kAccumulators) slot = 0, tparity ^= 1;
+        }
+      }
+      if (!ok) {
+        if (elected()) mma_commit(&S.drain);
+        __syncwarp();
+        mbar_wait(&S.drain, 0);
+      }
+    } else {
+      // A block's scales replace those of the block kScaleRing earlier.  Those have been read
+      // when the MMAs of the block kAccumulators earlier are done, for they took its accumulator.
+      constexpr int kAhead = 4;  // blocks whose scales are on their way
+      int stage = 0, slot = 0, old_stage = 0, since = 0;
+      uint32_t old_parity = 0;
+      bool ok = true;
+      const int r0 = (warp - 2) * 64 + lane, r1 = r0 + 32;  // this lane's two tokens
+      for (int t = first; t < tiles && ok; t += stride) {
+        const ProductTile tile = tile_at<kTileN>(P, S, t);
+        const float* a0 = P.a_scale + static_cast<int64_t>(tile.row0 + r0) * P.kb;
+        const float* a1 = a0 + static_cast<int64_t>(32) * P.kb;
+        const int wb = tile.n0 / kBlock;
+        const float* w0 = P.w_scale + (static_cast<int64_t>(tile.expert) * P.nb + wb) * P.kb;
+        const bool on0 = r0 < tile.rows, on1 = r1 < tile.rows, two = kBlocksN == 2 && wb + 1 < P.nb;
+        const auto at = [&](const float* p, int b, bool on) {
+          return on && b < b1 ? __ldg(p + b) : 0.f;
+        };
+        float sa0[kAhead], sa1[kAhead], sw[kAhead][kBlocksN];
+        const auto load = [&](int i, int b) {
+          sa0[i] = at(a0, b, on0);
+          sa1[i] = at(a1, b, on1);
+          sw[i][0] = at(w0, b, true);
+          if constexpr (kBlocksN == 2) sw[i][1] = at(w0 + P.kb, b, two);
+        };
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) load(i, b0 + i);
+        for (int b4 = b0; b4 < b1 && ok; b4 += kAhead) {
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            const int b = b4 + i;
+            if (b >= b1) break;
+            if (since < kAccumulators) {
+              ++since;
+            } else {
+              if (!role_wait(&S.done[old_stage], old_parity, dead)) {
+                ok = false;
+                break;
+              }
+              if (++old_stage == kStages) old_stage = 0, old_parity ^= 1;
+            }
+#pragma unroll
+            for (int h = 0; h < kBlocksN; ++h) {
+              S.scale[slot][h][r0] = sa0[i] * sw[i][h];
+              S.scale[slot][h][r1] = sa1[i] * sw[i][h];
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.done[stage]);
+            slot = (slot + 1) % kScaleRing;
+            load(i, b + kAhead);
+            if (++stage == kStages) stage = 0;
+          }
+        }
+      }
+      // the rows past the last expert
+      T* out = static_cast<T*>(P.out);
+      for (int64_t r = group_start(P, P.experts) + static_cast<int64_t>(blockIdx.x); r < P.rows;
+           r += gridDim.x)
+        for (int c = threadIdx.x - 64; c < P.n; c += 64)
+          out[r * P.out_stride + c] = from_f32<T>(0.f);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    char* mine = staging + (warp - 4) * kWarpStaging;
+    const uint32_t taddr0 = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kSums;
+    int stage = 0;
+    uint32_t parity = 0, count = 0;  // count: blocks so far
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += stride) {
+      const ProductTile tile = tile_at<kTileN>(P, S, t);
+      const int row0 = tile.row0 + quarter * 32;
+      const int rows = tile.rows - quarter * 32;  // of this warp; none or less: nothing to do
+      const int col0 = tile.n0 + half * kSums;
+      const bool on = rows > 0 && col0 < P.n;
+      uint64_t acc[kSums / 2];
+#pragma unroll
+      for (int i = 0; i < kSums / 2; ++i) acc[i] = 0;
+      for (int b = b0; b < b1; ++b) {
+        if (!role_wait(&S.done[stage], parity, dead)) {
+          ok = false;
+          break;
+        }
+        fence_after_sync();
+        const uint32_t slot = count % kAccumulators;
+        const float sc = S.scale[count % kScaleRing][half * kSums / kBlock][quarter * 32 + lane];
+        const uint64_t s = pair_of(sc, sc);
+        const uint32_t taddr = taddr0 + slot * kTileN;
+        uint32_t v[2][32];
+        if (on) {
+          tmem_read(taddr, v[0]);
+          tmem_read(taddr + 32, v[1]);
+          if constexpr (kSums == 128) {  // 64 columns are on their way at a time
+            tmem_arrived(v[0]);
+            tmem_arrived(v[1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                fma_pair(acc[h * 16 + i], v[h][2 * i], v[h][2 * i + 1], s);
+              tmem_read(taddr + (2 + h) * 32, v[h]);
+            }
+          }
+          tmem_arrived(v[0]);
+          tmem_arrived(v[1]);
+        }
+        // the accumulator is handed back before its last columns are added
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.taken[slot]);
+        if (on) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              fma_pair(acc[kSums / 2 - 32 + h * 16 + i], v[h][2 * i], v[h][2 * i + 1], s);
+        }
+        if (++stage == kStages) stage = 0, parity ^= 1;
+        ++count;
+      }
+      if constexpr (kSplit) {
+        if (on && ok) {
+          float* join = reinterpret_cast<float*>(ring) + (quarter * 32 + lane) * Shape::kJoinStride +
+                        half * kSums;
+#pragma unroll
+          for (int i = 0; i < kSums / 2; i += 2) {
+            const float2 f = pair_values(acc[i]), g = pair_values(acc[i + 1]);
+            *reinterpret_cast<float4*>(join + 2 * i) = make_float4(f.x, f.y, g.x, g.y);
+          }
+        }
+      } else if (on && ok) {
+        if (rows >= 32 && col0 + kSums <= P.n && P.vector_out)
+          store_tile<T, kSums, true>(P, mine, row0, rows, col0, acc);
+        else
+          store_tile<T, kSums, false>(P, mine, row0, rows, col0, acc);
+      }
+    }
+  }
+  __syncwarp();
+  if constexpr (kSplit) {
+    cluster_sync();
+    if (first < tiles && !S.dead) {
+      const ProductTile tile = tile_at<kTileN>(P, S, first);
+      const int cols = kTileN / split, c0 = part * cols;
+      const uint32_t base = smem_u32(ring);
+      T* out = static_cast<T*>(P.out);
+      for (int i = threadIdx.x; i < tile.rows * cols; i += kProductThreads) {
+        const int r = i / cols, c = c0 + i % cols;
+        if (tile.n0 + c >= P.n) continue;
+        float sum = 0.f;
+        for (int p = 0; p < split; ++p) sum += load_cluster(base + (r * Shape::kJoinStride + c) * 4, p);
+        out[(static_cast<int64_t>(tile.row0) + r) * P.out_stride + tile.n0 + c] = from_f32<T>(sum);
+      }
+    }
+    cluster_sync();
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  if (warp == 2) tmem_dealloc(tmem, kTmemColumns);
+  if (threadIdx.x == 0 && S.dead && P.status) atomicOr(P.status, TBE_ERR_TIMEOUT);
+}
+
+// A map of an 8-bit matrix for 128-byte-swizzled boxes of 128 columns.
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+bool make_map(CUtensorMap* map, const uint8_t* base, int64_t rows, int64_t cols, int64_t stride,
+              int box_rows) {
+  const EncodeTiled encode = encode_tiled();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};
+  const cuuint32_t box[2] = {kBlock, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t steps[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides,
+                box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 tbe_status launched() {
@@ -245,7 +821,6 @@ extern "C" tbe_status tbe_expert_product(const uint8_t* a, int64_t a_stride, con
                                          const int32_t* offsets, int64_t rows, int64_t n,
                                          int64_t k, int32_t experts, void* out, int32_t out_dtype,
                                          int64_t out_stride, int32_t* status, void* stream) {
-  (void)status;
   if (rows < 0 || n < 0 || k < 1 || experts < 1) return TBE_EINVAL;
   if (!dtype_bytes(out_dtype)) return TBE_EUNSUPPORTED;
   if (rows > INT32_MAX || n > INT32_MAX || k > INT32_MAX || experts > TBE_MAX_EXPERTS ||
@@ -256,17 +831,73 @@ extern "C" tbe_status tbe_expert_product(const uint8_t* a, int64_t a_stride, con
       out_stride < n)
     return TBE_EINVAL;
   if (!aligned_to(a_scale, 4) || !aligned_to(w_scale, 4) || !aligned_to(offsets, 4) ||
-      !aligned_to(out, dtype_bytes(out_dtype)))
+      !aligned_to(out, dtype_bytes(out_dtype)) || !aligned_to(status, 4))
     return TBE_EINVAL;
   if (k % 16 || a_stride % 16 || !aligned_to(a, 16) || !aligned_to(w, 16)) return TBE_EUNSUPPORTED;
-  if ((n + kTile - 1) / kTile > 65535) return TBE_EUNSUPPORTED;
-  return for_dtype(out_dtype, [&](auto t) {
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return TBE_ECUDA;
+  ProductArgs P;
+  P.a_scale = a_scale;
+  P.w_scale = w_scale;
+  P.offsets = offsets;
+  P.out = out;
+  P.out_stride = out_stride;
+  P.status = status;
+  P.rows = static_cast<int>(rows);
+  P.n = static_cast<int>(n);
+  P.k = static_cast<int>(k);
+  P.experts = experts;
+  P.kb = static_cast<int>((k + kBlock - 1) / kBlock);
+  P.nb = static_cast<int>((n + kBlock - 1) / kBlock);
+  const int ob = dtype_bytes(out_dtype);
+  P.vector_out = aligned_to(out, 16) && out_stride * ob % 16 == 0;
+  CUtensorMap a_map, a_part_map;
+  if (!make_map(&a_map, a, rows, k, a_stride, kTileM) ||
+      !make_map(&a_part_map, a, rows, k, a_stride, kRowBox))
+    return TBE_ECUDA;
+  const auto launch = [&](auto t, auto tile_n, auto split_tag, int split) -> tbe_status {
     using T = decltype(t);
-    const dim3 grid(static_cast<unsigned>(rows / kTile + 1 < 1024 ? rows / kTile + 1 : 1024),
-                    static_cast<unsigned>((n + kTile - 1) / kTile));
-    product_kernel<T><<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(
-        a, a_stride, a_scale, w, w_scale, offsets, static_cast<int>(rows), n, k, experts,
-        static_cast<T*>(out), out_stride);
+    constexpr int kTileN = decltype(tile_n)::value;
+    constexpr bool kSplit = decltype(split_tag)::value;
+    P.n_tiles = static_cast<int>((n + kTileN - 1) / kTileN);
+    CUtensorMap w_map;
+    if (!make_map(&w_map, w, static_cast<int64_t>(experts) * n, k, k, kTileN)) return TBE_ECUDA;
+    const auto kernel = product_kernel<T, kTileN, kSplit>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem) !=
+        cudaSuccess)
+      return TBE_ECUDA;
+    // tiles, at most (every expert's last one may be a part)
+    P.row_tiles = static_cast<int>(rows / kTileM + (experts < rows ? experts : rows));
+    const int64_t most = static_cast<int64_t>(P.row_tiles) * P.n_tiles;
+    if (most > INT32_MAX / 8) return TBE_EUNSUPPORTED;  // the kernel counts tiles in 32 bits
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(kSplit ? most * split : most < sms ? most : sms));
+    cfg.blockDim = dim3(kProductThreads);
+    cfg.dynamicSmemBytes = kProductSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kSplit ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kernel, a_map, a_part_map, w_map, P) != cudaSuccess)
+      return TBE_ECUDA;
     return launched();
+  };
+  using Narrow = std::integral_constant<int, 128>;
+  using Wide = std::integral_constant<int, 256>;
+  return for_dtype(out_dtype, [&](auto t) {
+    const int64_t tiles =
+        (rows / kTileM + (experts < rows ? experts : rows)) * ((n + 127) / 128);
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= sms && P.kb >= split * 4) split *= 2;
+    if (split > 1) return launch(t, Narrow{}, std::true_type{}, split);
+    if (rows < static_cast<int64_t>(experts) * 512)
+      return launch(t, Narrow{}, std::false_type{}, 1);
+    return launch(t, Wide{}, std::false_type{}, 1);
   });
 }
