@@ -10,7 +10,8 @@
  * The norm holds over the whole range of fp32: each thread's short fp32 sums
  * of squares are formed again with a power-of-two factor where they leave
  * [2^-60, 2^100], and are joined in fp64 in an order that depends on the sizes
- * alone.  An infinity or NaN among the gradients makes the norm infinite or
+ * and on where in 16 bytes each tensor begins: the same call gives the same
+ * bits.  An infinity or NaN among the gradients makes the norm infinite or
  * NaN, and c then follows the formula (0, or NaN).
  *
  * Ordering, allocation and errors follow tbe.h.

@@ -1,6 +1,8 @@
 // Expert layer: assignments sorted by expert, the tokens' rows carried to
 // their experts and back with weights applied, and the gradients of both.
 // The operations are specified in include/tbe_experts.h.
+#include <type_traits>
+
 #include "internal.h"
 #include "rows.cuh"
 #include "tbe_experts.h"
@@ -12,18 +14,37 @@ constexpr unsigned kAll = 0xffffffffu;
 
 // ---------------------------------------------------------------------- sort
 //
-// A counting sort: a warp takes a contiguous chunk of the assignments, counts
-// its experts in its own shared-memory row, and after a scan over (expert,
-// warp) walks the chunk again, 32 assignments at a time, giving each its place:
-// the warp's running count of the expert plus the number of lower lanes with
-// the same expert.  Stable by construction, no atomics on results.  Dropped
-// assignments are counted as expert E, which comes last.
+// A counting sort in one launch: one cluster of up to 16 CTAs, a warp a contiguous
+// chunk of the assignments.  A warp counts its experts in its own row of shared
+// memory; the rows are scanned over (expert, CTA, warp), the CTAs reading one
+// another's totals in shared memory; then each warp walks its chunk again, 32
+// assignments at a time, giving each its place: the warp's running count of the
+// expert plus the number of lower lanes with the same expert.  Stable by
+// construction, no atomics on results.  Dropped assignments are counted as
+// expert E, which comes last.
 constexpr int kSortWarps = 32;
+constexpr int kSortUnroll = 4;      // rounds of 32 assignments whose loads are in flight
+constexpr int kSortPerCta = 2048;   // assignments from which another CTA pays
+constexpr int kSortMostCtas = 16;
 
 template <typename IdT>
-__device__ __forceinline__ int expert_of(const IdT* ids, int64_t a, int experts) {
-  const IdT e = ids[a];
+__device__ __forceinline__ int expert_of(IdT e, int experts) {
   return e >= 0 && e < static_cast<IdT>(experts) ? static_cast<int>(e) : experts;
+}
+
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ int load_from_cta(const int* p, int rank) {
+  const unsigned addr = static_cast<unsigned>(__cvta_generic_to_shared(p));
+  unsigned remote;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+  return v;
 }
 
 template <typename IdT>
@@ -33,38 +54,73 @@ __global__ void __launch_bounds__(kSortWarps * 32)
   extern __shared__ int sort_smem[];
   __shared__ int warp_sum[kSortWarps];
   const int buckets = experts + 1;
-  int* count = sort_smem;  // [kSortWarps][buckets]
+  int* total = sort_smem;            // [buckets] this CTA's assignments of each expert
+  int* count = sort_smem + buckets;  // [kSortWarps][buckets]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ctas = gridDim.x, rank = blockIdx.x;  // one cluster
   for (int i = threadIdx.x; i < kSortWarps * buckets; i += blockDim.x) count[i] = 0;
   __syncthreads();
-  const int64_t chunk = ((static_cast<int64_t>(n) + kSortWarps * 32 - 1) / (kSortWarps * 32)) * 32;
-  const int64_t first = warp * chunk;
+  const int warps = ctas * kSortWarps;
+  const int64_t chunk = (static_cast<int64_t>(n) + warps * 32 - 1) / (warps * 32) * 32;
+  const int64_t first = (static_cast<int64_t>(rank) * kSortWarps + warp) * chunk;
   const int64_t last = first + chunk < n ? first + chunk : n;
   int* mine = count + warp * buckets;
-  for (int64_t a = first + lane; a < last; a += 32) atomicAdd(mine + expert_of(ids, a, experts), 1);
+  for (int64_t a0 = first + lane; a0 < last; a0 += 32 * kSortUnroll) {
+    IdT e[kSortUnroll];
+#pragma unroll
+    for (int u = 0; u < kSortUnroll; ++u) e[u] = a0 + 32 * u < last ? ids[a0 + 32 * u] : IdT(0);
+#pragma unroll
+    for (int u = 0; u < kSortUnroll; ++u)
+      if (a0 + 32 * u < last) atomicAdd(mine + expert_of(e[u], experts), 1);
+  }
   __syncthreads();
-  // exclusive scan over (expert, warp); one expert per thread, in rounds
+  for (int e = threadIdx.x; e < buckets; e += blockDim.x) {
+    int c = 0;
+    for (int w = 0; w < kSortWarps; ++w) c += count[w * buckets + e];
+    total[e] = c;
+  }
+  if (ctas > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  // exclusive scan over (expert, CTA, warp); one expert per thread, in rounds
   int carry = 0;
   for (int e0 = 0; e0 < buckets; e0 += blockDim.x) {
     const int e = e0 + threadIdx.x;
-    int total = 0;
-    if (e < buckets)
-      for (int w = 0; w < kSortWarps; ++w) total += count[w * buckets + e];
-    int incl = total;
+    int all = 0, before_me = 0;
+    if (e < buckets) {
+      if (ctas == 1) {
+        all = total[e];
+      } else {
+        for (int r = 0; r < ctas; ++r) {
+          const int c = load_from_cta(total + e, r);
+          all += c;
+          before_me += r < rank ? c : 0;
+        }
+      }
+    }
+    int incl = all;
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(kAll, incl, o);
       if (lane >= o) incl += y;
     }
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    int before = carry;
-    for (int w = 0; w < kSortWarps; ++w) {
-      if (w < warp) before += warp_sum[w];
-      carry += warp_sum[w];
+    int sums = warp_sum[lane];  // kSortWarps of them, scanned by every warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kAll, sums, o);
+      if (lane >= o) sums += y;
     }
-    int at = before + incl - total;
+    const int before = carry + (warp ? __shfl_sync(kAll, sums, warp - 1) : 0);
+    carry += __shfl_sync(kAll, sums, 31);
     if (e < buckets) {
-      offsets[e] = at;  // offsets[E]: the first dropped place, the number kept
+      int at = before + incl - all;
+      if (rank == 0) offsets[e] = at;  // offsets[E]: the first dropped place, the number kept
+      at += before_me;
       for (int w = 0; w < kSortWarps; ++w) {
         const int c = count[w * buckets + e];
         count[w * buckets + e] = at;
@@ -73,28 +129,41 @@ __global__ void __launch_bounds__(kSortWarps * 32)
     }
     __syncthreads();
   }
-  for (int64_t a0 = first; a0 < last; a0 += 32) {
-    const int64_t a = a0 + lane;
-    const bool on = a < last;
-    const unsigned live = __ballot_sync(kAll, on);
-    if (on) {
-      const int e = expert_of(ids, a, experts);
-      const unsigned same = __match_any_sync(live, e);
-      const int place = mine[e] + __popc(same & ((1u << lane) - 1));
-      __syncwarp(live);
-      if ((same >> lane) == 1u) mine[e] = place + 1;  // the highest lane of its expert
-      position[a] = e < experts ? place : -1;
-      source[place] = e < experts ? static_cast<int>(a) : -1;
+  if (ctas > 1) cluster_arrive();  // this CTA reads no other's memory any more
+  for (int64_t a0 = first; a0 < last; a0 += 32 * kSortUnroll) {
+    IdT id[kSortUnroll];
+#pragma unroll
+    for (int u = 0; u < kSortUnroll; ++u) {
+      const int64_t a = a0 + 32 * u + lane;
+      id[u] = a < last ? ids[a] : IdT(0);
     }
-    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < kSortUnroll; ++u) {
+      const int64_t a = a0 + 32 * u + lane;
+      const bool on = a < last;
+      const int e = on ? expert_of(id[u], experts) : -1;
+      const unsigned same = __match_any_sync(kAll, e);
+      int place = 0;
+      if (on) place = mine[e] + __popc(same & ((1u << lane) - 1));
+      __syncwarp();
+      if (on && (same >> lane) == 1u) mine[e] = place + 1;  // the highest lane of its expert
+      __syncwarp();
+      if (on) {
+        position[a] = e < experts ? place : -1;
+        source[place] = e < experts ? static_cast<int>(a) : -1;
+      }
+    }
   }
+  if (ctas > 1) cluster_wait();  // no CTA ends while another may read its totals
 }
 
 // --------------------------------------------------------------- moving rows
 //
-// A group of threads serves one token: it reads the token's row once and
-// writes (or reads and sums) its k rows.  `log_group` threads a token, the
-// block's 256 threads serving several narrow tokens or one wide one.
+// Memory bounds these kernels: a token's row is read once and its k rows are
+// written, or the k rows are read and one is written.  A group of threads
+// serves one token, `log_group` threads each; the block's 256 threads serve
+// several narrow tokens or one wide one.  Rows that do not begin on 16-byte
+// boundaries are moved in 16-byte vectors all the same (inner_span, load_vec).
 constexpr int kMoveThreads = 256;
 
 struct Group {
@@ -114,113 +183,246 @@ __device__ __forceinline__ int64_t kept_rows(const int* offsets, int experts, in
   return m < 0 ? 0 : m > rows ? rows : m;
 }
 
-template <typename T, int V>
+// Clears rows [first, last): those of dropped assignments.
+template <typename T, bool kAligned>
+__device__ __forceinline__ void clear_rows(int t, int threads, int width, int64_t first,
+                                           int64_t last, T* rows, int64_t stride) {
+  Pack<T, kVec<T>> zero;
+#pragma unroll
+  for (int i = 0; i < kVec<T>; ++i) zero.v[i] = from_f32<T>(0.f);
+  for (int64_t r = first; r < last; ++r) {
+    T* row = rows + r * stride;
+    const Span s = inner_span<T, kAligned>(row, width);
+    for (int e = s.lo + t * kVec<T>; e < s.hi; e += threads * kVec<T>) store_vec(row + e, zero);
+    for_ends(s, width, t, threads, [&](int e) { row[e] = from_f32<T>(0.f); });
+  }
+}
+
+template <typename T, bool kAligned>
 __global__ void __launch_bounds__(kMoveThreads)
-    dispatch_kernel(const T* __restrict__ x, int64_t tokens, int k, int vecs, int64_t x_stride,
+    dispatch_kernel(const T* __restrict__ x, int64_t tokens, int k, int width, int64_t x_stride,
                     const int* __restrict__ offsets, int experts, const int* __restrict__ position,
                     T* __restrict__ rows, int64_t rows_stride, int log_group) {
   const Group g = my_group(log_group);
   if (g.token >= tokens) return;
   const int64_t all = tokens * k;
   const int* pos = position + g.token * k;
-  const int64_t kept = kept_rows(offsets, experts, all);
-  for (int c = g.t; c < vecs; c += g.size) {
-    const Pack<T, V> v = *reinterpret_cast<const Pack<T, V>*>(x + g.token * x_stride + c * V);
-    for (int j = 0; j < k; ++j) {
+  const T* src = x + g.token * x_stride;
+  const int step = g.size * kVec<T>;
+  if constexpr (kAligned) {
+    for (int e = g.t * kVec<T>; e < width; e += 2 * step) {
+      const bool two = e + step < width;
+      const Pack<T, kVec<T>> v0 = load_vec<T, true>(src + e);
+      Pack<T, kVec<T>> v1 = v0;
+      if (two) v1 = load_vec<T, true>(src + e + step);
+      for (int j = 0; j < k; ++j) {
+        const int64_t p = pos[j];
+        if (p < 0 || p >= all) continue;
+        T* row = rows + p * rows_stride;
+        store_vec(row + e, v0);
+        if (two) store_vec(row + e + step, v1);
+      }
+    }
+  } else {
+    for (int j = 0; j < k; ++j) {  // every row has boundaries of its own
       const int64_t p = pos[j];
-      if (p >= 0 && p < all)
-        *reinterpret_cast<Pack<T, V>*>(rows + p * rows_stride + c * V) = v;
+      if (p < 0 || p >= all) continue;
+      T* row = rows + p * rows_stride;
+      const Span s = inner_span<T, false>(row, width);
+      for (int e = s.lo + g.t * kVec<T>; e < s.hi; e += step)
+        store_vec(row + e, load_vec<T, false>(src + e));
+      for_ends(s, width, g.t, g.size, [&](int e) { row[e] = src[e]; });
     }
   }
-  // the rows of the dropped assignments: each token clears its own k places
-  for (int64_t r = g.token * k < kept ? kept : g.token * k; r < (g.token + 1) * k; ++r)
-    for (int c = g.t; c < vecs; c += g.size) {
-      Pack<T, V> z;
-#pragma unroll
-      for (int i = 0; i < V; ++i) z.v[i] = from_f32<T>(0.f);
-      *reinterpret_cast<Pack<T, V>*>(rows + r * rows_stride + c * V) = z;
-    }
+  const int64_t kept = kept_rows(offsets, experts, all), mine = g.token * k;
+  clear_rows<T, kAligned>(g.t, g.size, width, mine < kept ? kept : mine, mine + k, rows,
+                          rows_stride);
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kMoveThreads)
-    combine_kernel(const T* __restrict__ y, int64_t tokens, int k, int vecs, int64_t y_stride,
+template <typename T, bool kAligned>
+__global__ void __launch_bounds__(kMoveThreads, sizeof(T) == 4 ? 6 : 5)
+    combine_kernel(const T* __restrict__ y, int64_t tokens, int k, int width, int64_t y_stride,
                    const int* __restrict__ position, const float* __restrict__ weights,
                    T* __restrict__ out, int64_t out_stride, int log_group) {
+  constexpr int kRows = 4;  // rows whose loads are in flight
   const Group g = my_group(log_group);
   if (g.token >= tokens) return;
   const int64_t all = tokens * k;
   const int* pos = position + g.token * k;
   const float* w = weights + g.token * k;
-  for (int c = g.t; c < vecs; c += g.size) {
-    float acc[V];
+  T* dst = out + g.token * out_stride;
+  const Span s = inner_span<T, kAligned>(dst, width);
+  for (int e = s.lo + g.t * kVec<T>; e < s.hi; e += g.size * kVec<T>) {
+    float acc[kVec<T>];
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = 0.f;
-    for (int j = 0; j < k; ++j) {
-      const int64_t p = pos[j];
-      if (p < 0 || p >= all) continue;
-      const float s = weights ? w[j] : 1.f;
-      const Pack<T, V> v = *reinterpret_cast<const Pack<T, V>*>(y + p * y_stride + c * V);
+    for (int i = 0; i < kVec<T>; ++i) acc[i] = 0.f;
+    for (int j0 = 0; j0 < k; j0 += kRows) {
+      Pack<T, kVec<T>> v[kRows];
+      float f[kRows];
+      bool on[kRows];
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = fmaf(s, to_f32(v.v[i]), acc[i]);
+      for (int u = 0; u < kRows; ++u) {
+        const int64_t p = j0 + u < k ? pos[j0 + u] : -1;
+        on[u] = p >= 0 && p < all;
+        if (on[u]) {
+          f[u] = weights ? w[j0 + u] : 1.f;
+          v[u] = load_vec<T, kAligned>(y + p * y_stride + e);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kRows; ++u)
+        if (on[u]) {
+          float r[kVec<T>];
+          to_floats<T>(v[u], r);
+#pragma unroll
+          for (int i = 0; i < kVec<T>; ++i) acc[i] = fmaf(f[u], r[i], acc[i]);
+        }
     }
-    Pack<T, V> o;
-#pragma unroll
-    for (int i = 0; i < V; ++i) o.v[i] = from_f32<T>(acc[i]);
-    *reinterpret_cast<Pack<T, V>*>(out + g.token * out_stride + c * V) = o;
+    store_vec(dst + e, from_floats<T>(acc));
   }
+  if constexpr (!kAligned)
+    for_ends(s, width, g.t, g.size, [&](int e) {
+      float acc = 0.f;
+      for (int j = 0; j < k; ++j) {
+        const int64_t p = pos[j];
+        if (p >= 0 && p < all) acc = fmaf(weights ? w[j] : 1.f, to_f32(y[p * y_stride + e]), acc);
+      }
+      dst[e] = from_f32<T>(acc);
+    });
 }
 
-// One warp a token: the dot products are sums over the warp's lanes.
-template <typename T, int V>
-__global__ void __launch_bounds__(kMoveThreads)
-    combine_backward_kernel(const T* __restrict__ grad_out, const T* __restrict__ y,
-                            int64_t tokens, int k, int vecs, int64_t go_stride, int64_t y_stride,
-                            const int* __restrict__ offsets, int experts,
-                            const int* __restrict__ position, const float* __restrict__ weights,
-                            T* __restrict__ grad_y, int64_t gy_stride,
-                            float* __restrict__ grad_weights) {
-  const Group g = my_group(5);
-  if (g.token >= tokens) return;
-  const int64_t all = tokens * k;
-  const int* pos = position + g.token * k;
+// Sum over a group of `size` lanes; the whole warp calls it.
+__device__ __forceinline__ float group_sum(float v, int size) {
+  for (int o = size >> 1; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+
+// The gradients of combine, a group (a warp, or a part of one for narrow rows) a token: grad_out's row is read once for four
+// of the token's rows, whose loads are in flight together.  65536 tokens x 4 rows of
+// 2048 bf16: see by_assignment for what it measured against the other form.
+template <typename T>
+__global__ void __launch_bounds__(kMoveThreads, 4)
+    combine_backward_by_token(const T* __restrict__ grad_out, const T* __restrict__ y,
+                              int64_t tokens, int k, int width, int64_t go_stride,
+                              int64_t y_stride, const int* __restrict__ offsets, int experts,
+                              const int* __restrict__ position,
+                              const float* __restrict__ weights, T* __restrict__ grad_y,
+                              int64_t gy_stride, float* __restrict__ grad_weights,
+                              int log_group) {
+  constexpr int kRows = 4;
+  const Group g = my_group(log_group);
+  const bool live = g.token < tokens;  // the others take part in the sums
+  const int64_t all = tokens * k, mine = g.token * k;
   const T* go = grad_out + g.token * go_stride;
-  for (int j = 0; j < k; ++j) {
-    const int64_t p = pos[j];
-    const bool on = p >= 0 && p < all;
-    float dot = 0.f;
-    if (on) {
-      const float s = weights ? weights[g.token * k + j] : 1.f;
-      for (int c = g.t; c < vecs; c += 32) {
-        const Pack<T, V> d = *reinterpret_cast<const Pack<T, V>*>(go + c * V);
-        if (grad_weights) {
-          const Pack<T, V> v = *reinterpret_cast<const Pack<T, V>*>(y + p * y_stride + c * V);
+  for (int j0 = 0; j0 < k; j0 += kRows) {
+    int64_t p[kRows];
+    float f[kRows], dot[kRows];
 #pragma unroll
-          for (int i = 0; i < V; ++i) dot = fmaf(to_f32(d.v[i]), to_f32(v.v[i]), dot);
-        }
-        if (grad_y) {
-          Pack<T, V> o;
+    for (int u = 0; u < kRows; ++u) {
+      p[u] = live && j0 + u < k ? position[mine + j0 + u] : -1;
+      if (p[u] >= all) p[u] = -1;
+      f[u] = p[u] >= 0 && weights ? weights[mine + j0 + u] : 1.f;
+      dot[u] = 0.f;
+    }
+    for (int e = g.t * kVec<T>; live && e < width; e += g.size * kVec<T>) {
+      const Pack<T, kVec<T>> gv = load_vec<T, true>(go + e);
+      Pack<T, kVec<T>> v[kRows];
+      if (grad_weights) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) o.v[i] = from_f32<T>(s * to_f32(d.v[i]));
-          *reinterpret_cast<Pack<T, V>*>(grad_y + p * gy_stride + c * V) = o;
-        }
+        for (int u = 0; u < kRows; ++u)
+          if (p[u] >= 0) v[u] = load_vec<T, true>(y + p[u] * y_stride + e);
+      }
+      float d[kVec<T>];
+      to_floats<T>(gv, d);
+      if (grad_weights) {
+#pragma unroll
+        for (int u = 0; u < kRows; ++u)
+          if (p[u] >= 0) {
+            float r[kVec<T>];
+            to_floats<T>(v[u], r);
+#pragma unroll
+            for (int i = 0; i < kVec<T>; ++i) dot[u] = fmaf(d[i], r[i], dot[u]);
+          }
+      }
+      if (grad_y) {
+#pragma unroll
+        for (int u = 0; u < kRows; ++u)
+          if (p[u] >= 0) {
+            float r[kVec<T>];
+#pragma unroll
+            for (int i = 0; i < kVec<T>; ++i) r[i] = f[u] * d[i];
+            store_vec(grad_y + p[u] * gy_stride + e, from_floats<T>(r));
+          }
       }
     }
     if (grad_weights) {
 #pragma unroll
-      for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(kAll, dot, o);
-      if (g.t == 0) grad_weights[g.token * k + j] = dot;
+      for (int u = 0; u < kRows; ++u) {
+        const float sum = group_sum(dot[u], g.size);
+        if (live && g.t == 0 && j0 + u < k) grad_weights[mine + j0 + u] = sum;
+      }
     }
   }
-  if (!grad_y) return;
+  if (!grad_y || !live) return;
   const int64_t kept = kept_rows(offsets, experts, all);
-  for (int64_t r = g.token * k < kept ? kept : g.token * k; r < (g.token + 1) * k; ++r)
-    for (int c = g.t; c < vecs; c += 32) {
-      Pack<T, V> z;
+  clear_rows<T, true>(g.t, g.size, width, mine < kept ? kept : mine, mine + k, grad_y, gy_stride);
+}
+
+// The same, a group an assignment: for rows that share no boundaries, and for tokens
+// too few to fill the GPU.
+template <typename T, bool kAligned>
+__global__ void __launch_bounds__(kMoveThreads)
+    combine_backward_by_assignment(const T* __restrict__ grad_out, const T* __restrict__ y,
+                                   int64_t tokens, int k, int width, int64_t go_stride,
+                                   int64_t y_stride, const int* __restrict__ offsets, int experts,
+                                   const int* __restrict__ position,
+                                   const float* __restrict__ weights, T* __restrict__ grad_y,
+                                   int64_t gy_stride, float* __restrict__ grad_weights,
+                                   int log_group) {
+  const Group g = my_group(log_group);
+  const int64_t a = g.token, all = tokens * k;  // a group is an assignment here
+  const bool live = a < all;  // the others take part in the sums
+  const int64_t p = live ? position[a] : -1;
+  const bool on = p >= 0 && p < all;
+  float dot = 0.f;
+  if (on) {
+    const float f = weights ? weights[a] : 1.f;
+    const T* go = grad_out + a / k * go_stride;
+    const T* yr = y + p * y_stride;
+    T* gy = grad_y + p * gy_stride;
+    const Span s = inner_span<T, kAligned>(grad_y ? gy : yr, width);
+#pragma unroll 2
+    for (int e = s.lo + g.t * kVec<T>; e < s.hi; e += g.size * kVec<T>) {
+      const Pack<T, kVec<T>> gv = load_vec<T, kAligned>(go + e);
+      float d[kVec<T>], r[kVec<T>];
+      if (grad_weights) {
+        const Pack<T, kVec<T>> yv = load_vec<T, kAligned>(yr + e);
+        to_floats<T>(gv, d);
+        to_floats<T>(yv, r);
 #pragma unroll
-      for (int i = 0; i < V; ++i) z.v[i] = from_f32<T>(0.f);
-      *reinterpret_cast<Pack<T, V>*>(grad_y + r * gy_stride + c * V) = z;
+        for (int i = 0; i < kVec<T>; ++i) dot = fmaf(d[i], r[i], dot);
+      } else {
+        to_floats<T>(gv, d);
+      }
+      if (grad_y) {
+#pragma unroll
+        for (int i = 0; i < kVec<T>; ++i) r[i] = f * d[i];
+        store_vec(gy + e, from_floats<T>(r));
+      }
     }
+    if constexpr (!kAligned)
+      for_ends(s, width, g.t, g.size, [&](int e) {
+        const float d = to_f32(go[e]);
+        if (grad_weights) dot = fmaf(d, to_f32(yr[e]), dot);
+        if (grad_y) gy[e] = from_f32<T>(f * d);
+      });
+  }
+  if (grad_weights) {
+    dot = group_sum(dot, g.size);
+    if (live && g.t == 0) grad_weights[a] = dot;
+  }
+  if (grad_y && live && a >= kept_rows(offsets, experts, all))
+    clear_rows<T, kAligned>(g.t, g.size, width, a, a + 1, grad_y, gy_stride);
 }
 
 // -------------------------------------------------------------- host checks
@@ -228,7 +430,7 @@ __global__ void __launch_bounds__(kMoveThreads)
 tbe_status check_rows(int32_t dtype, int64_t tokens, int32_t k, int64_t width) {
   if (tokens < 0 || k < 1 || width < 0) return TBE_EINVAL;
   if (!dtype_bytes(dtype)) return TBE_EUNSUPPORTED;
-  if (tokens > INT32_MAX / k || width > INT32_MAX) return TBE_EUNSUPPORTED;
+  if (tokens > INT32_MAX / k || width > INT32_MAX / 2) return TBE_EUNSUPPORTED;
   return TBE_OK;
 }
 
@@ -246,9 +448,15 @@ bool vector_rows(const void* p, int bytes, int64_t stride, int64_t width) {
   return aligned_to(p, 16) && stride * bytes % 16 == 0 && width * bytes % 16 == 0;
 }
 
-int log_group_of(int64_t vecs) {
+// Threads of a group: one for each 16-byte place of a row of `width` elements
+// (and one more where rows do not begin on boundaries) while the tokens are few
+// and latency counts; a quarter of that, at least a warp, once they fill the GPU,
+// so that a thread has several loads in flight.
+int log_group_of(int64_t tokens, int64_t width, int bytes, bool aligned) {
+  int64_t places = (width * bytes + 15) / 16 + (aligned ? 0 : 1);
+  if (tokens * places > 152 * 2048 && places > 128) places = (places + 3) / 4;
   int lg = 0;
-  while (lg < 8 && (1 << lg) < vecs) ++lg;
+  while (lg < 8 && (1 << lg) < places) ++lg;
   return lg;
 }
 
@@ -262,16 +470,14 @@ tbe_status launched() {
   return cudaGetLastError() == cudaSuccess ? TBE_OK : TBE_ECUDA;
 }
 
-// Calls f with a value of the row type and the vector length as a constant.
-template <int V>
-struct VecTag {
-  static constexpr int v = V;
-};
+// Calls f with a value of the row type and whether rows are aligned, as a constant.
 template <typename F>
-tbe_status for_dtype(int32_t dtype, bool vec, F f) {
-  if (dtype == TBE_DT_F32) return vec ? f(float{}, VecTag<4>{}) : f(float{}, VecTag<1>{});
-  if (dtype == TBE_DT_F16) return vec ? f(__half{}, VecTag<8>{}) : f(__half{}, VecTag<1>{});
-  return vec ? f(__nv_bfloat16{}, VecTag<8>{}) : f(__nv_bfloat16{}, VecTag<1>{});
+tbe_status for_dtype(int32_t dtype, bool aligned, F f) {
+  using Yes = std::true_type;
+  using No = std::false_type;
+  if (dtype == TBE_DT_F32) return aligned ? f(float{}, Yes{}) : f(float{}, No{});
+  if (dtype == TBE_DT_F16) return aligned ? f(__half{}, Yes{}) : f(__half{}, No{});
+  return aligned ? f(__nv_bfloat16{}, Yes{}) : f(__nv_bfloat16{}, No{});
 }
 
 }  // namespace
@@ -291,12 +497,29 @@ extern "C" tbe_status tbe_expert_sort(const void* ids, int32_t index_dtype, int6
     return TBE_EINVAL;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int n = static_cast<int>(tokens * k);
-  const size_t smem = static_cast<size_t>(kSortWarps) * (experts + 1) * 4;
+  const size_t smem = static_cast<size_t>(kSortWarps + 1) * (experts + 1) * 4;
+  int ctas = 1;
+  while (ctas < kSortMostCtas && n > ctas * kSortPerCta) ctas *= 2;
   const auto go = [&](auto* p, auto kernel) {
+    // clusters above eight CTAs have to be asked for
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSortWarps * (TBE_MAX_EXPERTS + 1) * 4) != cudaSuccess)
+                             (kSortWarps + 1) * (TBE_MAX_EXPERTS + 1) * 4) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+            cudaSuccess)
       return TBE_ECUDA;
-    kernel<<<1, kSortWarps * 32, smem, s>>>(p, n, experts, offsets, source, position);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kSortWarps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctas > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kernel, p, n, experts, offsets, source, position) != cudaSuccess)
+      return TBE_ECUDA;
     return launched();
   };
   return index_dtype == TBE_DT_I32
@@ -318,11 +541,11 @@ extern "C" tbe_status tbe_expert_dispatch(const void* x, int32_t dtype, int64_t 
   const bool vec = vector_rows(x, b, x_stride, width) && vector_rows(rows, b, rows_stride, width);
   return for_dtype(dtype, vec, [&](auto t, auto v) {
     using T = decltype(t);
-    constexpr int V = decltype(v)::v;
-    const int vecs = static_cast<int>(width / V), lg = log_group_of(vecs);
-    dispatch_kernel<T, V><<<static_cast<unsigned>(group_blocks(tokens, lg)), kMoveThreads, 0,
+    constexpr bool kAligned = decltype(v)::value;
+    const int lg = log_group_of(tokens, width, b, kAligned);
+    dispatch_kernel<T, kAligned><<<static_cast<unsigned>(group_blocks(tokens, lg)), kMoveThreads, 0,
                             static_cast<cudaStream_t>(stream)>>>(
-        static_cast<const T*>(x), tokens, k, vecs, x_stride, offsets, experts, position,
+        static_cast<const T*>(x), tokens, k, static_cast<int>(width), x_stride, offsets, experts, position,
         static_cast<T*>(rows), rows_stride, lg);
     return launched();
   });
@@ -342,11 +565,11 @@ extern "C" tbe_status tbe_expert_combine(const void* y, int32_t dtype, int64_t t
   const bool vec = vector_rows(y, b, y_stride, width) && vector_rows(out, b, out_stride, width);
   return for_dtype(dtype, vec, [&](auto t, auto v) {
     using T = decltype(t);
-    constexpr int V = decltype(v)::v;
-    const int vecs = static_cast<int>(width / V), lg = log_group_of(vecs);
-    combine_kernel<T, V><<<static_cast<unsigned>(group_blocks(tokens, lg)), kMoveThreads, 0,
+    constexpr bool kAligned = decltype(v)::value;
+    const int lg = log_group_of(tokens, width, b, kAligned);
+    combine_kernel<T, kAligned><<<static_cast<unsigned>(group_blocks(tokens, lg)), kMoveThreads, 0,
                            static_cast<cudaStream_t>(stream)>>>(
-        static_cast<const T*>(y), tokens, k, vecs, y_stride, position, weights,
+        static_cast<const T*>(y), tokens, k, static_cast<int>(width), y_stride, position, weights,
         static_cast<T*>(out), out_stride, lg);
     return launched();
   });
@@ -373,12 +596,19 @@ extern "C" tbe_status tbe_expert_combine_backward(
                    (!grad_y || vector_rows(grad_y, b, grad_y_stride, width));
   return for_dtype(dtype, vec, [&](auto t, auto v) {
     using T = decltype(t);
-    constexpr int V = decltype(v)::v;
-    combine_backward_kernel<T, V><<<static_cast<unsigned>(group_blocks(tokens, 5)), kMoveThreads,
-                                    0, static_cast<cudaStream_t>(stream)>>>(
+    constexpr bool kAligned = decltype(v)::value;
+    // a group a token, if that fills the GPU (24 warps a multiprocessor)
+    const bool by_token = kAligned && tokens * ((width * b + 511) / 512) >= 152 * 24;
+    const auto kernel = by_token ? combine_backward_by_token<T>
+                                 : combine_backward_by_assignment<T, kAligned>;
+    const int64_t groups = by_token ? tokens : tokens * k;
+    int lg = log_group_of(groups, width, b, kAligned);
+    if (lg > 5) lg = 5;
+    kernel<<<static_cast<unsigned>(group_blocks(groups, lg)), kMoveThreads, 0,
+             static_cast<cudaStream_t>(stream)>>>(
         static_cast<const T*>(grad_out), static_cast<const T*>(y), tokens, k,
-        static_cast<int>(width / V), grad_out_stride, y_stride, offsets, experts, position,
-        weights, static_cast<T*>(grad_y), grad_y_stride, grad_weights);
+        static_cast<int>(width), grad_out_stride, y_stride, offsets, experts, position, weights,
+        static_cast<T*>(grad_y), grad_y_stride, grad_weights, lg);
     return launched();
   });
 }

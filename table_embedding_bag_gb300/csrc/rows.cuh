@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "tbe.h"
 
@@ -40,6 +41,105 @@ template <typename T, int V>
 struct alignas(V * sizeof(T)) Pack {
   T v[V];
 };
+
+template <typename T>
+constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+
+// A vector's values in fp32, and the rounding back.
+template <typename T>
+__device__ __forceinline__ void to_floats(const Pack<T, kVec<T>>& v, float (&f)[kVec<T>]) {
+  const uint4 q = *reinterpret_cast<const uint4*>(&v);
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      f[i] = __uint_as_float(w[i]);
+    } else if constexpr (std::is_same_v<T, __half>) {
+      const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = h.x;
+      f[2 * i + 1] = h.y;
+    } else {  // a bf16 is the upper half of an fp32
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ Pack<T, kVec<T>> from_floats(const float (&f)[kVec<T>]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      w[i] = __float_as_uint(f[i]);
+    } else if constexpr (std::is_same_v<T, __half>) {
+      const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  const uint4 q = make_uint4(w[0], w[1], w[2], w[3]);
+  return *reinterpret_cast<const Pack<T, kVec<T>>*>(&q);
+}
+
+// Elements of T between the 16-byte boundary at or before p and p.
+template <typename T>
+__device__ __forceinline__ int lead(const void* p) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+}
+
+// The elements [lo, hi) of a row of `width` that are moved in 16-byte vectors, on
+// the 16-byte boundaries of the row `to` that is written; the others, a few at both
+// ends, are moved one by one.  kAligned: every row begins on a boundary and ends
+// with a whole vector.  Otherwise the inner part leaves out so much that the
+// aligned vectors around it lie within the row of any other alignment too.
+struct Span {
+  int lo, hi;
+};
+template <typename T, bool kAligned>
+__device__ __forceinline__ Span inner_span(const T* to, int width) {
+  if constexpr (kAligned) return {0, width};
+  const int lo = 2 * kVec<T> - lead<T>(to);
+  if (lo + 2 * kVec<T> > width) return {width, width};
+  return {lo, lo + ((width - 2 * kVec<T> - lo) / kVec<T> + 1) * kVec<T>};
+}
+
+// The vector at p, cut out of the two aligned vectors it lies in.
+template <typename T, bool kAligned>
+__device__ __forceinline__ Pack<T, kVec<T>> load_vec(const T* __restrict__ p) {
+  if constexpr (kAligned) {
+    return *reinterpret_cast<const Pack<T, kVec<T>>*>(p);
+  } else {
+    const int shift = lead<T>(p), bytes = shift * static_cast<int>(sizeof(T));
+    const uint4* q = reinterpret_cast<const uint4*>(p - shift);
+    const uint4 a = q[0], b = q[shift ? 1 : 0];
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = bytes & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = bytes & 4 ? w[i + 1] : w[i];
+    const int bits = (bytes & 3) * 8;
+    uint4 o;
+    o.x = __funnelshift_r(w[0], w[1], bits);
+    o.y = __funnelshift_r(w[1], w[2], bits);
+    o.z = __funnelshift_r(w[2], w[3], bits);
+    o.w = __funnelshift_r(w[3], w[4], bits);
+    return *reinterpret_cast<const Pack<T, kVec<T>>*>(&o);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store_vec(T* p, const Pack<T, kVec<T>>& v) {
+  *reinterpret_cast<Pack<T, kVec<T>>*>(p) = v;
+}
+
+// Calls f(e) for this thread's share of the elements outside the span.
+template <typename F>
+__device__ __forceinline__ void for_ends(Span s, int width, int t, int threads, F f) {
+  const int ends = s.lo + width - s.hi;
+  for (int i = t; i < ends; i += threads) f(i < s.lo ? i : s.hi + i - s.lo);
+}
 
 inline int dtype_bytes(int32_t dtype) {
   return dtype == TBE_DT_F32 ? 4 : dtype == TBE_DT_F16 || dtype == TBE_DT_BF16 ? 2 : 0;

@@ -11,8 +11,6 @@ import ctypes
 
 import torch
 
-from . import _build  # noqa: F401  (the library's place)
-
 __all__ = [
     "tbe_expert_sort", "tbe_expert_dispatch", "tbe_expert_dispatch_fp8", "tbe_expert_combine",
     "tbe_expert_combine_backward", "tbe_expert_dispatch_backward", "tbe_quantize_rows",
@@ -40,9 +38,15 @@ def configure(lib):
     lib.tbe_quantize_weights.restype = ctypes.c_int
 
 
+_lib_ = None
+
+
 def _lib():
-    import table_embedding_bag_gb300 as tbe
-    return tbe._load()
+    global _lib_
+    if _lib_ is None:
+        import table_embedding_bag_gb300 as tbe
+        _lib_ = tbe._load()
+    return _lib_
 
 
 def _ok(call, code):
@@ -51,63 +55,69 @@ def _ok(call, code):
         raise tbe.TBEError(call, code)
 
 
-class _On:
-    """The stream a call runs on: allocations made inside belong to it."""
+# The calls below take microseconds on the GPU, so their checks are written to
+# take few on the host: no torch.cuda.current_stream() object (2.8 us), no check
+# of what was just allocated.
+def _stream_of(stream, t):
+    """The cudaStream_t a call on t's device runs on."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return stream.cuda_stream
 
-    def __init__(self, stream):
-        self.stream = torch.cuda.current_stream() if stream is None else stream
-        self.ptr = self.stream.cuda_stream
-        self.ctx = None if stream is None else torch.cuda.stream(stream)
 
-    def empty(self, shape, dtype, like):
-        if self.ctx is None:
-            return torch.empty(shape, dtype=dtype, device=like.device)
-        with self.ctx:
-            return torch.empty(shape, dtype=dtype, device=like.device)
+def _empty(stream, shape, dtype, like):
+    """An output that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _matrix(t, name, dtypes, cols=None, rows=None):
     """A 2-d CUDA tensor with contiguous columns; returns its row stride."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions")
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor with two dimensions")
     r, c = t.shape
-    if cols is not None and c != cols:
-        raise ValueError(f"{name} must have {cols} columns")
-    if rows is not None and r != rows:
-        raise ValueError(f"{name} must have {rows} rows")
+    if (cols is not None and c != cols) or (rows is not None and r != rows):
+        raise ValueError(f"{name} must have the shape [{rows if rows is not None else '*'}, "
+                         f"{cols if cols is not None else '*'}]")
+    if t.is_contiguous():
+        return c
     s0, s1 = t.stride()
     if c > 1 and s1 != 1:
         raise ValueError(f"{name} must have contiguous columns")
     if r <= 1:
-        return max(c, 1)
+        return c
     if s0 < c:
         raise ValueError(f"{name} must not have overlapping rows")
-    return max(s0, 1)
+    return s0
 
 
 def _dense(t, name, dtype, shape):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if not t.is_cuda or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name} must be a contiguous CUDA tensor of shape {tuple(shape)}")
 
 
-def _plan(offsets, position):
-    if offsets.dim() != 1 or offsets.numel() < 2:
-        raise ValueError("offsets must have num_experts + 1 entries")
-    _dense(offsets, "offsets", torch.int32, offsets.shape)
-    return _positions(position)
-
-
 def _positions(position):
-    if position.dim() != 2 or position.shape[1] < 1:
-        raise ValueError("position must have the shape [tokens, k], k >= 1")
-    _dense(position, "position", torch.int32, position.shape)
-    return position.shape
+    if position.dtype != torch.int32:
+        raise TypeError("position must be torch.int32")
+    shape = position.shape
+    if len(shape) != 2 or shape[1] < 1 or not position.is_contiguous() or not position.is_cuda:
+        raise ValueError("position must be a contiguous CUDA tensor [tokens, k], k >= 1")
+    return shape
+
+
+def _experts(offsets):
+    if offsets.dtype != torch.int32:
+        raise TypeError("offsets must be torch.int32")
+    n = offsets.numel() - 1
+    if n < 1 or offsets.dim() != 1 or not offsets.is_contiguous() or not offsets.is_cuda:
+        raise ValueError("offsets must be a contiguous CUDA tensor [num_experts + 1]")
+    return n
 
 
 def tbe_expert_sort(ids, num_experts, offsets=None, source=None, position=None, stream=None):
@@ -122,50 +132,51 @@ def tbe_expert_sort(ids, num_experts, offsets=None, source=None, position=None, 
     _dense(ids, "ids", ids.dtype, ids.shape)
     if not 1 <= num_experts <= TBE_MAX_EXPERTS:
         raise ValueError(f"num_experts must lie in [1, {TBE_MAX_EXPERTS}]")
-    on = _On(stream)
     tokens, k = ids.shape
     if offsets is None:
-        offsets = on.empty(num_experts + 1, torch.int32, ids)
+        offsets = _empty(stream, num_experts + 1, torch.int32, ids)
     else:
         _dense(offsets, "offsets", torch.int32, (num_experts + 1,))
     if source is None:
-        source = on.empty(tokens * k, torch.int32, ids)
+        source = _empty(stream, tokens * k, torch.int32, ids)
     else:
         _dense(source, "source", torch.int32, (tokens * k,))
     if position is None:
-        position = on.empty((tokens, k), torch.int32, ids)
+        position = _empty(stream, (tokens, k), torch.int32, ids)
     else:
         _dense(position, "position", torch.int32, (tokens, k))
     _ok("tbe_expert_sort", _lib().tbe_expert_sort(
         ids.data_ptr(), _ID_DT[ids.dtype], tokens, k, num_experts, offsets.data_ptr(),
-        source.data_ptr(), position.data_ptr(), on.ptr))
+        source.data_ptr(), position.data_ptr(), _stream_of(stream, ids)))
     return offsets, source, position
 
 
 def tbe_expert_dispatch(x, offsets, position, out=None, stream=None):
     """rows [tokens * k, width]: x's rows at their sorted places, zeros after the
     last kept one."""
-    tokens, k = _plan(offsets, position)
+    experts = _experts(offsets)
+    tokens, k = _positions(position)
     xs = _matrix(x, "x", _ROW_DT, rows=tokens)
-    on = _On(stream)
-    width = x.shape[1]
+    width = os_ = x.shape[1]
     if out is None:
-        out = on.empty((tokens * k, width), x.dtype, x)
-    os_ = _matrix(out, "out", (x.dtype,), width, tokens * k)
+        out = _empty(stream, (tokens * k, width), x.dtype, x)
+    else:
+        os_ = _matrix(out, "out", (x.dtype,), width, tokens * k)
     _ok("tbe_expert_dispatch", _lib().tbe_expert_dispatch(
-        x.data_ptr(), _ROW_DT[x.dtype], tokens, k, width, xs, offsets.data_ptr(),
-        offsets.numel() - 1, position.data_ptr(), out.data_ptr(), os_, on.ptr))
+        x.data_ptr(), _ROW_DT[x.dtype], tokens, k, width, xs, offsets.data_ptr(), experts,
+        position.data_ptr(), out.data_ptr(), os_, _stream_of(stream, x)))
     return out
 
 
-def _fp8_out(on, x, rows, out, scale):
-    width = x.shape[1]
+def _fp8_out(stream, x, rows, out, scale):
+    width = qs = x.shape[1]
     blocks = -(-width // TBE_SCALE_BLOCK)
     if out is None:
-        out = on.empty((rows, width), torch.float8_e4m3fn, x)
-    qs = _matrix(out, "out", (torch.float8_e4m3fn,), width, rows)
+        out = _empty(stream, (rows, width), torch.float8_e4m3fn, x)
+    else:
+        qs = _matrix(out, "out", (torch.float8_e4m3fn,), width, rows)
     if scale is None:
-        scale = on.empty((rows, blocks), torch.float32, x)
+        scale = _empty(stream, (rows, blocks), torch.float32, x)
     else:
         _dense(scale, "scale", torch.float32, (rows, blocks))
     return out, qs, scale
@@ -174,24 +185,23 @@ def _fp8_out(on, x, rows, out, scale):
 def tbe_expert_dispatch_fp8(x, offsets, position, out=None, scale=None, stream=None):
     """The dispatch with the rows quantised to e4m3 on the way: (q [tokens * k,
     width], scale [tokens * k, ceil(width / 128)])."""
-    tokens, k = _plan(offsets, position)
+    experts = _experts(offsets)
+    tokens, k = _positions(position)
     xs = _matrix(x, "x", _ROW_DT, rows=tokens)
-    on = _On(stream)
-    out, qs, scale = _fp8_out(on, x, tokens * k, out, scale)
+    out, qs, scale = _fp8_out(stream, x, tokens * k, out, scale)
     _ok("tbe_expert_dispatch_fp8", _lib().tbe_expert_dispatch_fp8(
-        x.data_ptr(), _ROW_DT[x.dtype], tokens, k, x.shape[1], xs, offsets.data_ptr(),
-        offsets.numel() - 1, position.data_ptr(), out.data_ptr(), qs, scale.data_ptr(), on.ptr))
+        x.data_ptr(), _ROW_DT[x.dtype], tokens, k, x.shape[1], xs, offsets.data_ptr(), experts,
+        position.data_ptr(), out.data_ptr(), qs, scale.data_ptr(), _stream_of(stream, x)))
     return out, scale
 
 
 def tbe_quantize_rows(x, out=None, scale=None, stream=None):
     """Rows to e4m3 with an fp32 scale for each 128 columns: (q, scale)."""
     xs = _matrix(x, "x", _ROW_DT)
-    on = _On(stream)
-    out, qs, scale = _fp8_out(on, x, x.shape[0], out, scale)
+    out, qs, scale = _fp8_out(stream, x, x.shape[0], out, scale)
     _ok("tbe_quantize_rows", _lib().tbe_expert_dispatch_fp8(
         x.data_ptr(), _ROW_DT[x.dtype], x.shape[0], 1, x.shape[1], xs, None, 0, None,
-        out.data_ptr(), qs, scale.data_ptr(), on.ptr))
+        out.data_ptr(), qs, scale.data_ptr(), _stream_of(stream, x)))
     return out, scale
 
 
@@ -203,19 +213,19 @@ def tbe_quantize_weights(w, out=None, scale=None, stream=None):
     if w.dim() != 3:
         raise ValueError("w must have the shape [experts, n, k]")
     _dense(w, "w", w.dtype, w.shape)
-    on = _On(stream)
     e, n, k = w.shape
     grid = (e, -(-n // TBE_SCALE_BLOCK), -(-k // TBE_SCALE_BLOCK))
     if out is None:
-        out = on.empty((e, n, k), torch.float8_e4m3fn, w)
+        out = _empty(stream, (e, n, k), torch.float8_e4m3fn, w)
     else:
         _dense(out, "out", torch.float8_e4m3fn, (e, n, k))
     if scale is None:
-        scale = on.empty(grid, torch.float32, w)
+        scale = _empty(stream, grid, torch.float32, w)
     else:
         _dense(scale, "scale", torch.float32, grid)
     _ok("tbe_quantize_weights", _lib().tbe_quantize_weights(
-        w.data_ptr(), _ROW_DT[w.dtype], e, n, k, out.data_ptr(), scale.data_ptr(), on.ptr))
+        w.data_ptr(), _ROW_DT[w.dtype], e, n, k, out.data_ptr(), scale.data_ptr(),
+        _stream_of(stream, w)))
     return out, scale
 
 
@@ -224,16 +234,17 @@ def tbe_expert_combine(y, position, weights=None, out=None, stream=None):
     weights [tokens, k], or None for ones) and summed per token."""
     tokens, k = _positions(position)
     ys = _matrix(y, "y", _ROW_DT, rows=tokens * k)
-    on = _On(stream)
-    width = y.shape[1]
+    width = os_ = y.shape[1]
     if weights is not None:
         _dense(weights, "weights", torch.float32, (tokens, k))
     if out is None:
-        out = on.empty((tokens, width), y.dtype, y)
-    os_ = _matrix(out, "out", (y.dtype,), width, tokens)
+        out = _empty(stream, (tokens, width), y.dtype, y)
+    else:
+        os_ = _matrix(out, "out", (y.dtype,), width, tokens)
     _ok("tbe_expert_combine", _lib().tbe_expert_combine(
         y.data_ptr(), _ROW_DT[y.dtype], tokens, k, width, ys, position.data_ptr(),
-        None if weights is None else weights.data_ptr(), out.data_ptr(), os_, on.ptr))
+        None if weights is None else weights.data_ptr(), out.data_ptr(), os_,
+        _stream_of(stream, y)))
     return out
 
 
@@ -246,25 +257,26 @@ def tbe_expert_combine_backward(grad_out, y, offsets, position, weights=None, gr
                                 grad_weights=None, stream=None):
     """Gradients of tbe_expert_combine: (grad_y [tokens * k, width], grad_weights
     [tokens, k] fp32)."""
-    tokens, k = _plan(offsets, position)
+    experts = _experts(offsets)
+    tokens, k = _positions(position)
     gs = _matrix(grad_out, "grad_out", _ROW_DT, rows=tokens)
-    width = grad_out.shape[1]
+    width = gys = grad_out.shape[1]
     ys = _matrix(y, "y", (grad_out.dtype,), width, tokens * k)
-    on = _On(stream)
     if weights is not None:
         _dense(weights, "weights", torch.float32, (tokens, k))
     if grad_y is None:
-        grad_y = on.empty((tokens * k, width), grad_out.dtype, grad_out)
-    gys = _matrix(grad_y, "grad_y", (grad_out.dtype,), width, tokens * k)
+        grad_y = _empty(stream, (tokens * k, width), grad_out.dtype, grad_out)
+    else:
+        gys = _matrix(grad_y, "grad_y", (grad_out.dtype,), width, tokens * k)
     if grad_weights is None:
-        grad_weights = on.empty((tokens, k), torch.float32, grad_out)
+        grad_weights = _empty(stream, (tokens, k), torch.float32, grad_out)
     else:
         _dense(grad_weights, "grad_weights", torch.float32, (tokens, k))
     _ok("tbe_expert_combine_backward", _lib().tbe_expert_combine_backward(
         grad_out.data_ptr(), y.data_ptr(), _ROW_DT[grad_out.dtype], tokens, k, width, gs, ys,
-        offsets.data_ptr(), offsets.numel() - 1, position.data_ptr(),
+        offsets.data_ptr(), experts, position.data_ptr(),
         None if weights is None else weights.data_ptr(), grad_y.data_ptr(), gys,
-        grad_weights.data_ptr(), on.ptr))
+        grad_weights.data_ptr(), _stream_of(stream, grad_out)))
     return grad_y, grad_weights
 
 
@@ -281,8 +293,8 @@ def tbe_expert_product(a, a_scale, w, w_scale, offsets=None, out=None, out_dtype
     rows, k = a.shape
     if w.dim() != 3 or w.shape[2] != k:
         raise ValueError(f"w must have the shape [experts, n, {k}]")
-    _dense(w, "w", fp8, w.shape)
-    e, n = w.shape[0], w.shape[1]
+    e, n, _ = shape = w.shape
+    _dense(w, "w", fp8, shape)
     kb = -(-k // TBE_SCALE_BLOCK)
     _dense(a_scale, "a_scale", torch.float32, (rows, kb))
     _dense(w_scale, "w_scale", torch.float32, (e, -(-n // TBE_SCALE_BLOCK), kb))
@@ -290,18 +302,19 @@ def tbe_expert_product(a, a_scale, w, w_scale, offsets=None, out=None, out_dtype
         _dense(offsets, "offsets", torch.int32, (e + 1,))
     elif e != 1:
         raise ValueError("offsets may be None with one expert only")
-    if status is not None:
-        _dense(status, "status", torch.int32, status.shape)
-        if not status.numel():
-            raise ValueError("status must have an entry")
-    on = _On(stream)
+    if status is not None and (status.dtype != torch.int32 or not status.is_cuda or
+                               status.numel() < 1):
+        raise ValueError("status must be an int32 CUDA tensor with an entry")
+    os_ = n
     if out is None:
         if out_dtype not in _ROW_DT:
             raise TypeError("out_dtype must be float16, bfloat16 or float32")
-        out = on.empty((rows, n), out_dtype, a)
-    os_ = _matrix(out, "out", _ROW_DT, n, rows)
+        out = _empty(stream, (rows, n), out_dtype, a)
+    else:
+        os_ = _matrix(out, "out", _ROW_DT, n, rows)
     _ok("tbe_expert_product", _lib().tbe_expert_product(
         a.data_ptr(), as_, a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
         None if offsets is None else offsets.data_ptr(), rows, n, k, e, out.data_ptr(),
-        _ROW_DT[out.dtype], os_, None if status is None else status.data_ptr(), on.ptr))
+        _ROW_DT[out.dtype], os_, None if status is None else status.data_ptr(),
+        _stream_of(stream, a)))
     return out
