@@ -21,8 +21,79 @@ __device__ __forceinline__ float block_scale(float amax) {
   return fmaxf(amax * kInvMax, kTinyScale);
 }
 
-__device__ __forceinline__ uint8_t to_e4m3(float v) {
-  return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ uint2 to_e4m3(const float (&v)[8], float f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * f, v[2 * i + 1] * f), __NV_SATFINITE,
+                                    __NV_E4M3);
+  return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+
+// e4m3(x / s) of eight values, as a division in fp32 gives it.  The quotient lies
+// between x times a little less and a little more than 1 / s (2^-21 of it is more than
+// the errors on the way add up to: 2^-23 of the approximate reciprocal and three
+// roundings of 2^-24), and rounding is monotonic, so
+// where both give the same e4m3 values the quotients do too.  Where they differ (one lane
+// in some thousands) the values are divided.
+__device__ __forceinline__ Pack<uint8_t, 8> quantized(const float (&x)[8], float s) {
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  uint2 q = to_e4m3(x, inv * (1.f - 0x1p-21f));
+  const uint2 more = to_e4m3(x, inv * (1.f + 0x1p-21f));
+  if (q.x != more.x || q.y != more.y) {
+    float d[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d[i] = __fdiv_rn(x[i], s);
+    q = to_e4m3(d, 1.f);
+  }
+  return *reinterpret_cast<const Pack<uint8_t, 8>*>(&q);
+}
+
+// Eight consecutive values of a row.
+template <typename T>
+struct Eight {
+  Pack<T, kVec<T>> v[8 / kVec<T>];
+  __device__ __forceinline__ void floats(float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8 / kVec<T>; ++i) {
+      float x[kVec<T>];
+      to_floats<T>(v[i], x);
+#pragma unroll
+      for (int u = 0; u < kVec<T>; ++u) f[i * kVec<T> + u] = x[u];
+    }
+  }
+};
+
+// Values col .. col + 7, zeros from `width` on.
+template <typename T, bool kAligned>
+__device__ __forceinline__ Eight<T> load8(const T* row, int col, int width) {
+  Eight<T> e;
+#pragma unroll
+  for (int i = 0; i < 8 / kVec<T>; ++i) {
+    if (kAligned && col < width) {
+      e.v[i] = *reinterpret_cast<const Pack<T, kVec<T>>*>(row + col + i * kVec<T>);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kVec<T>; ++u) {
+        const int c = col + i * kVec<T> + u;
+        e.v[i].v[u] = !kAligned && c < width ? row[c] : from_f32<T>(0.f);
+      }
+    }
+  }
+  return e;
+}
+
+template <bool kAligned>
+__device__ __forceinline__ void store8(uint8_t* row, int col, int width,
+                                       const Pack<uint8_t, 8>& e) {
+  if (kAligned) {
+    if (col < width) *reinterpret_cast<Pack<uint8_t, 8>*>(row + col) = e;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (col + i < width) row[col + i] = e.v[i];
+  }
 }
 
 // Sixteen lanes quantise a token's block of 128 columns, eight columns each; a
@@ -42,49 +113,45 @@ __global__ void __launch_bounds__(256)
   const int64_t all = tokens * k;
   const T* row = x + token * x_stride;
   const int* pos = position + token * k;
-  // gridDim.y warps share a token's pairs of blocks
-  for (int b0 = blockIdx.y * 2; b0 < blocks; b0 += gridDim.y * 2) {
+  // gridDim.y warps share a token's pairs of blocks; the next pair's values are on their way
+  // while one is quantised.  Four places' addresses are formed before the loop.
+  constexpr int kPlaces = 4;
+  uint8_t* q_to[kPlaces];
+  float* scale_to[kPlaces];
+#pragma unroll
+  for (int j = 0; j < kPlaces; ++j) {
+    const int64_t p = j < k ? (position ? pos[j] : token) : -1;
+    const bool on = p >= 0 && p < all;
+    q_to[j] = on ? q + p * q_stride : nullptr;
+    scale_to[j] = on ? scale + p * blocks : nullptr;
+  }
+  const int step = gridDim.y * 2;
+  Eight<T> next = load8<T, kAligned>(row, (blockIdx.y * 2 + half) * kBlock + col_in, width);
+  for (int b0 = blockIdx.y * 2; b0 < blocks; b0 += step) {
     const int b = b0 + half;
     const int col = b * kBlock + col_in;
-    T in[8];
+    float in[8];
+    next.floats(in);
+    if (b0 + step < blocks) next = load8<T, kAligned>(row, col + step * kBlock, width);
     float amax = 0.f;
-    if (kAligned) {
 #pragma unroll
-      for (int i = 0; i < 8; i += kVec<T>) {
-        Pack<T, kVec<T>> v;
-        if (col < width) {
-          v = *reinterpret_cast<const Pack<T, kVec<T>>*>(row + col + i);
-        } else {
-#pragma unroll
-          for (int u = 0; u < kVec<T>; ++u) v.v[u] = from_f32<T>(0.f);
-        }
-#pragma unroll
-        for (int u = 0; u < kVec<T>; ++u) in[i + u] = v.v[u];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) in[i] = col + i < width ? row[col + i] : from_f32<T>(0.f);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(to_f32(in[i])));  // passes over NaN
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(in[i]));  // passes over NaN
 #pragma unroll
     for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const float s = block_scale(amax);
-    Pack<uint8_t, 8> e;
+    const Pack<uint8_t, 8> e = quantized(in, s);
+    const bool mine = col < width, first = col_in == 0 && b < blocks;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e.v[i] = to_e4m3(__fdiv_rn(to_f32(in[i]), s));
-    for (int j = 0; j < k; ++j) {
-      const int64_t p = position ? pos[j] : token;
-      if (p < 0 || p >= all || b >= blocks) continue;
-      uint8_t* dst = q + p * q_stride + col;
-      if (kAligned) {
-        if (col < width) *reinterpret_cast<Pack<uint8_t, 8>*>(dst) = e;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (col + i < width) dst[i] = e.v[i];
+    for (int j = 0; j < kPlaces; ++j)
+      if (q_to[j]) {
+        if (mine) store8<kAligned>(q_to[j], col, width, e);
+        if (first) scale_to[j][b] = s;
       }
-      if (col_in == 0) scale[p * blocks + b] = s;
+    for (int j = kPlaces; j < k; ++j) {
+      const int64_t p = pos[j];
+      if (p < 0 || p >= all) continue;
+      if (mine) store8<kAligned>(q + p * q_stride, col, width, e);
+      if (first) scale[p * blocks + b] = s;
     }
   }
   if (!position) return;
@@ -103,22 +170,31 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// One CTA a 128 x 128 block of an expert's weights.
-template <typename T>
+// One CTA a 128 x 128 block of an expert's weights, read once: a thread holds eight
+// columns of eight rows, 16 rows apart.
+template <typename T, bool kAligned>
 __global__ void __launch_bounds__(256)
     quantize_weights_kernel(const T* __restrict__ w, int64_t n, int64_t k, int nb, int kb,
                             uint8_t* __restrict__ q, float* __restrict__ scale) {
   __shared__ float warp_max[8];
   const int64_t unit = blockIdx.x;
   const int64_t e = unit / (static_cast<int64_t>(nb) * kb);
-  const int64_t row0 = unit / kb % nb * kBlock, col0 = unit % kb * kBlock;
-  const T* src = w + e * n * k;
-  uint8_t* dst = q + e * n * k;
-  const int c = threadIdx.x & (kBlock - 1);
-  const bool in = col0 + c < k;
+  const int64_t row0 = unit / kb % nb * kBlock + threadIdx.x / 16;
+  const int col = static_cast<int>(unit % kb * kBlock) + threadIdx.x % 16 * 8;
+  const int cols = static_cast<int>(k);
+  const T* src = w + (e * n + row0) * k;
+  Eight<T> in[8];
   float amax = 0.f;
-  for (int r = threadIdx.x / kBlock; r < kBlock && row0 + r < n; r += 256 / kBlock)
-    if (in) amax = fmaxf(amax, fabsf(to_f32(src[(row0 + r) * k + col0 + c])));
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    in[i] = load8<T, kAligned>(src + i * 16 * k, col, row0 + i * 16 < n ? cols : 0);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float x[8];
+    in[i].floats(x);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) amax = fmaxf(amax, fabsf(x[u]));  // passes over NaN
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = amax;
@@ -126,10 +202,13 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int i = 0; i < 8; ++i) amax = fmaxf(amax, warp_max[i]);
   const float s = block_scale(amax);
-  for (int r = threadIdx.x / kBlock; r < kBlock && row0 + r < n; r += 256 / kBlock)
-    if (in)
-      dst[(row0 + r) * k + col0 + c] =
-          to_e4m3(__fdiv_rn(to_f32(src[(row0 + r) * k + col0 + c]), s));
+  uint8_t* dst = q + (e * n + row0) * k;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float x[8];
+    in[i].floats(x);
+    store8<kAligned>(dst + i * 16 * k, col, row0 + i * 16 < n ? cols : 0, quantized(x, s));
+  }
   if (threadIdx.x == 0) scale[unit] = s;
 }
 
@@ -165,16 +244,18 @@ constexpr int kRowBox = 32;
 constexpr int kScaleWarps = 2;
 constexpr int kEpilogueWarps = 8;
 constexpr int kTmemColumns = 512;
-constexpr int kRingBytes = 196608;
-constexpr int kMaxStages = 6;
-constexpr int kWarpStaging = 32 * 80;  // a warp's staging: 32 rows of 64 (+16) bytes
-constexpr int kProductSmem = kRingBytes + kEpilogueWarps * kWarpStaging + 1024;
+constexpr int kMaxStages = 5;
+constexpr int kStoreBox = 128;  // bytes of a row of a stored box
 
 template <int kTileN>
 struct ProductShape {
   static constexpr int kAccumulators = kTmemColumns / kTileN;
   static constexpr int kStageBytes = (kTileM + kTileN) * kBlock;  // tokens, then weight rows
-  static constexpr int kStages = kRingBytes / kStageBytes;
+  static constexpr int kStages = kTileN == 256 ? 3 : 5;
+  static constexpr int kRing = kStages * kStageBytes;
+  static constexpr int kHeld = kTileN / 128;  // boxes of 32 rows a warp's staging holds
+  static constexpr int kWarpStaging = kHeld * 32 * kStoreBox;
+  static constexpr int kSmem = kRing + kEpilogueWarps * kWarpStaging + 1024;
   static constexpr int kSums = kTileN / 2;        // of an epilogue thread
   static constexpr int kBlocksN = kTileN / kBlock;  // scale blocks of n
   static constexpr int kJoinStride = kTileN + 4;  // split sums meet in the ring: [128][..] floats
@@ -190,7 +271,7 @@ struct ProductArgs {
   int rows, n, k, experts;
   int kb, nb, n_tiles;  // blocks of k and of n, tiles of n
   int row_tiles;        // the most row tiles that the experts can have
-  bool vector_out;      // 16-byte stores of whole vectors are aligned
+  bool tma_out;         // the rows of out allow TMA stores
 };
 
 struct ProductShared {
@@ -417,58 +498,98 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Stores a warp's 32 rows x kSums columns: 64 bytes of a row at a time through
-// the warp's staging buffer, so that a store instruction covers 8 rows x 64
-// contiguous bytes.  kWhole: all rows and columns count and 16-byte stores are
-// aligned.
-template <typename T, int kSums, bool kWhole>
-__device__ __forceinline__ void store_tile(const ProductArgs& P, char* staging, int row0, int rows,
-                                           int col0, const uint64_t (&acc)[kSums / 2]) {
-  constexpr int kCols = 64 / static_cast<int>(sizeof(T));  // columns of one pass
-  constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+// Before a warp writes to its staging buffer: the stores that read it are done
+// with it.
+__device__ __forceinline__ void staging_free() {
+  if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+}
+
+// One 16-byte part of a row of sums, rounded: elements c .. c + 16 / sizeof(T) - 1.
+template <typename T, int kPairs>
+__device__ __forceinline__ uint4 rounded(const uint64_t (&acc)[kPairs], int c) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      const float2 f = pair_values(acc[c / 2 + i / 2]);
+      w[i] = __float_as_uint(i % 2 ? f.y : f.x);
+    } else {
+      const float2 f = pair_values(acc[c / 2 + i]);
+      w[i] = pack2<T>(f.x, f.y);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Stores a warp's 32 whole rows by TMA, boxes of 32 rows x 128 bytes: the copies run
+// while the warp goes on to the next tile.  (Stores from registers held the tile
+// up: 65536 x 4096 x 1024, 305 us instead of 233.)  The boxes stand in the 128-byte
+// swizzle, so that the lanes' writes spread over the banks; columns from n on are
+// clipped.
+template <typename T, int kSums, int kHeld>
+__device__ __forceinline__ void store_boxes(const ProductArgs& P, const CUtensorMap* map,
+                                            char* staging, int row0, int col0,
+                                            const uint64_t (&acc)[kSums / 2]) {
+  constexpr int kCols = kStoreBox / static_cast<int>(sizeof(T));
+  constexpr int kPart = 16 / static_cast<int>(sizeof(T));
   const int lane = threadIdx.x & 31;
-  uint4* mine = reinterpret_cast<uint4*>(staging + lane * 80);
-  const char* src = staging + lane / 4 * 80 + lane % 4 * 16;
-  const int64_t pitch = P.out_stride * 8;  // eight rows
-  T* dst = static_cast<T*>(P.out) + (static_cast<int64_t>(row0) + lane / 4) * P.out_stride + col0 +
-           lane % 4 * kVec;
+#pragma unroll
+  for (int c0 = 0; c0 < kSums; c0 += kHeld * kCols) {
+    staging_free();
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c0 + h * kCols < kSums)
+          *reinterpret_cast<uint4*>(staging + h * 32 * kStoreBox + lane * kStoreBox +
+                                    ((i ^ (lane & 7)) << 4)) =
+              rounded<T>(acc, c0 + h * kCols + i * kPart);
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) {
+#pragma unroll
+      for (int h = 0; h < kHeld; ++h)
+        if (c0 + h * kCols < kSums && col0 + c0 + h * kCols < P.n)
+          asm volatile(
+              "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::
+                  "l"(map),
+              "r"(col0 + c0 + h * kCols), "r"(row0), "r"(smem_u32(staging + h * 32 * kStoreBox))
+              : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+  }
+}
+
+// Stores up to 32 rows, of any alignment, 64 bytes of a row at a time through the
+// staging buffer.
+template <typename T, int kSums>
+__device__ __forceinline__ void store_rows(const ProductArgs& P, char* staging, int row0, int rows,
+                                           int col0, const uint64_t (&acc)[kSums / 2]) {
+  constexpr int kCols = 64 / static_cast<int>(sizeof(T));
+  constexpr int kPart = 16 / static_cast<int>(sizeof(T));
+  const int lane = threadIdx.x & 31;
+  staging_free();
 #pragma unroll
   for (int c0 = 0; c0 < kSums; c0 += kCols) {
-    if (!kWhole && col0 + c0 >= P.n) break;
+    if (col0 + c0 >= P.n) break;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(T) == 4) {
-          const float2 f = pair_values(acc[(c0 + v * 4) / 2 + i / 2]);
-          w[i] = __float_as_uint(i % 2 ? f.y : f.x);
-        } else {
-          const float2 f = pair_values(acc[(c0 + v * 8) / 2 + i]);
-          w[i] = pack2<T>(f.x, f.y);
-        }
-      }
-      mine[v] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<uint4*>(staging + lane * 80 + i * 16) = rounded<T>(acc, c0 + i * kPart);
     __syncwarp();
-    if constexpr (kWhole) {
-      uint4 q[4];
+    const int cols = P.n - col0 - c0 < kCols ? P.n - col0 - c0 : kCols;
+    T* dst = static_cast<T*>(P.out) + static_cast<int64_t>(row0) * P.out_stride + col0 + c0;
+    if (P.tma_out) {  // whole 16-byte parts, on 16-byte boundaries
 #pragma unroll
-      for (int g = 0; g < 4; ++g) q[g] = *reinterpret_cast<const uint4*>(src + g * 8 * 80);
-#pragma unroll
-      for (int g = 0; g < 4; ++g) *reinterpret_cast<uint4*>(dst + g * pitch + c0) = q[g];
+      for (int r = lane / 4; r < 32; r += 8)
+        if (r < rows && lane % 4 * kPart < cols)
+          *reinterpret_cast<uint4*>(dst + r * P.out_stride + lane % 4 * kPart) =
+              *reinterpret_cast<const uint4*>(staging + r * 80 + lane % 4 * 16);
     } else {
-      const int col = col0 + c0 + lane % 4 * kVec;
-      for (int g = 0; g < 4; ++g) {
-        if (g * 8 + lane / 4 >= rows) break;
-        const char* from = src + g * 8 * 80;
-        T* to = dst + g * pitch + c0;
-        if (P.vector_out && col + kVec <= P.n) {
-          *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
-        } else {
-          for (int i = 0; i < kVec && col + i < P.n; ++i)
-            to[i] = reinterpret_cast<const T*>(from)[i];
-        }
+      for (int i = lane; i < rows * kCols; i += 32) {
+        const int r = i / kCols, c = i % kCols;
+        if (c < cols)
+          dst[r * P.out_stride + c] = *reinterpret_cast<const T*>(staging + r * 80 + c * sizeof(T));
       }
     }
     __syncwarp();
@@ -480,6 +601,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap a_map,
                    const __grid_constant__ CUtensorMap a_part_map,
                    const __grid_constant__ CUtensorMap w_map,
+                   const __grid_constant__ CUtensorMap out_map,
                    const __grid_constant__ ProductArgs P) {
   using Shape = ProductShape<kTileN>;
   constexpr int kStages = Shape::kStages, kStageBytes = Shape::kStageBytes;
@@ -489,7 +611,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   __shared__ ProductShared S;
   char* ring = reinterpret_cast<char*>(
       (reinterpret_cast<uintptr_t>(product_smem) + 1023) & ~uintptr_t(1023));
-  char* staging = ring + kRingBytes;
+  char* staging = ring + Shape::kRing;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int* dead = &S.dead;
 
@@ -505,6 +627,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 2) tmem_alloc(&S.tmem, kTmemColumns);
+  // so far nothing that the kernel before this one writes has been read
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   build_tiles(P, S);
   fence_before_sync();
   __syncthreads();
@@ -642,14 +767,19 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       // the rows past the last expert
       T* out = static_cast<T*>(P.out);
       for (int64_t r = group_start(P, P.experts) + static_cast<int64_t>(blockIdx.x); r < P.rows;
-           r += gridDim.x)
-        for (int c = threadIdx.x - 64; c < P.n; c += 64)
-          out[r * P.out_stride + c] = from_f32<T>(0.f);
+           r += gridDim.x) {
+        T* row = out + r * P.out_stride;
+        if (P.tma_out)
+          for (int c = (threadIdx.x - 64) * kVec<T>; c < P.n; c += 64 * kVec<T>)
+            *reinterpret_cast<uint4*>(row + c) = make_uint4(0, 0, 0, 0);
+        else
+          for (int c = threadIdx.x - 64; c < P.n; c += 64) row[c] = from_f32<T>(0.f);
+      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int quarter = warp & 3, half = (warp - 4) >> 2;
-    char* mine = staging + (warp - 4) * kWarpStaging;
+    char* mine = staging + (warp - 4) * Shape::kWarpStaging;
     const uint32_t taddr0 = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kSums;
     int stage = 0;
     uint32_t parity = 0, count = 0;  // count: blocks so far
@@ -716,12 +846,13 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           }
         }
       } else if (on && ok) {
-        if (rows >= 32 && col0 + kSums <= P.n && P.vector_out)
-          store_tile<T, kSums, true>(P, mine, row0, rows, col0, acc);
+        if (rows >= 32 && P.tma_out)
+          store_boxes<T, kSums, Shape::kHeld>(P, &out_map, mine, row0, col0, acc);
         else
-          store_tile<T, kSums, false>(P, mine, row0, rows, col0, acc);
+          store_rows<T, kSums>(P, mine, row0, rows < 32 ? rows : 32, col0, acc);
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncwarp();
   if constexpr (kSplit) {
@@ -748,7 +879,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   if (threadIdx.x == 0 && S.dead && P.status) atomicOr(P.status, TBE_ERR_TIMEOUT);
 }
 
-// A map of an 8-bit matrix for 128-byte-swizzled boxes of 128 columns.
+// A map of a matrix of 1-, 2- or 4-byte elements, a row every `stride` bytes, for
+// 128-byte-swizzled boxes of 128 bytes x box_rows.
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -767,16 +899,20 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-bool make_map(CUtensorMap* map, const uint8_t* base, int64_t rows, int64_t cols, int64_t stride,
-              int box_rows) {
+bool make_map(CUtensorMap* map, const void* base, int bytes, int64_t rows, int64_t cols,
+              int64_t stride, int box_rows) {
   const EncodeTiled encode = encode_tiled();
   if (!encode) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};
-  const cuuint32_t box[2] = {kBlock, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / bytes),
+                             static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t steps[2] = {1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides,
-                box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const CUtensorMapDataType type = bytes == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16
+                                                : CU_TENSOR_MAP_DATA_TYPE_UINT32;
+  return encode(map, type, 2, const_cast<void*>(base), dims, strides, box, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -845,9 +981,13 @@ extern "C" tbe_status tbe_quantize_weights(const void* w, int32_t dtype, int64_t
   if (nb * kb > INT32_MAX / experts) return TBE_EUNSUPPORTED;
   return for_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    quantize_weights_kernel<T><<<static_cast<unsigned>(experts * nb * kb), 256, 0,
-                                 static_cast<cudaStream_t>(stream)>>>(
-        static_cast<const T*>(w), n, k, static_cast<int>(nb), static_cast<int>(kb), q, scale);
+    const bool aligned = k % 8 == 0 && aligned_to(w, 16) && aligned_to(q, 8);
+    const auto kernel =
+        aligned ? quantize_weights_kernel<T, true> : quantize_weights_kernel<T, false>;
+    kernel<<<static_cast<unsigned>(experts * nb * kb), 256, 0,
+             static_cast<cudaStream_t>(stream)>>>(static_cast<const T*>(w), n, k,
+                                                  static_cast<int>(nb), static_cast<int>(kb), q,
+                                                  scale);
     return launched();
   });
 }
@@ -889,20 +1029,24 @@ extern "C" tbe_status tbe_expert_product(const uint8_t* a, int64_t a_stride, con
   P.kb = static_cast<int>((k + kBlock - 1) / kBlock);
   P.nb = static_cast<int>((n + kBlock - 1) / kBlock);
   const int ob = dtype_bytes(out_dtype);
-  P.vector_out = aligned_to(out, 16) && out_stride * ob % 16 == 0;
+  // (a TMA store clips a row at a multiple of 16 bytes)
+  P.tma_out = aligned_to(out, 16) && out_stride * ob % 16 == 0 && n * ob % 16 == 0;
   CUtensorMap a_map, a_part_map;
-  if (!make_map(&a_map, a, rows, k, a_stride, kTileM) ||
-      !make_map(&a_part_map, a, rows, k, a_stride, kRowBox))
+  if (!make_map(&a_map, a, 1, rows, k, a_stride, kTileM) ||
+      !make_map(&a_part_map, a, 1, rows, k, a_stride, kRowBox))
     return TBE_ECUDA;
+  CUtensorMap out_map = a_map;  // not used unless P.tma_out
+  if (P.tma_out && !make_map(&out_map, out, ob, rows, n, out_stride * ob, 32)) return TBE_ECUDA;
   const auto launch = [&](auto t, auto tile_n, auto split_tag, int split) -> tbe_status {
     using T = decltype(t);
     constexpr int kTileN = decltype(tile_n)::value;
     constexpr bool kSplit = decltype(split_tag)::value;
     P.n_tiles = static_cast<int>((n + kTileN - 1) / kTileN);
     CUtensorMap w_map;
-    if (!make_map(&w_map, w, static_cast<int64_t>(experts) * n, k, k, kTileN)) return TBE_ECUDA;
+    if (!make_map(&w_map, w, 1, static_cast<int64_t>(experts) * n, k, k, kTileN)) return TBE_ECUDA;
     const auto kernel = product_kernel<T, kTileN, kSplit>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem) !=
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             ProductShape<kTileN>::kSmem) !=
         cudaSuccess)
       return TBE_ECUDA;
     // tiles, at most (every expert's last one may be a part)
@@ -912,15 +1056,18 @@ extern "C" tbe_status tbe_expert_product(const uint8_t* a, int64_t a_stride, con
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(kSplit ? most * split : most < sms ? most : sms));
     cfg.blockDim = dim3(kProductThreads);
-    cfg.dynamicSmemBytes = kProductSmem;
+    cfg.dynamicSmemBytes = ProductShape<kTileN>::kSmem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(split);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    // its start may overlap the end of the kernel before it (griddepcontrol.wait)
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(split);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = kSplit ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, kernel, a_map, a_part_map, w_map, P) != cudaSuccess)
+    cfg.numAttrs = kSplit ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, a_map, a_part_map, w_map, out_map, P) != cudaSuccess)
       return TBE_ECUDA;
     return launched();
   };
@@ -932,12 +1079,13 @@ extern "C" tbe_status tbe_expert_product(const uint8_t* a, int64_t a_stride, con
     int split = 1;
     while (split < 8 && tiles * split * 2 <= sms && P.kb >= split * 4) split *= 2;
     if (split > 1) return launch(t, Narrow{}, std::true_type{}, split);
-    // Rounds of tiles over the multiprocessors, times a tile's time: measured, a block of k
-    // takes 0.39 us of 256 columns and 0.3 of 128, and a tile's start and store 1.8 and 1 us
-    // (65536 rows, 16 experts, 4096 x 4096: 0.88 ms with 256 columns, 1.03 with 128).
+    // Rounds of tiles over the multiprocessors, times a tile's time: measured on 65536 rows of
+    // 16 experts and 4096 columns, a block of k takes 0.42 us of 256 columns and 0.27 of 128,
+    // and a tile's start and end 1.55 and 0.76 us (k = 2048: 444 us with 256 columns, 501 with
+    // 128; 5000 rows, 8 experts, 1000 x 1008: 21.6 and 18.2).
     const int64_t m = rows / kTileM + (experts < rows ? experts : rows) / 2;
     const auto rounds = [&](int64_t cols) { return (m * ((n + cols - 1) / cols) + sms - 1) / sms; };
-    if (rounds(128) * (P.kb * 30 + 100) < rounds(256) * (P.kb * 39 + 180))
+    if (rounds(128) * (P.kb * 27 + 76) < rounds(256) * (P.kb * 42 + 155))
       return launch(t, Narrow{}, std::false_type{}, 1);
     return launch(t, Wide{}, std::false_type{}, 1);
   });
