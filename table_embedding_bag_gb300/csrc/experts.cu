@@ -14,18 +14,28 @@ constexpr unsigned kAll = 0xffffffffu;
 
 // ---------------------------------------------------------------------- sort
 //
-// A counting sort in one launch: one cluster of up to 16 CTAs, a warp a contiguous
-// chunk of the assignments.  A warp counts its experts in its own row of shared
-// memory; the rows are scanned over (expert, CTA, warp), the CTAs reading one
-// another's totals in shared memory; then each warp walks its chunk again, 32
-// assignments at a time, giving each its place: the warp's running count of the
-// expert plus the number of lower lanes with the same expert.  Stable by
-// construction, no atomics on results.  Dropped assignments are counted as
-// expert E, which comes last.
+// A counting sort: a warp takes a contiguous chunk of the assignments and counts
+// its experts in its own row of shared memory; the rows are scanned over (expert,
+// CTA, warp); then each warp walks its chunk again, 32 assignments at a time,
+// giving each its place: the warp's running count of the expert plus the number
+// of lower lanes with the same expert.  Stable by construction, no atomics on
+// results.  Dropped assignments are counted as expert E, which comes last.
+//
+// Up to kSortOneLaunch assignments it is one launch of one cluster, whose CTAs read
+// one another's totals in shared memory; above, three launches over the whole GPU
+// (count, scan, rank), whose totals stand in the part of `position` that their
+// CTA writes last.  Both measured (64 experts): 65536 assignments 9.0 us in one
+// launch and 11.8 in three, 131072 13.3 and 13.2, 262144 21.7 and 12.6, a million 70
+// and 25 us.
 constexpr int kSortWarps = 32;
 constexpr int kSortUnroll = 4;      // rounds of 32 assignments whose loads are in flight
 constexpr int kSortPerCta = 2048;   // assignments from which another CTA pays
 constexpr int kSortMostCtas = 16;
+constexpr int kSortOneLaunch = 131072;
+constexpr int kSortGridChunk = 4096;  // assignments of a CTA of three launches, at least
+constexpr int kSortGridCtas = 304;
+constexpr int kScanCtas = 8;
+static_assert(kSortGridChunk > TBE_MAX_EXPERTS, "a CTA's totals fit its part of position");
 
 template <typename IdT>
 __device__ __forceinline__ int expert_of(IdT e, int experts) {
@@ -47,100 +57,66 @@ __device__ __forceinline__ int load_from_cta(const int* p, int rank) {
   return v;
 }
 
+// Assignments [first, last) of a warp.
+struct Chunk {
+  int64_t first, last;
+};
+__device__ __forceinline__ Chunk warp_chunk(int64_t n, int64_t cta_first, int64_t per_warp) {
+  const int64_t first = cta_first + (threadIdx.x >> 5) * per_warp;
+  return {first, first + per_warp < n ? first + per_warp : n};
+}
+
+// Every warp's counts of its chunk, count[warp][expert], and their sums over
+// the warps, total[expert].  The whole CTA; ends before a barrier.
 template <typename IdT>
-__global__ void __launch_bounds__(kSortWarps * 32)
-    expert_sort_kernel(const IdT* __restrict__ ids, int n, int experts, int* __restrict__ offsets,
-                       int* __restrict__ source, int* __restrict__ position) {
-  extern __shared__ int sort_smem[];
-  __shared__ int warp_sum[kSortWarps];
-  const int buckets = experts + 1;
-  int* total = sort_smem;            // [buckets] this CTA's assignments of each expert
-  int* count = sort_smem + buckets;  // [kSortWarps][buckets]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ctas = gridDim.x, rank = blockIdx.x;  // one cluster
+__device__ __forceinline__ void count_chunks(const IdT* ids, Chunk c, int experts, int* count,
+                                             int* total) {
+  const int buckets = experts + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < kSortWarps * buckets; i += blockDim.x) count[i] = 0;
   __syncthreads();
-  const int warps = ctas * kSortWarps;
-  const int64_t chunk = (static_cast<int64_t>(n) + warps * 32 - 1) / (warps * 32) * 32;
-  const int64_t first = (static_cast<int64_t>(rank) * kSortWarps + warp) * chunk;
-  const int64_t last = first + chunk < n ? first + chunk : n;
   int* mine = count + warp * buckets;
-  for (int64_t a0 = first + lane; a0 < last; a0 += 32 * kSortUnroll) {
+  for (int64_t a0 = c.first + lane; a0 < c.last; a0 += 32 * kSortUnroll) {
     IdT e[kSortUnroll];
 #pragma unroll
-    for (int u = 0; u < kSortUnroll; ++u) e[u] = a0 + 32 * u < last ? ids[a0 + 32 * u] : IdT(0);
+    for (int u = 0; u < kSortUnroll; ++u) e[u] = a0 + 32 * u < c.last ? ids[a0 + 32 * u] : IdT(0);
 #pragma unroll
     for (int u = 0; u < kSortUnroll; ++u)
-      if (a0 + 32 * u < last) atomicAdd(mine + expert_of(e[u], experts), 1);
+      if (a0 + 32 * u < c.last) atomicAdd(mine + expert_of(e[u], experts), 1);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < buckets; e += blockDim.x) {
-    int c = 0;
-    for (int w = 0; w < kSortWarps; ++w) c += count[w * buckets + e];
-    total[e] = c;
+    int sum = 0;
+#pragma unroll 16
+    for (int w = 0; w < kSortWarps; ++w) sum += count[w * buckets + e];
+    total[e] = sum;
   }
-  if (ctas > 1) {
-    cluster_arrive();
-    cluster_wait();
-  } else {
-    __syncthreads();
+}
+
+// Turns expert e's counts into every warp's first place, from `at` on.
+__device__ __forceinline__ void counts_to_places(int* count, int buckets, int e, int at) {
+#pragma unroll 16
+  for (int w = 0; w < kSortWarps; ++w) {
+    const int c = count[w * buckets + e];
+    count[w * buckets + e] = at;
+    at += c;
   }
-  // exclusive scan over (expert, CTA, warp); one expert per thread, in rounds
-  int carry = 0;
-  for (int e0 = 0; e0 < buckets; e0 += blockDim.x) {
-    const int e = e0 + threadIdx.x;
-    int all = 0, before_me = 0;
-    if (e < buckets) {
-      if (ctas == 1) {
-        all = total[e];
-      } else {
-        for (int r = 0; r < ctas; ++r) {
-          const int c = load_from_cta(total + e, r);
-          all += c;
-          before_me += r < rank ? c : 0;
-        }
-      }
-    }
-    int incl = all;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kAll, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    int sums = warp_sum[lane];  // kSortWarps of them, scanned by every warp
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kAll, sums, o);
-      if (lane >= o) sums += y;
-    }
-    const int before = carry + (warp ? __shfl_sync(kAll, sums, warp - 1) : 0);
-    carry += __shfl_sync(kAll, sums, 31);
-    if (e < buckets) {
-      int at = before + incl - all;
-      if (rank == 0) offsets[e] = at;  // offsets[E]: the first dropped place, the number kept
-      at += before_me;
-      for (int w = 0; w < kSortWarps; ++w) {
-        const int c = count[w * buckets + e];
-        count[w * buckets + e] = at;
-        at += c;
-      }
-    }
-    __syncthreads();
-  }
-  if (ctas > 1) cluster_arrive();  // this CTA reads no other's memory any more
-  for (int64_t a0 = first; a0 < last; a0 += 32 * kSortUnroll) {
+}
+
+template <typename IdT>
+__device__ __forceinline__ void rank_chunk(const IdT* ids, Chunk c, int experts, int* mine,
+                                           int* source, int* position) {
+  const int lane = threadIdx.x & 31;
+  for (int64_t a0 = c.first; a0 < c.last; a0 += 32 * kSortUnroll) {
     IdT id[kSortUnroll];
 #pragma unroll
     for (int u = 0; u < kSortUnroll; ++u) {
       const int64_t a = a0 + 32 * u + lane;
-      id[u] = a < last ? ids[a] : IdT(0);
+      id[u] = a < c.last ? ids[a] : IdT(0);
     }
 #pragma unroll
     for (int u = 0; u < kSortUnroll; ++u) {
       const int64_t a = a0 + 32 * u + lane;
-      const bool on = a < last;
+      const bool on = a < c.last;
       const int e = on ? expert_of(id[u], experts) : -1;
       const unsigned same = __match_any_sync(kAll, e);
       int place = 0;
@@ -154,7 +130,169 @@ __global__ void __launch_bounds__(kSortWarps * 32)
       }
     }
   }
+}
+
+// Exclusive scan over the CTA's threads, and the sum; kSortWarps warps.
+__device__ __forceinline__ int block_scan(int v, int* warp_sum, int* sum) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kAll, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  int sums = warp_sum[lane];  // scanned by every warp
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kAll, sums, o);
+    if (lane >= o) sums += y;
+  }
+  const int before = warp ? __shfl_sync(kAll, sums, warp - 1) : 0;
+  *sum = __shfl_sync(kAll, sums, 31);
+  __syncthreads();
+  return before + incl - v;
+}
+
+template <typename IdT>
+__global__ void __launch_bounds__(kSortWarps * 32)
+    expert_sort_kernel(const IdT* __restrict__ ids, int n, int experts, int* __restrict__ offsets,
+                       int* __restrict__ source, int* __restrict__ position) {
+  extern __shared__ int sort_smem[];
+  __shared__ int warp_sum[kSortWarps];
+  const int buckets = experts + 1;
+  int* total = sort_smem;            // [buckets] this CTA's assignments of each expert
+  int* count = sort_smem + buckets;  // [kSortWarps][buckets]
+  const int ctas = gridDim.x, rank = blockIdx.x;  // one cluster
+  const int warps = ctas * kSortWarps;
+  const int64_t per_warp = (static_cast<int64_t>(n) + warps * 32 - 1) / (warps * 32) * 32;
+  const Chunk chunk = warp_chunk(n, rank * kSortWarps * per_warp, per_warp);
+  count_chunks(ids, chunk, experts, count, total);
+  if (ctas > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  int carry = 0;
+  for (int e0 = 0; e0 < buckets; e0 += blockDim.x) {  // one expert per thread, in rounds
+    const int e = e0 + threadIdx.x;
+    int all = 0, before_me = 0;
+    if (e < buckets) {
+      if (ctas == 1) {
+        all = total[e];
+      } else {
+        int c[kSortMostCtas];
+#pragma unroll
+        for (int r = 0; r < kSortMostCtas; ++r) c[r] = r < ctas ? load_from_cta(total + e, r) : 0;
+#pragma unroll
+        for (int r = 0; r < kSortMostCtas; ++r) {
+          all += c[r];
+          before_me += r < rank ? c[r] : 0;
+        }
+      }
+    }
+    int sum;
+    const int at = carry + block_scan(all, warp_sum, &sum);
+    carry += sum;
+    if (e < buckets) {
+      if (rank == 0) offsets[e] = at;  // offsets[E]: the first dropped place, the number kept
+      counts_to_places(count, buckets, e, at + before_me);
+    }
+  }
+  __syncthreads();
+  if (ctas > 1) cluster_arrive();  // this CTA reads no other's memory any more
+  rank_chunk(ids, chunk, experts, count + (threadIdx.x >> 5) * buckets, source, position);
   if (ctas > 1) cluster_wait();  // no CTA ends while another may read its totals
+}
+
+// The three launches.  The CTAs have equal parts of the assignments (the first n % ctas one
+// more), and a CTA's totals, then its first places, stand at the start of its part of position
+// until it ranks them.
+__device__ __forceinline__ int64_t cta_first(int n, int c, int ctas) {
+  const int rest = n % ctas;
+  return static_cast<int64_t>(n / ctas) * c + (c < rest ? c : rest);
+}
+__device__ __forceinline__ Chunk my_chunk(int n) {
+  const int64_t first = cta_first(n, blockIdx.x, gridDim.x);
+  const int64_t last = cta_first(n, blockIdx.x + 1, gridDim.x);
+  const int64_t per_warp = (last - first + kSortWarps * 32 - 1) / (kSortWarps * 32) * 32;
+  return warp_chunk(last, first, per_warp);
+}
+
+template <typename IdT>
+__global__ void __launch_bounds__(kSortWarps * 32)
+    expert_count_kernel(const IdT* __restrict__ ids, int n, int experts,
+                        int* __restrict__ position) {
+  extern __shared__ int sort_smem[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int buckets = experts + 1;
+  count_chunks(ids, my_chunk(n), experts, sort_smem + buckets, sort_smem);
+  int* row = position + cta_first(n, blockIdx.x, gridDim.x);
+  for (int e = threadIdx.x; e < buckets; e += blockDim.x)  // the entries it summed: no barrier
+    row[e] = sort_smem[e];
+}
+
+// One CTA, or for many experts a cluster whose CTAs have equal shares of them; `segments`
+// threads an expert, each over a run of the counting CTAs.
+__global__ void __launch_bounds__(kSortWarps * 32)
+    expert_scan_kernel(int n, int experts, int ctas, int share, int segments,
+                       int* __restrict__ offsets, int* __restrict__ position) {
+  __shared__ int warp_sum[kSortWarps];
+  __shared__ int total;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int run = (ctas + segments - 1) / segments;
+  // an expert's threads are neighbours, so the scan runs over (expert, run of CTAs)
+  const int in_share = static_cast<int>(threadIdx.x) / segments;
+  const int e = static_cast<int>(blockIdx.x) * share + in_share;
+  const bool on = in_share < share && e <= experts;
+  const int c0 = static_cast<int>(threadIdx.x) % segments * run;
+  const int c1 = on ? (c0 + run < ctas ? c0 + run : ctas) : c0;
+  int sum = 0;
+#pragma unroll 8
+  for (int c = c0; c < c1; ++c) sum += position[cta_first(n, c, ctas) + e];
+  int all;
+  int at = block_scan(sum, warp_sum, &all);
+  if (gridDim.x > 1) {
+    if (threadIdx.x == 0) total = all;
+    cluster_arrive();
+    cluster_wait();
+    int before[kScanCtas];
+#pragma unroll
+    for (int r = 0; r < kScanCtas; ++r)
+      before[r] = r < static_cast<int>(blockIdx.x) ? load_from_cta(&total, r) : 0;
+#pragma unroll
+    for (int r = 0; r < kScanCtas; ++r) at += before[r];
+    cluster_arrive();
+  }
+  if (on && c0 == 0) offsets[e] = at;
+#pragma unroll 8
+  for (int c = c0; c < c1; ++c) {
+    int* p = position + cta_first(n, c, ctas) + e;
+    const int v = *p;
+    *p = at;
+    at += v;
+  }
+  if (gridDim.x > 1) cluster_wait();  // no CTA ends while another may read its total
+}
+
+template <typename IdT>
+__global__ void __launch_bounds__(kSortWarps * 32)
+    expert_rank_kernel(const IdT* __restrict__ ids, int n, int experts,
+                       int* __restrict__ source, int* position) {
+  extern __shared__ int sort_smem[];
+  const int buckets = experts + 1;
+  int* count = sort_smem + buckets;
+  const Chunk chunk = my_chunk(n);
+  count_chunks(ids, chunk, experts, count, sort_smem);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int* row = position + cta_first(n, blockIdx.x, gridDim.x);
+  for (int e = threadIdx.x; e < buckets; e += blockDim.x)
+    counts_to_places(count, buckets, e, row[e]);
+  __syncthreads();  // the places have been read: position may be written
+  rank_chunk(ids, chunk, experts, count + (threadIdx.x >> 5) * buckets, source, position);
 }
 
 // --------------------------------------------------------------- moving rows
@@ -498,33 +636,74 @@ extern "C" tbe_status tbe_expert_sort(const void* ids, int32_t index_dtype, int6
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int n = static_cast<int>(tokens * k);
   const size_t smem = static_cast<size_t>(kSortWarps + 1) * (experts + 1) * 4;
-  int ctas = 1;
-  while (ctas < kSortMostCtas && n > ctas * kSortPerCta) ctas *= 2;
-  const auto go = [&](auto* p, auto kernel) {
-    // clusters above eight CTAs have to be asked for
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (kSortWarps + 1) * (TBE_MAX_EXPERTS + 1) * 4) != cudaSuccess ||
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
-            cudaSuccess)
+  // shared memory above 48 KB and clusters above eight CTAs have to be asked for
+  const auto room_for = [&](auto kernel) {
+    return smem <= 48 * 1024 ||
+           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (kSortWarps + 1) * (TBE_MAX_EXPERTS + 1) * 4) == cudaSuccess;
+  };
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kSortWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  const auto one_launch = [&](auto* p) {
+    using IdT = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
+    const auto kernel = expert_sort_kernel<IdT>;
+    int ctas = 1;
+    while (ctas < kSortMostCtas && n > ctas * kSortPerCta) ctas *= 2;
+    if (!room_for(kernel) ||
+        (ctas > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                          1) != cudaSuccess))
       return TBE_ECUDA;
-    cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(kSortWarps * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
     cfg.numAttrs = ctas > 1 ? 1 : 0;
     if (cudaLaunchKernelEx(&cfg, kernel, p, n, experts, offsets, source, position) != cudaSuccess)
       return TBE_ECUDA;
     return launched();
   };
-  return index_dtype == TBE_DT_I32
-             ? go(static_cast<const int32_t*>(ids), expert_sort_kernel<int32_t>)
-             : go(static_cast<const int64_t*>(ids), expert_sort_kernel<int64_t>);
+  const auto three_launches = [&](auto* p) {
+    using IdT = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
+    const int ctas = n / kSortGridChunk < kSortGridCtas ? n / kSortGridChunk : kSortGridCtas;
+    const auto count = expert_count_kernel<IdT>;
+    const auto rank = expert_rank_kernel<IdT>;
+    if (!room_for(count) || !room_for(rank)) return TBE_ECUDA;
+    const int scan_ctas = experts < 256 ? 1 : kScanCtas;
+    const int share = (experts + scan_ctas) / scan_ctas;  // of the E + 1 buckets
+    int segments = 1;
+    while (segments * 2 * share <= kSortWarps * 32) segments *= 2;
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.numAttrs = 0;
+    if (cudaLaunchKernelEx(&cfg, count, p, n, experts, position) != cudaSuccess)
+      return TBE_ECUDA;
+    note_launch();
+    // the next two begin while the launch before them ends (griddepcontrol.wait)
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(scan_ctas);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    cfg.gridDim = dim3(static_cast<unsigned>(scan_ctas));
+    cfg.dynamicSmemBytes = 0;
+    if (cudaLaunchKernelEx(&cfg, expert_scan_kernel, n, experts, ctas, share, segments, offsets,
+                           position) != cudaSuccess)
+      return TBE_ECUDA;
+    cfg.numAttrs = 1;
+    note_launch();
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.dynamicSmemBytes = smem;
+    if (cudaLaunchKernelEx(&cfg, rank, p, n, experts, source, position) != cudaSuccess)
+      return TBE_ECUDA;
+    return launched();
+  };
+  const auto go = [&](auto* p) { return n <= kSortOneLaunch ? one_launch(p) : three_launches(p); };
+  return index_dtype == TBE_DT_I32 ? go(static_cast<const int32_t*>(ids))
+                                   : go(static_cast<const int64_t*>(ids));
 }
 
 extern "C" tbe_status tbe_expert_dispatch(const void* x, int32_t dtype, int64_t tokens, int32_t k,
