@@ -279,6 +279,7 @@ struct ProductShared {
   // free and the block's product stands in its accumulator, and the block's scales are there;
   // taken: the accumulator has been read
   unsigned long long full[kMaxStages], done[kMaxStages], taken[4], drain;
+  unsigned long long stuck;  // nothing arrives (TBE_TEST_STUCK_WAIT)
   uint32_t tmem;
   int dead;
   float scale[kScaleRing][2][kTileM];  // [block][128 columns of n][token]
@@ -295,10 +296,10 @@ __device__ __forceinline__ int group_start(const ProductArgs& P, int e) {
 // A wait of a role: gives up at the bound, or soon after another role has.
 // The whole warp calls it and goes on or gives up as one.
 __device__ __forceinline__ bool role_wait(unsigned long long* bar, uint32_t parity,
-                                          volatile int* dead) {
+                                          volatile int* dead, uint32_t limit = kSpinLimit) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   bool got = false;
-  for (uint32_t i = 0; i < kSpinLimit && !got; ++i) {
+  for (uint32_t i = 0; i < limit && !got; ++i) {
     got = mbar_try_wait(bar, parity);
     if (i > 64 && !got) {
       if (*dead) break;
@@ -623,6 +624,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     for (int i = 0; i < kAccumulators; ++i)
       mbar_init(&S.taken[i], kEpilogueWarps);
     mbar_init(&S.drain, 1);
+    mbar_init(&S.stuck, 1);
     S.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -675,9 +677,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           if (++stage == kStages) stage = 0, parity ^= 1;
         }
       }
-      if (!ok)  // let the copies in flight land before the CTA ends
-        for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-          mbar_wait(&S.full[i % kStages], (i / kStages) & 1);
+      // Whoever has given up: the copies in flight land before the CTA ends.
+      for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+        mbar_wait(&S.full[i % kStages], (i / kStages) & 1);
     } else if (warp == 1) {
       const uint32_t idesc = make_idesc(0, kTileM, kTileN);  // e4m3 x e4m3 -> fp32
       const uint64_t a_desc = swizzled_desc(ring), w_desc = swizzled_desc(ring + kTileM * kBlock);
@@ -705,11 +707,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           if (++slot == kAccumulators) slot = 0, tparity ^= 1;
         }
       }
-      if (!ok) {
-        if (elected()) mma_commit(&S.drain);
-        __syncwarp();
-        mbar_wait(&S.drain, 0);
-      }
+      // Whoever has given up: the MMAs are done before tensor memory is freed.
+      if (elected()) mma_commit(&S.drain);
+      __syncwarp();
+      mbar_wait(&S.drain, 0);
     } else {
       // A block's scales replace those of the block kScaleRing earlier.  Those have been read
       // when the MMAs of the block kAccumulators earlier are done, for they took its accumulator.
@@ -784,6 +785,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     int stage = 0;
     uint32_t parity = 0, count = 0;  // count: blocks so far
     bool ok = true;
+    // test-only builds: a first wait that runs out, to take the way out below
+    if (TBE_TEST_STUCK_WAIT && first < tiles)
+      ok = role_wait(&S.stuck, 0, dead, TBE_TEST_STUCK_WAIT);
     for (int t = first; t < tiles && ok; t += stride) {
       const ProductTile tile = tile_at<kTileN>(P, S, t);
       const int row0 = tile.row0 + quarter * 32;
