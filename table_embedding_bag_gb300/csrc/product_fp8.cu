@@ -222,21 +222,29 @@ __global__ void __launch_bounds__(256)
 // registers: a scale differs from block to block, so the sum over blocks cannot
 // stay in tensor memory.
 //
-// A tile is 128 tokens x kTileN columns of n.  kTileN = 256 has two accumulators
-// in tensor memory and is for many tokens: it reads 96 bytes of shared memory a
-// multiply-add cycle where 128 columns read 128, all that shared memory gives.
-// kTileN = 128 has four accumulators, and finer tiles.
+// What bounds it: shared memory, which gives 128 bytes a clock, MMA operands and
+// arriving copies together; and tensor memory, which the epilogue reads while the
+// MMAs use most of its bandwidth (alone an epilogue warp's reads run at 800 bytes a
+// clock, beside MMAs at 150 to 220; a block of 256 columns has 128 KB).  So tiles
+// are as large as tensor memory allows, two accumulators of 256 columns, once
+// there are enough tokens.  How CTAs share a tile:
+//   kPair   two CTAs form 256 tokens x 256 columns of n: an MMA (cta_group::2) reads
+//           both CTAs' shared memory, which holds half of the tokens and half of the
+//           weight rows in each: two thirds of the bytes of a lone CTA with
+//           128 x 256 (65536 rows, 16 experts, 4096 x 4096: 765 us and 873)
+//   kAlone  a CTA forms 128 tokens x 128 columns, with four accumulators: for fewer
+//           or uneven tiles
+//   kSplit  the CTAs of a cluster each form a part of the sum over blocks of one
+//           kAlone tile, for few tokens; the parts meet in shared memory and are
+//           added in the order of the ranks (one row, 4096 x 4096: 14 us and 17)
 //
 // Warps: 0 issues the TMA copies, 1 the MMAs; 2 and 3 bring the blocks' scales
 // to shared memory ahead of their use (an epilogue warp that waits for its own
-// scales costs more than the block), and clear the rows past the last expert;
-// 4..11 are the epilogue: warp w holds tokens 32 (w % 4) .. + 31 (one a lane)
-// and half w / 8 of the columns.  A tile with few tokens copies them 32 rows at a
-// time; the other rows of the MMA hold what the buffer held before and reach
-// only results that are not stored.
-//
-// kSplit: the CTAs of a cluster each form a part of the sum over blocks of one
-// tile; the parts meet in shared memory and are added in the order of the ranks.
+// scales costs more than the block: 512 us instead of 587 at 4096 x 2048), and clear
+// the rows past the last expert; 4..11 are the epilogue: warp w holds tokens 32 (w % 4)
+// .. + 31 of its CTA (one a lane) and half w / 8 of the columns.  A tile with few tokens copies
+// them 32 rows at a time; the other rows of the MMA hold what the buffer held before and
+// reach only results that are not stored.
 constexpr int kTileM = 128;
 constexpr int kScaleRing = 8;  // blocks whose scales stand in shared memory
 constexpr int kProductThreads = 384;
@@ -247,11 +255,16 @@ constexpr int kTmemColumns = 512;
 constexpr int kMaxStages = 5;
 constexpr int kStoreBox = 128;  // bytes of a row of a stored box
 
-template <int kTileN>
+// How CTAs share a tile.
+enum Share { kAlone, kPair, kSplit };
+
+template <int kTileN, Share kShare>
 struct ProductShape {
+  static constexpr int kTileRows = kShare == kPair ? 2 * kTileM : kTileM;
+  static constexpr int kWRows = kShare == kPair ? kTileN / 2 : kTileN;  // weight rows of a CTA
   static constexpr int kAccumulators = kTmemColumns / kTileN;
-  static constexpr int kStageBytes = (kTileM + kTileN) * kBlock;  // tokens, then weight rows
-  static constexpr int kStages = kTileN == 256 ? 3 : 5;
+  static constexpr int kStageBytes = (kTileM + kWRows) * kBlock;  // tokens, then weight rows
+  static constexpr int kStages = kShare == kPair ? 4 : kTileN == 256 ? 3 : 5;
   static constexpr int kRing = kStages * kStageBytes;
   static constexpr int kHeld = kTileN / 128;  // boxes of 32 rows a warp's staging holds
   static constexpr int kWarpStaging = kHeld * 32 * kStoreBox;
@@ -335,17 +348,69 @@ __device__ __forceinline__ bool elected() {
   return one != 0;
 }
 
-__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y,
-                                         unsigned long long* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
-      : "memory");
+// Of a pair's barriers that count for both CTAs, the one of rank 0.
+template <bool kTwo>
+__device__ __forceinline__ uint32_t leader_bar(unsigned long long* bar) {
+  uint32_t addr = smem_u32(bar);
+  if constexpr (kTwo) asm volatile("mapa.shared::cluster.u32 %0, %0, 0;" : "+r"(addr));
+  return addr;
 }
 
-__device__ __forceinline__ void mbar_arrive(unsigned long long* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+// Copies a box into this CTA's memory; its bytes are counted at `bar`.
+template <bool kTwo>
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y,
+                                         uint32_t bar) {
+  if constexpr (kTwo)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Arrives, at this CTA's barrier or at both CTAs', when the MMAs issued so far
+// are done.
+template <bool kTwo>
+__device__ __forceinline__ void commit_to(unsigned long long* bar) {
+  if constexpr (kTwo)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
+        ".b64 [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    mma_commit(bar);
+}
+
+template <bool kTwo>
+__device__ __forceinline__ void take_tmem(uint32_t* slot, uint32_t cols) {
+  if constexpr (kTwo) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(slot)),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc(slot, cols);
+  }
+}
+template <bool kTwo>
+__device__ __forceinline__ void give_tmem(uint32_t base, uint32_t cols) {
+  if constexpr (kTwo)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols)
+                 : "memory");
+  else
+    tmem_dealloc(base, cols);
 }
 
 // Operand rows of 128 bytes, written by TMA in its 128-byte swizzle: 8-row
@@ -354,14 +419,23 @@ __device__ __forceinline__ uint64_t swizzled_desc(const void* p) {
   return make_smem_desc(p, 16, 1024) | (2ull << 61);
 }
 
+template <bool kTwo>
 __device__ __forceinline__ void mma_f8(uint32_t tmem, uint64_t adesc, uint64_t bdesc,
                                        uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+  if constexpr (kTwo)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 // Starts reading 32 columns of this warp's 32 tensor-memory lanes; the values
@@ -436,6 +510,7 @@ struct ProductTile {
 
 // Row tiles of all experts before each, in shared memory; the whole CTA.  Sums
 // stop at P.row_tiles, which offsets that rise do not reach.
+template <int kTileRows>
 __device__ __forceinline__ void build_tiles(const ProductArgs& P, ProductShared& S) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int carry = 0;
@@ -444,7 +519,7 @@ __device__ __forceinline__ void build_tiles(const ProductArgs& P, ProductShared&
     int tiles = 0;
     if (e < P.experts) {
       const int c = group_start(P, e + 1) - group_start(P, e);
-      tiles = c > 0 ? min((c + kTileM - 1) / kTileM, P.row_tiles) : 0;
+      tiles = c > 0 ? min((c + kTileRows - 1) / kTileRows, P.row_tiles) : 0;
     }
     int incl = tiles;
 #pragma unroll
@@ -466,7 +541,7 @@ __device__ __forceinline__ void build_tiles(const ProductArgs& P, ProductShared&
 }
 
 // Tile t of the walk: experts in order, and in an expert its row tiles first.
-template <int kTileN>
+template <int kTileN, int kTileRows>
 __device__ __forceinline__ ProductTile tile_at(const ProductArgs& P, const ProductShared& S,
                                                int t) {
   int lo = 0, hi = P.experts - 1;
@@ -480,8 +555,8 @@ __device__ __forceinline__ ProductTile tile_at(const ProductArgs& P, const Produ
   const int start = group_start(P, lo), end = group_start(P, lo + 1);
   ProductTile T;
   T.expert = lo;
-  T.row0 = start + at % m_tiles * kTileM;
-  T.rows = end - T.row0 < kTileM ? end - T.row0 : kTileM;
+  T.row0 = start + at % m_tiles * kTileRows;
+  T.rows = end - T.row0 < kTileRows ? end - T.row0 : kTileRows;
   T.n0 = at / m_tiles * kTileN;
   return T;
 }
@@ -597,14 +672,16 @@ __device__ __forceinline__ void store_rows(const ProductArgs& P, char* staging, 
   }
 }
 
-template <typename T, int kTileN, bool kSplit>
+template <typename T, int kTileN, Share kShare>
 __global__ void __launch_bounds__(kProductThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap a_map,
                    const __grid_constant__ CUtensorMap a_part_map,
                    const __grid_constant__ CUtensorMap w_map,
                    const __grid_constant__ CUtensorMap out_map,
                    const __grid_constant__ ProductArgs P) {
-  using Shape = ProductShape<kTileN>;
+  using Shape = ProductShape<kTileN, kShare>;
+  constexpr bool kTwo = kShare == kPair;
+  constexpr int kTileRows = Shape::kTileRows;
   constexpr int kStages = Shape::kStages, kStageBytes = Shape::kStageBytes;
   constexpr int kSums = Shape::kSums, kAccumulators = Shape::kAccumulators;
   constexpr int kBlocksN = Shape::kBlocksN;
@@ -622,29 +699,37 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       mbar_init(&S.done[i], 1 + kScaleWarps);
     }
     for (int i = 0; i < kAccumulators; ++i)
-      mbar_init(&S.taken[i], kEpilogueWarps);
+      mbar_init(&S.taken[i], kTwo ? 2 * kEpilogueWarps : kEpilogueWarps);
     mbar_init(&S.drain, 1);
     mbar_init(&S.stuck, 1);
     S.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 2) tmem_alloc(&S.tmem, kTmemColumns);
+  if (warp == 2) take_tmem<kTwo>(&S.tmem, kTmemColumns);
   // so far nothing that the kernel before this one writes has been read
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  build_tiles(P, S);
+  build_tiles<kTileRows>(P, S);
   fence_before_sync();
   __syncthreads();
+  if constexpr (kTwo) cluster_sync();  // the other CTA's barriers are there
   fence_after_sync();
   const uint32_t tmem = S.tmem;
   const int tiles = S.tile0[P.experts] * P.n_tiles;
-  const int split = kSplit ? static_cast<int>(cluster_size()) : 1;
-  const int part = kSplit ? static_cast<int>(cluster_rank()) : 0;
-  // tiles first, first + stride, ...; with kSplit a cluster has one
-  const int first = static_cast<int>(blockIdx.x) / split;
-  const int stride = kSplit ? tiles + 1 : static_cast<int>(gridDim.x);
+  const int split = kShare == kSplit ? static_cast<int>(cluster_size()) : 1;
+  const int part = kShare == kSplit ? static_cast<int>(cluster_rank()) : 0;
+  const int rank = kTwo ? static_cast<int>(cluster_rank()) : 0;
+  // a cluster's tiles are first, first + stride, ...; with kSplit it has one
+  const int first = static_cast<int>(blockIdx.x) / (kTwo ? 2 : split);
+  const int stride = kShare == kSplit ? tiles + 1 : static_cast<int>(gridDim.x) / (kTwo ? 2 : 1);
   const int b0 = static_cast<int>(static_cast<int64_t>(P.kb) * part / split);
   const int b1 = static_cast<int>(static_cast<int64_t>(P.kb) * (part + 1) / split);
+  // rows of tokens that the CTA of rank r copies for a tile of `rows` rows
+  const auto copied = [](int rows, int r) {
+    const int mine = (rows - r * kTileM + kRowBox - 1) / kRowBox * kRowBox;
+    return mine <= 0 ? 0 : mine >= kTileM ? kTileM : mine;
+  };
+
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
@@ -652,9 +737,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       uint32_t parity = 0;
       bool ok = true;
       for (int t = first; t < tiles && ok; t += stride) {
-        const ProductTile tile = tile_at<kTileN>(P, S, t);
-        const int mine = (tile.rows + kRowBox - 1) / kRowBox * kRowBox;  // rows to copy
-        const int w0 = tile.expert * P.n + tile.n0;
+        const ProductTile tile = tile_at<kTileN, kTileRows>(P, S, t);
+        const int mine = copied(tile.rows, rank);
+        const int row0 = tile.row0 + rank * kTileM;
+        const int w0 = tile.expert * P.n + tile.n0 + rank * Shape::kWRows;
+        const int bytes = (kTwo ? copied(tile.rows, 0) + copied(tile.rows, 1) + kTileN
+                                : mine + kTileN) * kBlock;
         for (int b = b0; b < b1; ++b) {
           if (!role_wait(&S.done[stage], parity ^ 1, dead)) {
             ok = false;
@@ -663,25 +751,26 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           char* a = ring + stage * kStageBytes;
           char* w = a + kTileM * kBlock;
           if (elected()) {
-            unsigned long long* bar = &S.full[stage];
-            mbar_expect_tx(bar, (mine + kTileN) * kBlock);
-            tma_load(w, &w_map, b * kBlock, w0, bar);
+            if (rank == 0) mbar_expect_tx(&S.full[stage], bytes);
+            const uint32_t bar = leader_bar<kTwo>(&S.full[stage]);
+            tma_load<kTwo>(w, &w_map, b * kBlock, w0, bar);
             if (mine == kTileM)
-              tma_load(a, &a_map, b * kBlock, tile.row0, bar);
+              tma_load<kTwo>(a, &a_map, b * kBlock, row0, bar);
             else
               for (int r = 0; r < mine; r += kRowBox)
-                tma_load(a + r * kBlock, &a_part_map, b * kBlock, tile.row0 + r, bar);
+                tma_load<kTwo>(a + r * kBlock, &a_part_map, b * kBlock, row0 + r, bar);
           }
           __syncwarp();
           ++issued;
           if (++stage == kStages) stage = 0, parity ^= 1;
         }
       }
-      // Whoever has given up: the copies in flight land before the CTA ends.
-      for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+      // Whoever has given up: the copies in flight land before the CTA ends (a pair's are counted
+      // at rank 0, and the cluster's last barrier follows).
+      for (int i = issued > kStages ? issued - kStages : 0; rank == 0 && i < issued; ++i)
         mbar_wait(&S.full[i % kStages], (i / kStages) & 1);
-    } else if (warp == 1) {
-      const uint32_t idesc = make_idesc(0, kTileM, kTileN);  // e4m3 x e4m3 -> fp32
+    } else if (warp == 1 && rank == 0) {  // a pair's MMAs are issued by rank 0
+      const uint32_t idesc = make_idesc(0, kTileRows, kTileN);  // e4m3 x e4m3 -> fp32
       const uint64_t a_desc = swizzled_desc(ring), w_desc = swizzled_desc(ring + kTileM * kBlock);
       int stage = 0, slot = 0;
       uint32_t parity = 0, tparity = 0;
@@ -699,8 +788,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           if (elected()) {
 #pragma unroll
             for (int i = 0; i < kBlock / 32; ++i)  // 32 columns are 32 bytes: 2 in the address
-              mma_f8(tmem + slot * kTileN, a_desc + at + i * 2, w_desc + at + i * 2, idesc, i > 0);
-            mma_commit(&S.done[stage]);
+              mma_f8<kTwo>(tmem + slot * kTileN, a_desc + at + i * 2, w_desc + at + i * 2, idesc, i > 0);
+            commit_to<kTwo>(&S.done[stage]);
           }
           __syncwarp();
           if (++stage == kStages) stage = 0, parity ^= 1;
@@ -708,10 +797,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
       }
       // Whoever has given up: the MMAs are done before tensor memory is freed.
-      if (elected()) mma_commit(&S.drain);
+      if (elected()) commit_to<kTwo>(&S.drain);
       __syncwarp();
       mbar_wait(&S.drain, 0);
-    } else {
+    } else if (warp >= 2) {
       // A block's scales replace those of the block kScaleRing earlier.  Those have been read
       // when the MMAs of the block kAccumulators earlier are done, for they took its accumulator.
       constexpr int kAhead = 4;  // blocks whose scales are on their way
@@ -720,12 +809,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       bool ok = true;
       const int r0 = (warp - 2) * 64 + lane, r1 = r0 + 32;  // this lane's two tokens
       for (int t = first; t < tiles && ok; t += stride) {
-        const ProductTile tile = tile_at<kTileN>(P, S, t);
-        const float* a0 = P.a_scale + static_cast<int64_t>(tile.row0 + r0) * P.kb;
+        const ProductTile tile = tile_at<kTileN, kTileRows>(P, S, t);
+        const int rows = tile.rows - rank * kTileM;
+        const float* a0 =
+            P.a_scale + (static_cast<int64_t>(tile.row0) + rank * kTileM + r0) * P.kb;
         const float* a1 = a0 + static_cast<int64_t>(32) * P.kb;
         const int wb = tile.n0 / kBlock;
         const float* w0 = P.w_scale + (static_cast<int64_t>(tile.expert) * P.nb + wb) * P.kb;
-        const bool on0 = r0 < tile.rows, on1 = r1 < tile.rows, two = kBlocksN == 2 && wb + 1 < P.nb;
+        const bool on0 = r0 < rows, on1 = r1 < rows, two = kBlocksN == 2 && wb + 1 < P.nb;
         const auto at = [&](const float* p, int b, bool on) {
           return on && b < b1 ? __ldg(p + b) : 0.f;
         };
@@ -758,7 +849,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
               S.scale[slot][h][r1] = sa1[i] * sw[i][h];
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&S.done[stage]);
+            if (lane == 0) arrive_at(smem_u32(&S.done[stage]));
             slot = (slot + 1) % kScaleRing;
             load(i, b + kAhead);
             if (++stage == kStages) stage = 0;
@@ -789,9 +880,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     if (TBE_TEST_STUCK_WAIT && first < tiles)
       ok = role_wait(&S.stuck, 0, dead, TBE_TEST_STUCK_WAIT);
     for (int t = first; t < tiles && ok; t += stride) {
-      const ProductTile tile = tile_at<kTileN>(P, S, t);
-      const int row0 = tile.row0 + quarter * 32;
-      const int rows = tile.rows - quarter * 32;  // of this warp; none or less: nothing to do
+      const ProductTile tile = tile_at<kTileN, kTileRows>(P, S, t);
+      const int row0 = tile.row0 + rank * kTileM + quarter * 32;
+      const int rows = tile.row0 + tile.rows - row0;  // of this warp; none or less: nothing to do
       const int col0 = tile.n0 + half * kSums;
       const bool on = rows > 0 && col0 < P.n;
       uint64_t acc[kSums / 2];
@@ -828,7 +919,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         // the accumulator is handed back before its last columns are added
         fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.taken[slot]);
+        if (lane == 0) arrive_at(leader_bar<kTwo>(&S.taken[slot]));
         if (on) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
@@ -839,7 +930,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         if (++stage == kStages) stage = 0, parity ^= 1;
         ++count;
       }
-      if constexpr (kSplit) {
+      if constexpr (kShare == kSplit) {
         if (on && ok) {
           float* join = reinterpret_cast<float*>(ring) + (quarter * 32 + lane) * Shape::kJoinStride +
                         half * kSums;
@@ -859,10 +950,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncwarp();
-  if constexpr (kSplit) {
+  if constexpr (kShare == kSplit) {
     cluster_sync();
     if (first < tiles && !S.dead) {
-      const ProductTile tile = tile_at<kTileN>(P, S, first);
+      const ProductTile tile = tile_at<kTileN, kTileRows>(P, S, first);
       const int cols = kTileN / split, c0 = part * cols;
       const uint32_t base = smem_u32(ring);
       T* out = static_cast<T*>(P.out);
@@ -878,8 +969,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   }
   fence_before_sync();
   __syncthreads();
+  if constexpr (kTwo) cluster_sync();  // the other CTA uses this one's barriers and memory no more
   fence_after_sync();
-  if (warp == 2) tmem_dealloc(tmem, kTmemColumns);
+  if (warp == 2) give_tmem<kTwo>(tmem, kTmemColumns);
   if (threadIdx.x == 0 && S.dead && P.status) atomicOr(P.status, TBE_ERR_TIMEOUT);
 }
 
@@ -1041,56 +1133,66 @@ extern "C" tbe_status tbe_expert_product(const uint8_t* a, int64_t a_stride, con
     return TBE_ECUDA;
   CUtensorMap out_map = a_map;  // not used unless P.tma_out
   if (P.tma_out && !make_map(&out_map, out, ob, rows, n, out_stride * ob, 32)) return TBE_ECUDA;
-  const auto launch = [&](auto t, auto tile_n, auto split_tag, int split) -> tbe_status {
+  const auto launch = [&](auto t, auto tile_n, auto share, int cluster) -> tbe_status {
     using T = decltype(t);
     constexpr int kTileN = decltype(tile_n)::value;
-    constexpr bool kSplit = decltype(split_tag)::value;
+    constexpr Share kShare = decltype(share)::value;
+    using Shape = ProductShape<kTileN, kShare>;
     P.n_tiles = static_cast<int>((n + kTileN - 1) / kTileN);
     CUtensorMap w_map;
-    if (!make_map(&w_map, w, 1, static_cast<int64_t>(experts) * n, k, k, kTileN)) return TBE_ECUDA;
-    const auto kernel = product_kernel<T, kTileN, kSplit>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             ProductShape<kTileN>::kSmem) !=
+    if (!make_map(&w_map, w, 1, static_cast<int64_t>(experts) * n, k, k, Shape::kWRows))
+      return TBE_ECUDA;
+    const auto kernel = product_kernel<T, kTileN, kShare>;
+    constexpr int kSmem = Shape::kSmem;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
         cudaSuccess)
       return TBE_ECUDA;
     // tiles, at most (every expert's last one may be a part)
-    P.row_tiles = static_cast<int>(rows / kTileM + (experts < rows ? experts : rows));
+    P.row_tiles =
+        static_cast<int>(rows / Shape::kTileRows + (experts < rows ? experts : rows));
     const int64_t most = static_cast<int64_t>(P.row_tiles) * P.n_tiles;
     if (most > INT32_MAX / 8) return TBE_EUNSUPPORTED;  // the kernel counts tiles in 32 bits
+    const int64_t room = sms / cluster;
+    const int64_t clusters = kShare == kSplit || most < room ? most : room;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(kSplit ? most * split : most < sms ? most : sms));
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * cluster));
     cfg.blockDim = dim3(kProductThreads);
-    cfg.dynamicSmemBytes = ProductShape<kTileN>::kSmem;
+    cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
     // its start may overlap the end of the kernel before it (griddepcontrol.wait)
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(split);
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = kSplit ? 2 : 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, kernel, a_map, a_part_map, w_map, out_map, P) != cudaSuccess)
       return TBE_ECUDA;
     return launched();
   };
   using Narrow = std::integral_constant<int, 128>;
   using Wide = std::integral_constant<int, 256>;
+  using Alone = std::integral_constant<Share, kAlone>;
+  using Pair = std::integral_constant<Share, kPair>;
+  using Split = std::integral_constant<Share, kSplit>;
   return for_dtype(out_dtype, [&](auto t) {
     const int64_t tiles =
         (rows / kTileM + (experts < rows ? experts : rows)) * ((n + 127) / 128);
     int split = 1;
     while (split < 8 && tiles * split * 2 <= sms && P.kb >= split * 4) split *= 2;
-    if (split > 1) return launch(t, Narrow{}, std::true_type{}, split);
-    // Rounds of tiles over the multiprocessors, times a tile's time: measured on 65536 rows of
-    // 16 experts and 4096 columns, a block of k takes 0.42 us of 256 columns and 0.27 of 128,
-    // and a tile's start and end 1.55 and 0.76 us (k = 2048: 444 us with 256 columns, 501 with
-    // 128; 5000 rows, 8 experts, 1000 x 1008: 21.6 and 18.2).
-    const int64_t m = rows / kTileM + (experts < rows ? experts : rows) / 2;
-    const auto rounds = [&](int64_t cols) { return (m * ((n + cols - 1) / cols) + sms - 1) / sms; };
-    if (rounds(128) * (P.kb * 27 + 76) < rounds(256) * (P.kb * 42 + 155))
-      return launch(t, Narrow{}, std::false_type{}, 1);
-    return launch(t, Wide{}, std::false_type{}, 1);
+    if (split > 1) return launch(t, Narrow{}, Split{}, split);
+    // Rounds of tiles over the multiprocessors (a pair takes two), times a tile's time: measured
+    // on 65536 rows of 16 experts and 4096 columns, a block of k takes a pair 0.40 us and a lone
+    // CTA 0.27, and a tile's start and end 1.43 and 0.76 us (k = 2048: 421 us in pairs, 501 alone;
+    // 5000 rows, 8 experts, 1000 x 1008: 21.6 and 18.2).
+    const int64_t parts = (experts < rows ? experts : rows) / 2;  // an expert's last tile, on average
+    const auto rounds = [](int64_t tiles, int64_t at_once) { return (tiles + at_once - 1) / at_once; };
+    const int64_t alone = rounds((rows / 128 + parts) * ((n + 127) / 128), sms);
+    const int64_t paired = rounds((rows / 256 + parts) * ((n + 255) / 256), sms / 2);
+    if (alone * (P.kb * 27 + 76) < paired * (P.kb * 40 + 143))
+      return launch(t, Narrow{}, Alone{}, 1);
+    return launch(t, Wide{}, Pair{}, 2);
   });
 }

@@ -168,6 +168,14 @@ def test_product_types_strides_and_unused_rows(dtype, n):
     check_product([0, 0, 0], n, 64, dtype, rest=50)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,k", [(1000, 400), (1001, 128), (2048, 1200)])
+def test_product_of_many_rows(n, k, dtype):
+    # enough tiles for pairs of CTAs; experts of one row, of a part of a tile, of none
+    check_product([9000, 0, 1, 257, 129, 200, 10613], n, k, dtype, rest=70, seed=k)
+    check_product([20000], n, k, dtype, out_pad=8)
+
+
 @pytest.mark.parametrize("rows,n,k", [(1, 4096, 7168), (16, 512, 4096), (2000, 384, 2048)])
 def test_product_long_sums(rows, n, k):
     check_product([rows], n, k, torch.bfloat16)

@@ -23,7 +23,7 @@ def stuck_lib(tmp_path_factory):
 
 
 @pytest.mark.parametrize("rows,n,k,groups", [
-    (5000, 1024, 512, 4), (3000, 512, 256, 8), (3, 256, 1024, 2)])  # both tile widths, and a split
+    (20000, 1024, 512, 4), (3000, 512, 256, 8), (3, 256, 1024, 2)])  # CTAs in pairs, alone, split
 def test_product_wait_runs_out_and_reports(stuck_lib, monkeypatch, rows, n, k, groups):
     g = torch.Generator(device="cuda")
     g.manual_seed(1)
