@@ -604,32 +604,42 @@ __device__ __forceinline__ uint4 rounded(const uint64_t (&acc)[kPairs], int c) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Stores a warp's 32 whole rows by TMA, boxes of 32 rows x 128 bytes: the copies run
-// while the warp goes on to the next tile.  (Stores from registers held the tile
-// up: 65536 x 4096 x 1024, 305 us instead of 264.)  The boxes stand in the 128-byte
-// swizzle, so that the lanes' writes spread over the banks; columns from n on are
-// clipped.
+// Part `i` (16 bytes) of row r of a box in the staging buffer: the 128-byte swizzle of
+// TMA, in which the lanes' writes (a row each) spread over the banks.
+__device__ __forceinline__ uint4* staged(char* staging, int box, int r, int i) {
+  return reinterpret_cast<uint4*>(staging + (box * 32 + r) * kStoreBox + ((i ^ (r & 7)) << 4));
+}
+
+// Puts columns c0 .. of the warp's sums into the staging buffer, kHeld boxes of 32
+// rows x 128 bytes.
+template <typename T, int kSums, int kHeld>
+__device__ __forceinline__ void stage(char* staging, int c0, const uint64_t (&acc)[kSums / 2]) {
+  constexpr int kCols = kStoreBox / static_cast<int>(sizeof(T));
+  constexpr int kPart = 16 / static_cast<int>(sizeof(T));
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c0 + h * kCols < kSums)
+        *staged(staging, h, lane, i) = rounded<T>(acc, c0 + h * kCols + i * kPart);
+}
+
+// Stores a warp's 32 whole rows by TMA: the copies run while the warp goes on to the next
+// tile.  (Stores from registers held the tile up: 65536 x 4096 x 1024, 305 us instead
+// of 264.)  Columns from n on are clipped.
 template <typename T, int kSums, int kHeld>
 __device__ __forceinline__ void store_boxes(const ProductArgs& P, const CUtensorMap* map,
                                             char* staging, int row0, int col0,
                                             const uint64_t (&acc)[kSums / 2]) {
   constexpr int kCols = kStoreBox / static_cast<int>(sizeof(T));
-  constexpr int kPart = 16 / static_cast<int>(sizeof(T));
-  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int c0 = 0; c0 < kSums; c0 += kHeld * kCols) {
     staging_free();
-#pragma unroll
-    for (int h = 0; h < kHeld; ++h)
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c0 + h * kCols < kSums)
-          *reinterpret_cast<uint4*>(staging + h * 32 * kStoreBox + lane * kStoreBox +
-                                    ((i ^ (lane & 7)) << 4)) =
-              rounded<T>(acc, c0 + h * kCols + i * kPart);
+    stage<T, kSums, kHeld>(staging, c0, acc);
     fence_proxy_async();
     __syncwarp();
-    if (lane == 0) {
+    if ((threadIdx.x & 31) == 0) {
 #pragma unroll
       for (int h = 0; h < kHeld; ++h)
         if (c0 + h * kCols < kSums && col0 + c0 + h * kCols < P.n)
@@ -643,37 +653,55 @@ __device__ __forceinline__ void store_boxes(const ProductArgs& P, const CUtensor
   }
 }
 
-// Stores up to 32 rows, of any alignment, 64 bytes of a row at a time through the
-// staging buffer.
-template <typename T, int kSums>
+// Stores up to 32 rows of any alignment: 16-byte parts on the boundaries of the row of
+// out, each cut out of the two staged parts it lies in, and the rows' ends element by
+// element.  (65536 rows, 16 experts, 4095 x 2048 bf16: 866 us all element by element.)
+template <typename T, int kSums, int kHeld>
 __device__ __forceinline__ void store_rows(const ProductArgs& P, char* staging, int row0, int rows,
                                            int col0, const uint64_t (&acc)[kSums / 2]) {
-  constexpr int kCols = 64 / static_cast<int>(sizeof(T));
-  constexpr int kPart = 16 / static_cast<int>(sizeof(T));
+  constexpr int kSize = static_cast<int>(sizeof(T));
+  constexpr int kCols = kStoreBox / kSize;
+  constexpr int kParts = kHeld * kStoreBox / 16;  // of a row of the buffer
+  constexpr int kEnd = 16 / kSize;                // elements of an end, at most
   const int lane = threadIdx.x & 31;
   staging_free();
 #pragma unroll
-  for (int c0 = 0; c0 < kSums; c0 += kCols) {
+  for (int c0 = 0; c0 < kSums; c0 += kHeld * kCols) {
     if (col0 + c0 >= P.n) break;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<uint4*>(staging + lane * 80 + i * 16) = rounded<T>(acc, c0 + i * kPart);
+    stage<T, kSums, kHeld>(staging, c0, acc);
     __syncwarp();
-    const int cols = P.n - col0 - c0 < kCols ? P.n - col0 - c0 : kCols;
-    T* dst = static_cast<T*>(P.out) + static_cast<int64_t>(row0) * P.out_stride + col0 + c0;
-    if (P.tma_out) {  // whole 16-byte parts, on 16-byte boundaries
-#pragma unroll
-      for (int r = lane / 4; r < 32; r += 8)
-        if (r < rows && lane % 4 * kPart < cols)
-          *reinterpret_cast<uint4*>(dst + r * P.out_stride + lane % 4 * kPart) =
-              *reinterpret_cast<const uint4*>(staging + r * 80 + lane % 4 * 16);
-    } else {
-      for (int i = lane; i < rows * kCols; i += 32) {
-        const int r = i / kCols, c = i % kCols;
-        if (c < cols)
-          dst[r * P.out_stride + c] = *reinterpret_cast<const T*>(staging + r * 80 + c * sizeof(T));
-      }
+    int cols = P.n - col0 - c0 < kSums - c0 ? P.n - col0 - c0 : kSums - c0;
+    const int bytes = (cols < kHeld * kCols ? cols : kHeld * kCols) * kSize;
+    char* to = reinterpret_cast<char*>(static_cast<T*>(P.out) +
+                                       static_cast<int64_t>(row0) * P.out_stride + col0 + c0);
+    const int64_t pitch = P.out_stride * kSize;
+    // bytes from a row's start to its first boundary
+    const auto head = [](const char* row) {
+      return static_cast<int>(-reinterpret_cast<uintptr_t>(row) & 15);
+    };
+#pragma unroll 4
+    for (int i = lane; i < rows * kParts; i += 32) {
+      const int r = i / kParts;
+      char* row = to + r * pitch;
+      const int at = head(row) + i % kParts * 16;  // counted in the row of the buffer
+      if (at + 16 > bytes) continue;
+      const int k = at >> 4, shift = at & 15;
+      uint4 v = *staged(staging, k >> 3, r, k & 7);
+      if (shift) v = cut(v, *staged(staging, (k + 1) >> 3, r, (k + 1) & 7), shift);
+      *reinterpret_cast<uint4*>(row + at) = v;
     }
+    if (!P.tma_out)
+      for (int i = lane; i < rows * 2 * kEnd; i += 32) {
+        const int r = i / (2 * kEnd), e = i % (2 * kEnd);
+        char* row = to + r * pitch;
+        const int first = head(row) < bytes ? head(row) : bytes;
+        const int last = first + (bytes - first) / 16 * 16;
+        const int at = e < kEnd ? e * kSize : last + (e - kEnd) * kSize;
+        if (at < (e < kEnd ? first : bytes))
+          *reinterpret_cast<T*>(row + at) = *reinterpret_cast<const T*>(
+              reinterpret_cast<const char*>(staged(staging, at >> 7, r, (at >> 4) & 7)) +
+              (at & 15));
+      }
     __syncwarp();
   }
 }
@@ -950,7 +978,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         if (rows >= 32 && P.tma_out)
           store_boxes<T, kSums, Shape::kHeld>(P, &out_map, mine, row0, col0, acc);
         else
-          store_rows<T, kSums>(P, mine, row0, rows < 32 ? rows : 32, col0, acc);
+          store_rows<T, kSums, Shape::kHeld>(P, mine, row0, rows < 32 ? rows : 32, col0, acc);
       }
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");

@@ -105,26 +105,27 @@ __device__ __forceinline__ Span inner_span(const T* to, int width) {
   return {lo, lo + ((width - 2 * kVec<T> - lo) / kVec<T> + 1) * kVec<T>};
 }
 
+// The 16 bytes that begin `bytes` (an even number) into the 32 of a, b.
+__device__ __forceinline__ uint4 cut(uint4 a, uint4 b, int bytes) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) w[i] = bytes & 8 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = bytes & 4 ? w[i + 1] : w[i];
+  const int bits = (bytes & 3) * 8;
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
 // The vector at p, cut out of the two aligned vectors it lies in.
 template <typename T, bool kAligned>
 __device__ __forceinline__ Pack<T, kVec<T>> load_vec(const T* __restrict__ p) {
   if constexpr (kAligned) {
     return *reinterpret_cast<const Pack<T, kVec<T>>*>(p);
   } else {
-    const int shift = lead<T>(p), bytes = shift * static_cast<int>(sizeof(T));
+    const int shift = lead<T>(p);
     const uint4* q = reinterpret_cast<const uint4*>(p - shift);
-    const uint4 a = q[0], b = q[shift ? 1 : 0];
-    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = bytes & 8 ? w[i + 2] : w[i];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = bytes & 4 ? w[i + 1] : w[i];
-    const int bits = (bytes & 3) * 8;
-    uint4 o;
-    o.x = __funnelshift_r(w[0], w[1], bits);
-    o.y = __funnelshift_r(w[1], w[2], bits);
-    o.z = __funnelshift_r(w[2], w[3], bits);
-    o.w = __funnelshift_r(w[3], w[4], bits);
+    const uint4 o = cut(q[0], q[shift ? 1 : 0], shift * static_cast<int>(sizeof(T)));
     return *reinterpret_cast<const Pack<T, kVec<T>>*>(&o);
   }
 }
