@@ -58,11 +58,12 @@ def _ok(call, code):
 # The calls below take microseconds on the GPU, so their checks are written to
 # take few on the host: no torch.cuda.current_stream() object (2.8 us), no check
 # of what was just allocated.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream_of(stream, t):
     """The cudaStream_t a call on t's device runs on."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
-    return stream.cuda_stream
+    return _raw_stream(t.get_device()) if stream is None else stream.cuda_stream
 
 
 def _empty(stream, shape, dtype, like):

@@ -105,6 +105,19 @@ def test_sort_of_more_assignments_than_any_split_holds():
     assert torch.equal(position.reshape(-1).long(), back)
 
 
+def test_sort_of_many_assignments_in_a_graph():
+    ids = make_ids(90_000, 3, 40, "drop", torch.int64, seed=1)
+    o, s, p = tbe.tbe_expert_sort(ids, 40)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tbe.tbe_expert_sort(ids, 40, offsets=o, source=s, position=p)
+    ids.copy_(make_ids(90_000, 3, 40, "drop", torch.int64, seed=2))
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    check_plan(ids, 40, (o, s, p))
+
+
 def rows_of(tokens, width, dtype, seed, layout):
     """Rows in several layouts: dense, with a row stride, or off every 16-byte boundary."""
     g = gen(seed)
@@ -189,6 +202,27 @@ def test_combine_backward(tokens, k, experts, width, layout):
             terms = torch.zeros_like(ref)
             ref[src], terms[src] = prods.sum(1), prods.abs().sum(1)
             close(gw.reshape(-1), ref, terms, width, torch.float32)
+
+
+def test_one_gradient_without_the_other():
+    tokens, k, width = 70, 2, 40
+    ids = make_ids(tokens, k, 4, "drop", torch.int32, seed=3)
+    offsets, _, position = tbe.tbe_expert_sort(ids, 4)
+    g, y = (rows_of(n, width, torch.bfloat16, n, "dense") for n in (tokens, tokens * k))
+    w = torch.randn(tokens, k, generator=gen(4), device="cuda")
+    want_y, want_w = tbe.tbe_expert_combine_backward(g, y, offsets, position, w)
+    got_y, got_w = torch.full_like(want_y, 9.0), torch.full_like(want_w, 9.0)
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def call(y_, gy, gw):
+        return tbe._load().tbe_expert_combine_backward(
+            g.data_ptr(), y_, 4, tokens, k, width, width, width, offsets.data_ptr(), 4,
+            position.data_ptr(), w.data_ptr(), gy, width, gw, stream)
+
+    assert call(None, got_y.data_ptr(), None) == 0  # y is not read
+    assert call(y.data_ptr(), None, got_w.data_ptr()) == 0
+    assert call(None, None, None) == 0
+    assert torch.equal(got_y, want_y) and torch.equal(got_w, want_w)
 
 
 def test_gradients_against_differences():
