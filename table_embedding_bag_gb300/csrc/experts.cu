@@ -718,8 +718,18 @@ extern "C" tbe_status tbe_expert_dispatch(const void* x, int32_t dtype, int64_t 
   if (experts < 1 || !check_plan(offsets, position) || !check_matrix(x, dtype, x_stride, width) ||
       !check_matrix(rows, dtype, rows_stride, width))
     return TBE_EINVAL;
-  const int b = dtype_bytes(dtype);
+  int b = dtype_bytes(dtype);
   const bool vec = vector_rows(x, b, x_stride, width) && vector_rows(rows, b, rows_stride, width);
+  // Rows are carried as they are, so 16-bit rows on 4-byte boundaries go as 4-byte elements: half
+  // as many at the rows' ends (93576 x 20 fp16, eight experts each: 16.8 us instead of 29.2).
+  if (!vec && b == 2 && width % 2 == 0 && x_stride % 2 == 0 && rows_stride % 2 == 0 &&
+      aligned_to(x, 4) && aligned_to(rows, 4)) {
+    dtype = TBE_DT_F32;
+    b = 4;
+    width /= 2;
+    x_stride /= 2;
+    rows_stride /= 2;
+  }
   return for_dtype(dtype, vec, [&](auto t, auto v) {
     using T = decltype(t);
     constexpr bool kAligned = decltype(v)::value;
