@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kSortWarps * 32)
 // several narrow tokens or one wide one.  Rows that do not begin on 16-byte
 // boundaries are moved in 16-byte vectors all the same (inner_span, load_vec).
 // 65536 tokens x 2048 bf16, four experts each: dispatch 202 us (6.6 TB/s), combine 197
-// (6.8), its gradient 356 (6.8); 4097 x 1001 fp16, three each: 10.4, 12.6 and 16.3 us.
+// (6.8), its gradient 356 (6.8); 4097 x 1001 fp16, three each: 10.4, 12.6 and 13.0 us.
 constexpr int kMoveThreads = 256;
 
 struct Group {
@@ -533,10 +533,10 @@ __global__ void __launch_bounds__(kMoveThreads)
     const Span s = inner_span<T, kAligned>(grad_y ? gy : yr, width);
 #pragma unroll 2
     for (int e = s.lo + g.t * kVec<T>; e < s.hi; e += g.size * kVec<T>) {
-      const Pack<T, kVec<T>> gv = load_vec<T, kAligned>(go + e);
+      const Pack<T, kVec<T>> gv = load_vec<T, kAligned, true>(go + e);
       float d[kVec<T>], r[kVec<T>];
       if (grad_weights) {
-        const Pack<T, kVec<T>> yv = load_vec<T, kAligned>(yr + e);
+        const Pack<T, kVec<T>> yv = load_vec<T, kAligned, true>(yr + e);
         to_floats<T>(gv, d);
         to_floats<T>(yv, r);
 #pragma unroll
