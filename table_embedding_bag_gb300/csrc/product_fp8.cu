@@ -63,6 +63,23 @@ struct Eight {
       for (int u = 0; u < kVec<T>; ++u) f[i * kVec<T> + u] = x[u];
     }
   }
+  // The largest magnitude; passes over NaN.
+  __device__ __forceinline__ float amax() const {
+    if constexpr (sizeof(T) == 4) {
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8 / kVec<T>; ++i)
+#pragma unroll
+        for (int u = 0; u < kVec<T>; ++u) m = fmaxf(m, fabsf(to_f32(v[i].v[u])));
+      return m;
+    } else {  // two at a time, exactly
+      using T2 = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
+      const T2* p = reinterpret_cast<const T2*>(v);
+      const T2 m = __hmax2(__hmax2(__habs2(p[0]), __habs2(p[1])),
+                           __hmax2(__habs2(p[2]), __habs2(p[3])));
+      return fmaxf(fmaxf(to_f32(m.x), to_f32(m.y)), 0.f);
+    }
+  }
 };
 
 // Values col .. col + 7, zeros from `width` on.
@@ -133,10 +150,8 @@ __global__ void __launch_bounds__(256)
     const int col = b * kBlock + col_in;
     float in[8];
     next.floats(in);
+    float amax = next.amax();
     if (b0 + step < blocks) next = load8<T, kAligned>(row, col + step * kBlock, width);
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(in[i]));  // passes over NaN
 #pragma unroll
     for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const float s = block_scale(amax);
@@ -190,12 +205,7 @@ __global__ void __launch_bounds__(256)
   for (int i = 0; i < 8; ++i)
     in[i] = load8<T, kAligned>(src + i * 16 * k, col, row0 + i * 16 < n ? cols : 0);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float x[8];
-    in[i].floats(x);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) amax = fmaxf(amax, fabsf(x[u]));  // passes over NaN
-  }
+  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, in[i].amax());
 #pragma unroll
   for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = amax;
