@@ -287,6 +287,13 @@ struct ProductShape {
   static constexpr int kJoinStride = kTileN + 4;  // split sums meet in the ring: [128][..] floats
 };
 
+// Test-only builds (-DTBE_TEST_STUCK_DRAIN=polls): after the wait for the last MMAs another one, on
+// an mbarrier that nothing arrives on, so that the MMAs' warp reports a wait that ran out after
+// its work is done.  0 (every regular build): no such wait.
+#ifndef TBE_TEST_STUCK_DRAIN
+#define TBE_TEST_STUCK_DRAIN 0
+#endif
+
 struct ProductArgs {
   const float* a_scale;
   const float* w_scale;
@@ -812,7 +819,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       // Whoever has given up: the copies in flight land before the CTA ends (a pair's are counted
       // at rank 0, and the cluster's last barrier follows).
       for (int i = issued > kStages ? issued - kStages : 0; rank == 0 && i < issued; ++i)
-        mbar_wait(&S.full[i % kStages], (i / kStages) & 1);
+        if (!mbar_wait(&S.full[i % kStages], (i / kStages) & 1)) *dead = 1;
+      // Rank 0's MMAs arrive at rank 1's barriers too: rank 1 sees the last arrival before it ends.
+      // (It may wait for as long as rank 0 takes to give up, and then for the MMAs.)
+      if (rank == 1 && !mbar_wait(&S.drain, 0, 2 * kSpinLimit)) *dead = 1;
     } else if (warp == 1 && rank == 0) {  // a pair's MMAs are issued by rank 0
       const uint32_t idesc = make_idesc(0, kTileRows, kTileN);  // e4m3 x e4m3 -> fp32
       const uint64_t a_desc = swizzled_desc(ring), w_desc = swizzled_desc(ring + kTileM * kBlock);
@@ -843,7 +853,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       // Whoever has given up: the MMAs are done before tensor memory is freed.
       if (elected()) commit_to<kTwo>(&S.drain);
       __syncwarp();
-      mbar_wait(&S.drain, 0);
+      if (!mbar_wait(&S.drain, 0) ||
+          (TBE_TEST_STUCK_DRAIN && !mbar_wait(&S.stuck, 0, TBE_TEST_STUCK_DRAIN)))
+        *dead = 1;
     } else if (warp >= 2) {
       // A block's scales replace those of the block kScaleRing earlier.  Those have been read
       // when the MMAs of the block kAccumulators earlier are done, for they took its accumulator.
