@@ -293,6 +293,11 @@ struct ProductShape {
 #ifndef TBE_TEST_STUCK_DRAIN
 #define TBE_TEST_STUCK_DRAIN 0
 #endif
+// Likewise (-DTBE_TEST_STUCK_COPY=polls): the second CTA of a pair, when it has filled its ring
+// once, waits for such an mbarrier and gives up, while the first goes on.
+#ifndef TBE_TEST_STUCK_COPY
+#define TBE_TEST_STUCK_COPY 0
+#endif
 
 struct ProductArgs {
   const float* a_scale;
@@ -312,9 +317,11 @@ struct ProductShared {
   // free and the block's product stands in its accumulator, and the block's scales are there;
   // taken: the accumulator has been read
   unsigned long long full[kMaxStages], done[kMaxStages], taken[4], drain;
-  unsigned long long stuck;  // nothing arrives (TBE_TEST_STUCK_WAIT)
+  unsigned long long left;   // the pair's other CTA has told how many blocks it has copied
+  unsigned long long stuck;  // nothing arrives (TBE_TEST_STUCK_...)
   uint32_t tmem;
   int dead;
+  int other_copied;
   float scale[kScaleRing][2][kTileM];  // [block][128 columns of n][token]
   int warp_sum[kProductThreads / 32];
   int tile0[TBE_MAX_EXPERTS + 1];  // first row tile of each expert
@@ -396,6 +403,21 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int 
 
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Writes to a variable of the CTA `rank` of the cluster.
+__device__ __forceinline__ void store_to_cta(int* p, uint32_t rank, int v) {
+  uint32_t addr = smem_u32(p);
+  asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(addr) : "r"(rank));
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void arrive_at_cta(unsigned long long* bar, uint32_t rank) {
+  uint32_t addr = smem_u32(bar);
+  asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(addr) : "r"(rank));
+  arrive_at(addr);
+}
+__device__ __forceinline__ void fence_cluster() {
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
 
 // Arrives, at this CTA's barrier or at both CTAs', when the MMAs issued so far
@@ -752,6 +774,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     for (int i = 0; i < kAccumulators; ++i)
       mbar_init(&S.taken[i], kTwo ? 2 * kEpilogueWarps : kEpilogueWarps);
     mbar_init(&S.drain, 1);
+    mbar_init(&S.left, 1);
     mbar_init(&S.stuck, 1);
     S.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -784,10 +807,20 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
-      int stage = 0, issued = 0;
+      int stage = 0, issued = 0, most = INT32_MAX;
       uint32_t parity = 0;
       bool ok = true;
-      for (int t = first; t < tiles && ok; t += stride) {
+      // Tells the pair's other CTA how many blocks this one has copied, and whether it gave up.
+      const auto tell = [&] {
+        if (elected()) {
+          store_to_cta(&S.other_copied, rank ^ 1, issued);
+          if (!ok) store_to_cta(&S.dead, rank ^ 1, 1);
+          fence_cluster();
+          arrive_at_cta(&S.left, rank ^ 1);
+        }
+        __syncwarp();
+      };
+      for (int t = first; t < tiles && issued < most; t += stride) {
         const ProductTile tile = tile_at<kTileN, kTileRows>(P, S, t);
         const int mine = copied(tile.rows, rank);
         const int row0 = tile.row0 + rank * kTileM;
@@ -795,10 +828,23 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         const int bytes = (kTwo ? copied(tile.rows, 0) + copied(tile.rows, 1) + kTileN
                                 : mine + kTileN) * kBlock;
         for (int b = b0; b < b1; ++b) {
-          if (!role_wait(&S.done[stage], parity ^ 1, dead)) {
+          const bool stuck = TBE_TEST_STUCK_COPY && kTwo && rank == 1 && issued == kStages;
+          if (ok && !(stuck ? role_wait(&S.stuck, 0, dead, TBE_TEST_STUCK_COPY)
+                            : role_wait(&S.done[stage], parity ^ 1, dead))) {
             ok = false;
-            break;
+            most = issued;
+            // Both CTAs' copies of a block count at rank 0's barrier, which can only be waited for
+            // if both are issued.  So the CTA that has issued fewer issues the others' counterparts;
+            // their stages are free, or the other CTA would not have filled its own.
+            if constexpr (kTwo) {
+              tell();
+              if (__all_sync(0xffffffffu, mbar_wait(&S.left, 0, 2 * kSpinLimit))) {
+                fence_cluster();
+                most = max(issued, *static_cast<volatile int*>(&S.other_copied));
+              }
+            }
           }
+          if (issued >= most) break;
           char* a = ring + stage * kStageBytes;
           char* w = a + kTileM * kBlock;
           if (elected()) {
@@ -816,6 +862,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           if (++stage == kStages) stage = 0, parity ^= 1;
         }
       }
+      if (kTwo && ok) tell();
       // Whoever has given up: the copies in flight land before the CTA ends (a pair's are counted
       // at rank 0, and the cluster's last barrier follows).
       for (int i = issued > kStages ? issued - kStages : 0; rank == 0 && i < issued; ++i)
