@@ -93,7 +93,9 @@ tbe_status tbe_expert_combine_backward(const void* grad_out, const void* y, int3
  * in fp32, with 1/448 rounded to fp32, the division rounded to nearest and the
  * values rounded to nearest even (448 is the largest).
  * q [E, N, K]; scale fp32 [E, ceil(N / 128), ceil(K / 128)].  An infinity
- * gives its block an infinite scale; a NaN stays one NaN value. */
+ * gives its block an infinite scale; a NaN stays one NaN value.
+ * Errors: TBE_EINVAL, TBE_EUNSUPPORTED (type; N or K above 2^31 - 513, or 2^31
+ * blocks), TBE_ECUDA. */
 tbe_status tbe_quantize_weights(const void* w, int32_t dtype, int64_t experts, int64_t n,
                                 int64_t k, uint8_t* q, float* scale, void* stream);
 
@@ -114,7 +116,8 @@ tbe_status tbe_quantize_weights(const void* w, int32_t dtype, int64_t experts, i
  * lies before its start has no rows.
  * status: device int32 word, or NULL; a bounded device wait that gave up sets
  * TBE_ERR_TIMEOUT in it (the outputs are then incomplete).
- * Errors: TBE_EINVAL, TBE_EUNSUPPORTED, TBE_ECUDA. */
+ * Errors: TBE_EINVAL, TBE_EUNSUPPORTED (type; alignment; rows, K or E N above
+ * 2^31 - 513, E > TBE_MAX_EXPERTS, or too many tiles), TBE_ECUDA. */
 tbe_status tbe_expert_product(const uint8_t* a, int64_t a_stride, const float* a_scale,
                               const uint8_t* w, const float* w_scale, const int32_t* offsets,
                               int64_t rows, int64_t n, int64_t k, int32_t experts, void* out,

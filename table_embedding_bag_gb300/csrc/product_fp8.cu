@@ -16,6 +16,9 @@ namespace {
 constexpr int kBlock = TBE_SCALE_BLOCK;
 constexpr float kInvMax = 1.f / 448.f;  // one over the largest e4m3 value, rounded to fp32
 constexpr float kTinyScale = 0x1p-126f;
+// Rows and columns are counted in 32 bits, and a block or a tile that begins inside a matrix may
+// end past it.
+constexpr int64_t kMostRows = INT32_MAX - 512;
 
 __device__ __forceinline__ float block_scale(float amax) {
   return fmaxf(amax * kInvMax, kTinyScale);
@@ -1186,7 +1189,7 @@ extern "C" tbe_status tbe_quantize_weights(const void* w, int32_t dtype, int64_t
                                            void* stream) {
   if (experts < 0 || n < 0 || k < 0) return TBE_EINVAL;
   if (!dtype_bytes(dtype)) return TBE_EUNSUPPORTED;
-  if (n > INT32_MAX || k > INT32_MAX || experts > INT32_MAX) return TBE_EUNSUPPORTED;
+  if (n > kMostRows || k > kMostRows || experts > INT32_MAX) return TBE_EUNSUPPORTED;
   if (!experts || !n || !k) return TBE_OK;
   if (!w || !q || !scale || !aligned_to(w, dtype_bytes(dtype)) || !aligned_to(scale, 4))
     return TBE_EINVAL;
@@ -1212,8 +1215,8 @@ extern "C" tbe_status tbe_expert_product(const uint8_t* a, int64_t a_stride, con
                                          int64_t out_stride, int32_t* status, void* stream) {
   if (rows < 0 || n < 0 || k < 1 || experts < 1) return TBE_EINVAL;
   if (!dtype_bytes(out_dtype)) return TBE_EUNSUPPORTED;
-  if (rows > INT32_MAX || n > INT32_MAX || k > INT32_MAX || experts > TBE_MAX_EXPERTS ||
-      experts * n > INT32_MAX)
+  if (rows > kMostRows || n > kMostRows || k > kMostRows || experts > TBE_MAX_EXPERTS ||
+      experts * n > kMostRows)
     return TBE_EUNSUPPORTED;
   if (!rows || !n) return TBE_OK;
   if (!a || !a_scale || !w || !w_scale || !out || (!offsets && experts != 1) || a_stride < k ||
