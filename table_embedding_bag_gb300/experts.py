@@ -2,8 +2,10 @@
 and combine with their gradients, 8-bit quantising, and the experts' products.
 
 As in the rest of the package the functions only check and marshal their
-arguments.  Outputs that are not given are allocated on the stream the call
-runs on.  A matrix may have any row stride; its columns must be contiguous.
+arguments.  A call runs on the device of its tensors, which must all be on one,
+whichever device is current.  Outputs that are not given are allocated on the
+stream the call runs on.  A matrix may have any row stride; its columns must be
+contiguous.
 """
 from __future__ import annotations
 
@@ -41,12 +43,30 @@ def configure(lib):
 _lib_ = None
 
 
-def _lib():
+_current_device = torch._C._cuda_getDevice
+_on_device = torch.cuda.device
+
+
+def _lib(device):
+    """The library, whose calls launch on the current device, for a call on `device`."""
     global _lib_
     if _lib_ is None:
         import table_embedding_bag_gb300 as tbe
         _lib_ = tbe._load()
-    return _lib_
+    return _lib_ if device == _current_device() else _OnDevice(_lib_, device)
+
+
+class _OnDevice:
+    """The library with `device` made current during each call."""
+
+    def __init__(self, lib, device):
+        self.lib, self.device = lib, device
+
+    def __getattr__(self, name):
+        def call(*args):
+            with _on_device(self.device):
+                return getattr(self.lib, name)(*args)
+        return call
 
 
 def _ok(call, code):
@@ -61,9 +81,13 @@ def _ok(call, code):
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _stream_of(stream, t):
-    """The cudaStream_t a call on t's device runs on."""
-    return _raw_stream(t.get_device()) if stream is None else stream.cuda_stream
+def _stream_of(stream, device):
+    """The cudaStream_t a call on `device` runs on."""
+    if stream is None:
+        return _raw_stream(device)
+    if stream.device_index != device:
+        raise ValueError("the stream must be one of the tensors' device")
+    return stream.cuda_stream
 
 
 def _empty(stream, shape, dtype, like):
@@ -74,12 +98,20 @@ def _empty(stream, shape, dtype, like):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _matrix(t, name, dtypes, cols=None, rows=None):
-    """A 2-d CUDA tensor with contiguous columns; returns its row stride."""
+def _refuse_device(t, name, device):
+    if device < 0 or t.get_device() < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    raise ValueError(f"{name} must be on the device of the other tensors")
+
+
+def _matrix(t, name, device, dtypes, cols=None, rows=None):
+    """A 2-d tensor on `device` with contiguous columns; returns its row stride."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}")
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor with two dimensions")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    if t.get_device() != device or device < 0:
+        _refuse_device(t, name, device)
     r, c = t.shape
     if (cols is not None and c != cols) or (rows is not None and r != rows):
         raise ValueError(f"{name} must have the shape [{rows if rows is not None else '*'}, "
@@ -96,28 +128,34 @@ def _matrix(t, name, dtypes, cols=None, rows=None):
     return s0
 
 
-def _dense(t, name, dtype, shape):
+def _dense(t, name, device, dtype, shape):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of shape {tuple(shape)}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}")
+    if t.get_device() != device or device < 0:
+        _refuse_device(t, name, device)
 
 
-def _positions(position):
+def _positions(position, device):
     if position.dtype != torch.int32:
         raise TypeError("position must be torch.int32")
     shape = position.shape
-    if len(shape) != 2 or shape[1] < 1 or not position.is_contiguous() or not position.is_cuda:
-        raise ValueError("position must be a contiguous CUDA tensor [tokens, k], k >= 1")
+    if len(shape) != 2 or shape[1] < 1 or not position.is_contiguous():
+        raise ValueError("position must be a contiguous tensor [tokens, k], k >= 1")
+    if position.get_device() != device or device < 0:
+        _refuse_device(position, "position", device)
     return shape
 
 
-def _experts(offsets):
+def _experts(offsets, device):
     if offsets.dtype != torch.int32:
         raise TypeError("offsets must be torch.int32")
     n = offsets.numel() - 1
-    if n < 1 or offsets.dim() != 1 or not offsets.is_contiguous() or not offsets.is_cuda:
-        raise ValueError("offsets must be a contiguous CUDA tensor [num_experts + 1]")
+    if n < 1 or offsets.dim() != 1 or not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous tensor [num_experts + 1]")
+    if offsets.get_device() != device or device < 0:
+        _refuse_device(offsets, "offsets", device)
     return n
 
 
@@ -130,79 +168,83 @@ def tbe_expert_sort(ids, num_experts, offsets=None, source=None, position=None, 
         raise TypeError("ids must be int32 or int64")
     if ids.dim() != 2 or ids.shape[1] < 1:
         raise ValueError("ids must have the shape [tokens, k], k >= 1")
-    _dense(ids, "ids", ids.dtype, ids.shape)
+    device = ids.get_device()
+    _dense(ids, "ids", device, ids.dtype, ids.shape)
     if not 1 <= num_experts <= TBE_MAX_EXPERTS:
         raise ValueError(f"num_experts must lie in [1, {TBE_MAX_EXPERTS}]")
     tokens, k = ids.shape
     if offsets is None:
         offsets = _empty(stream, num_experts + 1, torch.int32, ids)
     else:
-        _dense(offsets, "offsets", torch.int32, (num_experts + 1,))
+        _dense(offsets, "offsets", device, torch.int32, (num_experts + 1,))
     if source is None:
         source = _empty(stream, tokens * k, torch.int32, ids)
     else:
-        _dense(source, "source", torch.int32, (tokens * k,))
+        _dense(source, "source", device, torch.int32, (tokens * k,))
     if position is None:
         position = _empty(stream, (tokens, k), torch.int32, ids)
     else:
-        _dense(position, "position", torch.int32, (tokens, k))
-    _ok("tbe_expert_sort", _lib().tbe_expert_sort(
+        _dense(position, "position", device, torch.int32, (tokens, k))
+    _ok("tbe_expert_sort", _lib(device).tbe_expert_sort(
         ids.data_ptr(), _ID_DT[ids.dtype], tokens, k, num_experts, offsets.data_ptr(),
-        source.data_ptr(), position.data_ptr(), _stream_of(stream, ids)))
+        source.data_ptr(), position.data_ptr(), _stream_of(stream, device)))
     return offsets, source, position
 
 
 def tbe_expert_dispatch(x, offsets, position, out=None, stream=None):
     """rows [tokens * k, width]: x's rows at their sorted places, zeros after the
     last kept one."""
-    experts = _experts(offsets)
-    tokens, k = _positions(position)
-    xs = _matrix(x, "x", _ROW_DT, rows=tokens)
+    device = x.get_device()
+    experts = _experts(offsets, device)
+    tokens, k = _positions(position, device)
+    xs = _matrix(x, "x", device, _ROW_DT, rows=tokens)
     width = os_ = x.shape[1]
     if out is None:
         out = _empty(stream, (tokens * k, width), x.dtype, x)
     else:
-        os_ = _matrix(out, "out", (x.dtype,), width, tokens * k)
-    _ok("tbe_expert_dispatch", _lib().tbe_expert_dispatch(
+        os_ = _matrix(out, "out", device, (x.dtype,), width, tokens * k)
+    _ok("tbe_expert_dispatch", _lib(device).tbe_expert_dispatch(
         x.data_ptr(), _ROW_DT[x.dtype], tokens, k, width, xs, offsets.data_ptr(), experts,
-        position.data_ptr(), out.data_ptr(), os_, _stream_of(stream, x)))
+        position.data_ptr(), out.data_ptr(), os_, _stream_of(stream, device)))
     return out
 
 
-def _fp8_out(stream, x, rows, out, scale):
+def _fp8_out(stream, device, x, rows, out, scale):
     width = qs = x.shape[1]
     blocks = -(-width // TBE_SCALE_BLOCK)
     if out is None:
         out = _empty(stream, (rows, width), torch.float8_e4m3fn, x)
     else:
-        qs = _matrix(out, "out", (torch.float8_e4m3fn,), width, rows)
+        qs = _matrix(out, "out", device, (torch.float8_e4m3fn,), width, rows)
     if scale is None:
         scale = _empty(stream, (rows, blocks), torch.float32, x)
     else:
-        _dense(scale, "scale", torch.float32, (rows, blocks))
+        _dense(scale, "scale", device, torch.float32, (rows, blocks))
     return out, qs, scale
 
 
 def tbe_expert_dispatch_fp8(x, offsets, position, out=None, scale=None, stream=None):
     """The dispatch with the rows quantised to e4m3 on the way: (q [tokens * k,
     width], scale [tokens * k, ceil(width / 128)])."""
-    experts = _experts(offsets)
-    tokens, k = _positions(position)
-    xs = _matrix(x, "x", _ROW_DT, rows=tokens)
-    out, qs, scale = _fp8_out(stream, x, tokens * k, out, scale)
-    _ok("tbe_expert_dispatch_fp8", _lib().tbe_expert_dispatch_fp8(
+    device = x.get_device()
+    experts = _experts(offsets, device)
+    tokens, k = _positions(position, device)
+    xs = _matrix(x, "x", device, _ROW_DT, rows=tokens)
+    out, qs, scale = _fp8_out(stream, device, x, tokens * k, out, scale)
+    _ok("tbe_expert_dispatch_fp8", _lib(device).tbe_expert_dispatch_fp8(
         x.data_ptr(), _ROW_DT[x.dtype], tokens, k, x.shape[1], xs, offsets.data_ptr(), experts,
-        position.data_ptr(), out.data_ptr(), qs, scale.data_ptr(), _stream_of(stream, x)))
+        position.data_ptr(), out.data_ptr(), qs, scale.data_ptr(), _stream_of(stream, device)))
     return out, scale
 
 
 def tbe_quantize_rows(x, out=None, scale=None, stream=None):
     """Rows to e4m3 with an fp32 scale for each 128 columns: (q, scale)."""
-    xs = _matrix(x, "x", _ROW_DT)
-    out, qs, scale = _fp8_out(stream, x, x.shape[0], out, scale)
-    _ok("tbe_quantize_rows", _lib().tbe_expert_dispatch_fp8(
+    device = x.get_device()
+    xs = _matrix(x, "x", device, _ROW_DT)
+    out, qs, scale = _fp8_out(stream, device, x, x.shape[0], out, scale)
+    _ok("tbe_quantize_rows", _lib(device).tbe_expert_dispatch_fp8(
         x.data_ptr(), _ROW_DT[x.dtype], x.shape[0], 1, x.shape[1], xs, None, 0, None,
-        out.data_ptr(), qs, scale.data_ptr(), _stream_of(stream, x)))
+        out.data_ptr(), qs, scale.data_ptr(), _stream_of(stream, device)))
     return out, scale
 
 
@@ -213,39 +255,41 @@ def tbe_quantize_weights(w, out=None, scale=None, stream=None):
         raise TypeError("w must be float16, bfloat16 or float32")
     if w.dim() != 3:
         raise ValueError("w must have the shape [experts, n, k]")
-    _dense(w, "w", w.dtype, w.shape)
+    device = w.get_device()
+    _dense(w, "w", device, w.dtype, w.shape)
     e, n, k = w.shape
     grid = (e, -(-n // TBE_SCALE_BLOCK), -(-k // TBE_SCALE_BLOCK))
     if out is None:
         out = _empty(stream, (e, n, k), torch.float8_e4m3fn, w)
     else:
-        _dense(out, "out", torch.float8_e4m3fn, (e, n, k))
+        _dense(out, "out", device, torch.float8_e4m3fn, (e, n, k))
     if scale is None:
         scale = _empty(stream, grid, torch.float32, w)
     else:
-        _dense(scale, "scale", torch.float32, grid)
-    _ok("tbe_quantize_weights", _lib().tbe_quantize_weights(
+        _dense(scale, "scale", device, torch.float32, grid)
+    _ok("tbe_quantize_weights", _lib(device).tbe_quantize_weights(
         w.data_ptr(), _ROW_DT[w.dtype], e, n, k, out.data_ptr(), scale.data_ptr(),
-        _stream_of(stream, w)))
+        _stream_of(stream, device)))
     return out, scale
 
 
 def tbe_expert_combine(y, position, weights=None, out=None, stream=None):
     """out [tokens, width]: the experts' rows y [tokens * k, width] weighted (fp32
     weights [tokens, k], or None for ones) and summed per token."""
-    tokens, k = _positions(position)
-    ys = _matrix(y, "y", _ROW_DT, rows=tokens * k)
+    device = y.get_device()
+    tokens, k = _positions(position, device)
+    ys = _matrix(y, "y", device, _ROW_DT, rows=tokens * k)
     width = os_ = y.shape[1]
     if weights is not None:
-        _dense(weights, "weights", torch.float32, (tokens, k))
+        _dense(weights, "weights", device, torch.float32, (tokens, k))
     if out is None:
         out = _empty(stream, (tokens, width), y.dtype, y)
     else:
-        os_ = _matrix(out, "out", (y.dtype,), width, tokens)
-    _ok("tbe_expert_combine", _lib().tbe_expert_combine(
+        os_ = _matrix(out, "out", device, (y.dtype,), width, tokens)
+    _ok("tbe_expert_combine", _lib(device).tbe_expert_combine(
         y.data_ptr(), _ROW_DT[y.dtype], tokens, k, width, ys, position.data_ptr(),
         None if weights is None else weights.data_ptr(), out.data_ptr(), os_,
-        _stream_of(stream, y)))
+        _stream_of(stream, device)))
     return out
 
 
@@ -258,26 +302,27 @@ def tbe_expert_combine_backward(grad_out, y, offsets, position, weights=None, gr
                                 grad_weights=None, stream=None):
     """Gradients of tbe_expert_combine: (grad_y [tokens * k, width], grad_weights
     [tokens, k] fp32)."""
-    experts = _experts(offsets)
-    tokens, k = _positions(position)
-    gs = _matrix(grad_out, "grad_out", _ROW_DT, rows=tokens)
+    device = grad_out.get_device()
+    experts = _experts(offsets, device)
+    tokens, k = _positions(position, device)
+    gs = _matrix(grad_out, "grad_out", device, _ROW_DT, rows=tokens)
     width = gys = grad_out.shape[1]
-    ys = _matrix(y, "y", (grad_out.dtype,), width, tokens * k)
+    ys = _matrix(y, "y", device, (grad_out.dtype,), width, tokens * k)
     if weights is not None:
-        _dense(weights, "weights", torch.float32, (tokens, k))
+        _dense(weights, "weights", device, torch.float32, (tokens, k))
     if grad_y is None:
         grad_y = _empty(stream, (tokens * k, width), grad_out.dtype, grad_out)
     else:
-        gys = _matrix(grad_y, "grad_y", (grad_out.dtype,), width, tokens * k)
+        gys = _matrix(grad_y, "grad_y", device, (grad_out.dtype,), width, tokens * k)
     if grad_weights is None:
         grad_weights = _empty(stream, (tokens, k), torch.float32, grad_out)
     else:
-        _dense(grad_weights, "grad_weights", torch.float32, (tokens, k))
-    _ok("tbe_expert_combine_backward", _lib().tbe_expert_combine_backward(
+        _dense(grad_weights, "grad_weights", device, torch.float32, (tokens, k))
+    _ok("tbe_expert_combine_backward", _lib(device).tbe_expert_combine_backward(
         grad_out.data_ptr(), y.data_ptr(), _ROW_DT[grad_out.dtype], tokens, k, width, gs, ys,
         offsets.data_ptr(), experts, position.data_ptr(),
         None if weights is None else weights.data_ptr(), grad_y.data_ptr(), gys,
-        grad_weights.data_ptr(), _stream_of(stream, grad_out)))
+        grad_weights.data_ptr(), _stream_of(stream, device)))
     return grad_y, grad_weights
 
 
@@ -289,33 +334,35 @@ def tbe_expert_product(a, a_scale, w, w_scale, offsets=None, out=None, out_dtype
     w_scale from tbe_quantize_weights).  offsets None: one expert takes all
     rows.  Rows past offsets[-1] are zeros.  status: an int32 CUDA tensor that
     receives TBE_ERR_* bits, or None."""
-    fp8 = torch.float8_e4m3fn
-    as_ = _matrix(a, "a", (fp8,))
+    fp8, device = torch.float8_e4m3fn, a.get_device()
+    as_ = _matrix(a, "a", device, (fp8,))
     rows, k = a.shape
     if w.dim() != 3 or w.shape[2] != k:
         raise ValueError(f"w must have the shape [experts, n, {k}]")
     e, n, _ = shape = w.shape
-    _dense(w, "w", fp8, shape)
+    _dense(w, "w", device, fp8, shape)
     kb = -(-k // TBE_SCALE_BLOCK)
-    _dense(a_scale, "a_scale", torch.float32, (rows, kb))
-    _dense(w_scale, "w_scale", torch.float32, (e, -(-n // TBE_SCALE_BLOCK), kb))
+    _dense(a_scale, "a_scale", device, torch.float32, (rows, kb))
+    _dense(w_scale, "w_scale", device, torch.float32, (e, -(-n // TBE_SCALE_BLOCK), kb))
     if offsets is not None:
-        _dense(offsets, "offsets", torch.int32, (e + 1,))
+        _dense(offsets, "offsets", device, torch.int32, (e + 1,))
     elif e != 1:
         raise ValueError("offsets may be None with one expert only")
-    if status is not None and (status.dtype != torch.int32 or not status.is_cuda or
-                               status.numel() < 1):
-        raise ValueError("status must be an int32 CUDA tensor with an entry")
+    if status is not None:
+        if status.dtype != torch.int32 or status.numel() < 1:
+            raise ValueError("status must be an int32 tensor with an entry")
+        if status.get_device() != device:
+            _refuse_device(status, "status", device)
     os_ = n
     if out is None:
         if out_dtype not in _ROW_DT:
             raise TypeError("out_dtype must be float16, bfloat16 or float32")
         out = _empty(stream, (rows, n), out_dtype, a)
     else:
-        os_ = _matrix(out, "out", _ROW_DT, n, rows)
-    _ok("tbe_expert_product", _lib().tbe_expert_product(
+        os_ = _matrix(out, "out", device, _ROW_DT, n, rows)
+    _ok("tbe_expert_product", _lib(device).tbe_expert_product(
         a.data_ptr(), as_, a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
         None if offsets is None else offsets.data_ptr(), rows, n, k, e, out.data_ptr(),
         _ROW_DT[out.dtype], os_, None if status is None else status.data_ptr(),
-        _stream_of(stream, a)))
+        _stream_of(stream, device)))
     return out

@@ -7,7 +7,7 @@ import operator
 import numpy as np
 import torch
 
-from .experts import _ROW_DT, _empty, _lib, _ok, _stream_of
+from .experts import _ROW_DT, _empty, _lib, _ok, _refuse_device, _stream_of
 
 __all__ = ["tbe_grad_norm", "tbe_grad_clip", "TBE_GRAD_WORKSPACE_BYTES"]
 
@@ -43,7 +43,7 @@ def _filled(t):
     return True
 
 
-_dtype_of, _is_cuda = operator.attrgetter("dtype"), operator.attrgetter("is_cuda")
+_dtype_of = operator.attrgetter("dtype")
 _Tensor = torch.Tensor
 
 
@@ -54,8 +54,11 @@ def _table(grads, outs):
     dtypes = list(map(_dtype_of, grads))
     if not all(d in _ROW_DT for d in set(dtypes)):
         raise TypeError("gradients must be float16, bfloat16 or float32")
-    if not all(map(_is_cuda, grads)):
+    devices = set(map(_Tensor.get_device, grads))
+    if -1 in devices:
         raise ValueError("gradients must be CUDA tensors")
+    if len(devices) > 1:
+        raise ValueError("the gradients must be on one device")
     dense = all(map(_Tensor.is_contiguous, grads))
     if not dense and not all(g.is_contiguous() or _filled(g) for g in grads):
         raise ValueError("every gradient must fill one block of memory")
@@ -63,8 +66,8 @@ def _table(grads, outs):
     at = to = list(map(_Tensor.data_ptr, grads))
     if outs is not None:
         if list(map(_dtype_of, outs)) != dtypes or list(map(_Tensor.numel, outs)) != numel or \
-                not all(map(_is_cuda, outs)):
-            raise ValueError("out must hold a CUDA tensor of each gradient's type and size")
+                set(map(_Tensor.get_device, outs)) != devices:
+            raise ValueError("out must hold a tensor of each gradient's type, size and device")
         if not (dense and all(map(_Tensor.is_contiguous, outs))) and \
                 not all(o.shape == g.shape and o.stride() == g.stride() or
                         o.is_contiguous() and g.is_contiguous() for o, g in zip(outs, grads)):
@@ -77,29 +80,36 @@ def _table(grads, outs):
 
 
 def _scratch(stream, grads, norm, ws):
+    device = grads[0].get_device()
     if norm is None:
         norm = _empty(stream, (), torch.float32, grads[0])
-    elif norm.dtype != torch.float32 or norm.numel() != 1 or not norm.is_cuda:
-        raise ValueError("norm must be a float32 CUDA tensor with one entry")
+    else:
+        if norm.dtype != torch.float32 or norm.numel() != 1:
+            raise ValueError("norm must be a float32 tensor with one entry")
+        if norm.get_device() != device:
+            _refuse_device(norm, "norm", device)
     if ws is None:
         ws = _empty(stream, TBE_GRAD_WORKSPACE_BYTES, torch.uint8, grads[0])
-    elif ws.dtype != torch.uint8 or not ws.is_cuda or not ws.is_contiguous():
-        raise ValueError("ws must be a contiguous uint8 CUDA tensor")
-    return norm, ws
+    else:
+        if ws.dtype != torch.uint8 or not ws.is_contiguous():
+            raise ValueError("ws must be a contiguous uint8 tensor")
+        if ws.get_device() != device:
+            _refuse_device(ws, "ws", device)
+    return device, norm, ws
 
 
 def tbe_grad_norm(grads, norm=None, ws=None, stream=None):
     """Global 2-norm of a sequence of gradients (float16, bfloat16 or float32,
-    mixed as they come), as a float32 tensor with one entry.  ws: uint8
+    mixed as they come, on one device), as a float32 tensor with one entry.  ws: uint8
     scratch of TBE_GRAD_WORKSPACE_BYTES, allocated when not given."""
     grads = list(grads)
     if not grads:
         raise ValueError("no gradients")
     table = _table(grads, None)
-    norm, ws = _scratch(stream, grads, norm, ws)
-    _ok("tbe_grad_norm", _lib().tbe_grad_norm(
+    device, norm, ws = _scratch(stream, grads, norm, ws)
+    _ok("tbe_grad_norm", _lib(device).tbe_grad_norm(
         table.ctypes.data, len(grads), norm.data_ptr(), ws.data_ptr(), ws.numel(),
-        _stream_of(stream, norm)))
+        _stream_of(stream, device)))
     return norm
 
 
@@ -114,8 +124,8 @@ def tbe_grad_clip(grads, max_norm, out=None, norm=None, ws=None, stream=None):
         if len(out) != len(grads):
             raise ValueError("out must hold one tensor for each gradient")
     table = _table(grads, out)
-    norm, ws = _scratch(stream, grads, norm, ws)
-    _ok("tbe_grad_clip", _lib().tbe_grad_clip(
+    device, norm, ws = _scratch(stream, grads, norm, ws)
+    _ok("tbe_grad_clip", _lib(device).tbe_grad_clip(
         table.ctypes.data, len(grads), float(max_norm), norm.data_ptr(), ws.data_ptr(),
-        ws.numel(), _stream_of(stream, norm)))
+        ws.numel(), _stream_of(stream, device)))
     return norm
