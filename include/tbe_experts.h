@@ -102,8 +102,8 @@ tbe_status tbe_quantize_weights(const void* w, int32_t dtype, int64_t experts, i
 /* The experts' products on 8-bit rows and weights:
  *   out[r, n] = rn(sum_b a_scale[r, b] * w_scale[e, n / 128, b]
  *                        * sum_{i in block b} a[r, i] * w[e, n, i])
- * for offsets[e] <= r < offsets[e + 1], and out[r] = 0 for offsets[E] <= r <
- * rows.  The inner sums and the sum over blocks are fp32; the two scales are
+ * for offsets[e] <= r < offsets[e + 1], and out[r] = 0 for the other rows, those
+ * before offsets[0] and from offsets[E] on.  The inner sums and the sum over blocks are fp32; the two scales are
  * multiplied first, in fp32, so a product of scales below 2^-126 loses bits.
  * a [rows, K] e4m3 with a_scale [rows, ceil(K / 128)] (contiguous); w
  * [E, N, K] e4m3 (contiguous) with w_scale [E, ceil(N / 128), ceil(K / 128)]
@@ -113,7 +113,8 @@ tbe_status tbe_quantize_weights(const void* w, int32_t dtype, int64_t experts, i
  * hold the same values).  K, a_stride and the addresses of a and w must be
  * multiples of 16 (16-byte copies).
  * offsets are clamped into [0, rows], whatever they hold; an expert whose end
- * lies before its start has no rows.
+ * lies before its start has no rows.  What a row holds that two experts claim,
+ * or an expert and the rows of none, where offsets do not rise, is not defined.
  * status: device int32 word, or NULL; a bounded device wait that gave up sets
  * TBE_ERR_TIMEOUT in it (the outputs are then incomplete).
  * Errors: TBE_EINVAL, TBE_EUNSUPPORTED (type; alignment; rows, K or E N above

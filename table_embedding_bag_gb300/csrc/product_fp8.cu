@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(256)
 // Warps: 0 issues the TMA copies, 1 the MMAs; 2 and 3 bring the blocks' scales
 // to shared memory ahead of their use (an epilogue warp that waits for its own
 // scales costs more than the block: 512 us instead of 587 at 4096 x 2048), and clear
-// the rows past the last expert; 4..11 are the epilogue: warp w holds tokens 32 (w % 4)
+// the rows of no expert; 4..11 are the epilogue: warp w holds tokens 32 (w % 4)
 // .. + 31 of its CTA (one a lane) and half w / 8 of the columns.  A tile with few tokens copies
 // them 32 rows at a time; the other rows of the MMA hold what the buffer held before and
 // reach only results that are not stored.
@@ -962,11 +962,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           }
         }
       }
-      // the rows past the last expert
+      // the rows of no expert: before the first one's and past the last one's
       T* out = static_cast<T*>(P.out);
-      for (int64_t r = group_start(P, P.experts) + static_cast<int64_t>(blockIdx.x); r < P.rows;
-           r += gridDim.x) {
-        T* row = out + r * P.out_stride;
+      const int before = group_start(P, 0), past = group_start(P, P.experts);
+      for (int64_t i = blockIdx.x; i < before + static_cast<int64_t>(P.rows - past);
+           i += gridDim.x) {
+        T* row = out + (i < before ? i : past + (i - before)) * P.out_stride;
         if (P.tma_out)
           for (int c = (threadIdx.x - 64) * kVec<T>; c < P.n; c += 64 * kVec<T>)
             *reinterpret_cast<uint4*>(row + c) = make_uint4(0, 0, 0, 0);

@@ -332,7 +332,8 @@ def tbe_expert_product(a, a_scale, w, w_scale, offsets=None, out=None, out_dtype
     tbe_quantize_rows or tbe_expert_dispatch_fp8) of expert e, offsets[e] <= row
     < offsets[e + 1], times the transpose of w[e] (w [experts, n, k] e4m3 with
     w_scale from tbe_quantize_weights).  offsets None: one expert takes all
-    rows.  Rows past offsets[-1] are zeros.  status: an int32 CUDA tensor that
+    rows.  Rows before offsets[0] and from offsets[-1] on are zeros, so w, w_scale
+    and offsets may be those of a run of the experts.  status: an int32 CUDA tensor that
     receives TBE_ERR_* bits, or None."""
     fp8, device = torch.float8_e4m3fn, a.get_device()
     as_ = _matrix(a, "a", device, (fp8,))
