@@ -115,8 +115,9 @@ tbe_status tbe_quantize_weights(const void* w, int32_t dtype, int64_t experts, i
  * offsets are clamped into [0, rows], whatever they hold; an expert whose end
  * lies before its start has no rows.  What a row holds that two experts claim,
  * or an expert and the rows of none, where offsets do not rise, is not defined.
- * status: device int32 word, or NULL; a bounded device wait that gave up sets
- * TBE_ERR_TIMEOUT in it (the outputs are then incomplete).
+ * status: device int32 word, or NULL.  A bounded device wait that gave up sets
+ * TBE_ERR_TIMEOUT in it, and with or without it every element of out that may
+ * be lost is NaN.
  * Errors: TBE_EINVAL, TBE_EUNSUPPORTED (type; alignment; rows, K or E N above
  * 2^31 - 513, E > TBE_MAX_EXPERTS, or too many tiles), TBE_ECUDA. */
 tbe_status tbe_expert_product(const uint8_t* a, int64_t a_stride, const float* a_scale,

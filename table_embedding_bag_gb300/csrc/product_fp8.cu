@@ -748,6 +748,25 @@ __device__ __forceinline__ void store_rows(const ProductArgs& P, char* staging, 
   }
 }
 
+// After a wait that gave up: NaN in this CTA's share of its tiles, finished ones among them, so that
+// a product that is not whole does not pass for one.  The whole CTA, when no store is in flight.
+template <typename T, int kTileN, int kTileRows>
+__device__ __forceinline__ void mark_lost(const ProductArgs& P, const ProductShared& S, int first,
+                                          int tiles, int stride, int rank, int part, int split) {
+  const T nan = from_f32<T>(__int_as_float(0x7fffffff));
+  const int cols = kTileN / split;
+  for (int t = first; t < tiles; t += stride) {
+    const ProductTile tile = tile_at<kTileN, kTileRows>(P, S, t);
+    const int rows = min(tile.rows - rank * kTileM, kTileM);
+    T* out = static_cast<T*>(P.out) +
+             (static_cast<int64_t>(tile.row0) + rank * kTileM) * P.out_stride;
+    for (int i = threadIdx.x; i < rows * cols; i += kProductThreads) {
+      const int c = tile.n0 + part * cols + i % cols;
+      if (c < P.n) out[i / cols * P.out_stride + c] = nan;
+    }
+  }
+}
+
 template <typename T, int kTileN, Share kShare>
 __global__ void __launch_bounds__(kProductThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap a_map,
@@ -1058,6 +1077,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   }
   __syncwarp();
   if constexpr (kShare == kSplit) {
+    if (*dead && lane < split) store_to_cta(&S.dead, lane, 1);  // without one part the sum is lost
     cluster_sync();
     if (first < tiles && !S.dead) {
       const ProductTile tile = tile_at<kTileN, kTileRows>(P, S, first);
@@ -1093,7 +1113,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   if constexpr (kTwo) cluster_sync();  // the other CTA uses this one's barriers and memory no more
   fence_after_sync();
   if (warp == 2) give_tmem<kTwo>(tmem, kTmemColumns);
-  if (threadIdx.x == 0 && S.dead && P.status) atomicOr(P.status, TBE_ERR_TIMEOUT);
+  if (S.dead) {
+    mark_lost<T, kTileN, kTileRows>(P, S, first, tiles, stride, rank, part, split);
+    if (threadIdx.x == 0 && P.status) atomicOr(P.status, TBE_ERR_TIMEOUT);
+  }
 }
 
 // A map of a matrix of 1-, 2- or 4-byte elements, a row every `stride` bytes, for

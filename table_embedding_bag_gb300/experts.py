@@ -334,7 +334,8 @@ def tbe_expert_product(a, a_scale, w, w_scale, offsets=None, out=None, out_dtype
     w_scale from tbe_quantize_weights).  offsets None: one expert takes all
     rows.  Rows before offsets[0] and from offsets[-1] on are zeros, so w, w_scale
     and offsets may be those of a run of the experts.  status: an int32 CUDA tensor that
-    receives TBE_ERR_* bits, or None."""
+    receives TBE_ERR_* bits, or None; what a device wait that gave up may have
+    lost is NaN either way."""
     fp8, device = torch.float8_e4m3fn, a.get_device()
     as_ = _matrix(a, "a", device, (fp8,))
     rows, k = a.shape
