@@ -13,6 +13,12 @@
  * elements (at least the row's columns); their columns are contiguous.
  * Row data types are TBE_DT_F16, TBE_DT_BF16 and TBE_DT_F32.
  *
+ * No output may share memory with an input or with another output of its call.
+ * Columns of one buffer may lie beside columns of another.  Shared matrices, ids
+ * and positions are refused (TBE_EINVAL); matrices whose row strides differ
+ * count as shared where their columns meet modulo the strides' greatest common
+ * divisor.
+ *
  * Ordering, allocation and errors follow tbe.h: every call only enqueues work
  * on the given stream and returns, allocates nothing, can be captured into a
  * CUDA graph, and reports argument problems through tbe_status before

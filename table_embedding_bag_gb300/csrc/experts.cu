@@ -578,6 +578,11 @@ bool check_matrix(const void* p, int32_t dtype, int64_t stride, int64_t width) {
   return p && stride >= width && aligned_to(p, dtype_bytes(dtype));
 }
 
+Bytes bytes_of(const void* p, int32_t dtype, int64_t rows, int64_t width, int64_t stride) {
+  const int64_t b = dtype_bytes(dtype);
+  return {p, rows, width * b, stride * b};
+}
+
 bool check_plan(const int32_t* offsets, const int32_t* position) {
   return offsets && position && aligned_to(offsets, 4) && aligned_to(position, 4);
 }
@@ -635,8 +640,14 @@ extern "C" tbe_status tbe_expert_sort(const void* ids, int32_t index_dtype, int6
   if (!aligned_to(ids, index_dtype == TBE_DT_I32 ? 4 : 8) || !aligned_to(offsets, 4) ||
       !aligned_to(source, 4) || !aligned_to(position, 4))
     return TBE_EINVAL;
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int n = static_cast<int>(tokens * k);
+  const Bytes in_out[4] = {run_of(ids, int64_t(n) * (index_dtype == TBE_DT_I32 ? 4 : 8)),
+                           run_of(offsets, (int64_t(experts) + 1) * 4),
+                           run_of(source, int64_t(n) * 4), run_of(position, int64_t(n) * 4)};
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(in_out[i], in_out[j])) return TBE_EINVAL;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const size_t smem = static_cast<size_t>(kSortWarps + 1) * (experts + 1) * 4;
   // shared memory above 48 KB and clusters above eight CTAs have to be asked for
   const auto room_for = [&](auto kernel) {
@@ -716,7 +727,9 @@ extern "C" tbe_status tbe_expert_dispatch(const void* x, int32_t dtype, int64_t 
   if (bad != TBE_OK) return bad;
   if (!tokens || !width) return TBE_OK;
   if (experts < 1 || !check_plan(offsets, position) || !check_matrix(x, dtype, x_stride, width) ||
-      !check_matrix(rows, dtype, rows_stride, width))
+      !check_matrix(rows, dtype, rows_stride, width) ||
+      overlap(bytes_of(x, dtype, tokens, width, x_stride),
+              bytes_of(rows, dtype, tokens * k, width, rows_stride)))
     return TBE_EINVAL;
   int b = dtype_bytes(dtype);
   const bool vec = vector_rows(x, b, x_stride, width) && vector_rows(rows, b, rows_stride, width);
@@ -750,7 +763,9 @@ extern "C" tbe_status tbe_expert_combine(const void* y, int32_t dtype, int64_t t
   if (bad != TBE_OK) return bad;
   if (!tokens || !width) return TBE_OK;
   if (!check_plan(position, position) || !check_matrix(y, dtype, y_stride, width) ||
-      !check_matrix(out, dtype, out_stride, width) || !aligned_to(weights, 4))
+      !check_matrix(out, dtype, out_stride, width) || !aligned_to(weights, 4) ||
+      overlap(bytes_of(y, dtype, tokens * k, width, y_stride),
+              bytes_of(out, dtype, tokens, width, out_stride)))
     return TBE_EINVAL;
   const int b = dtype_bytes(dtype);
   const bool vec = vector_rows(y, b, y_stride, width) && vector_rows(out, b, out_stride, width);
@@ -780,6 +795,10 @@ extern "C" tbe_status tbe_expert_combine_backward(
   if (width && (!check_matrix(grad_out, dtype, grad_out_stride, width) ||
                 (grad_weights && !check_matrix(y, dtype, y_stride, width)) ||
                 (grad_y && !check_matrix(grad_y, dtype, grad_y_stride, width))))
+    return TBE_EINVAL;
+  const Bytes gy = bytes_of(grad_y, dtype, tokens * k, width, grad_y_stride);
+  if (overlap(bytes_of(grad_out, dtype, tokens, width, grad_out_stride), gy) ||
+      (grad_weights && overlap(bytes_of(y, dtype, tokens * k, width, y_stride), gy)))
     return TBE_EINVAL;
   const int b = dtype_bytes(dtype);
   const bool vec = vector_rows(grad_out, b, grad_out_stride, width) &&

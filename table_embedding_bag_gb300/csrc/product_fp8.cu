@@ -1190,6 +1190,8 @@ extern "C" tbe_status tbe_expert_dispatch_fp8(const void* x, int32_t dtype, int6
       !aligned_to(x, dtype_bytes(dtype)) || !aligned_to(scale, 4))
     return TBE_EINVAL;
   const int bytes = dtype_bytes(dtype);
+  if (overlap({x, tokens, width * bytes, x_stride * bytes}, {q, tokens * k, width, q_stride}))
+    return TBE_EINVAL;
   const bool aligned = width % 8 == 0 && x_stride * bytes % 16 == 0 && q_stride % 8 == 0 &&
                        aligned_to(x, 16) && aligned_to(q, 8);
   // one warp a token once there are enough of them, several for each before
@@ -1219,6 +1221,8 @@ extern "C" tbe_status tbe_quantize_weights(const void* w, int32_t dtype, int64_t
     return TBE_EINVAL;
   const int64_t nb = (n + kBlock - 1) / kBlock, kb = (k + kBlock - 1) / kBlock;
   if (nb * kb > INT32_MAX / experts) return TBE_EUNSUPPORTED;
+  if (overlap(run_of(w, experts * n * k * dtype_bytes(dtype)), run_of(q, experts * n * k)))
+    return TBE_EINVAL;
   return for_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     const bool aligned = k % 8 == 0 && aligned_to(w, 16) && aligned_to(q, 8);
@@ -1250,6 +1254,10 @@ extern "C" tbe_status tbe_expert_product(const uint8_t* a, int64_t a_stride, con
       !aligned_to(out, dtype_bytes(out_dtype)) || !aligned_to(status, 4))
     return TBE_EINVAL;
   if (k % 16 || a_stride % 16 || !aligned_to(a, 16) || !aligned_to(w, 16)) return TBE_EUNSUPPORTED;
+  const int ob = dtype_bytes(out_dtype);
+  const Bytes result = {out, rows, n * ob, out_stride * ob};
+  if (overlap({a, rows, k, a_stride}, result) || overlap(run_of(w, experts * n * k), result))
+    return TBE_EINVAL;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -1268,7 +1276,6 @@ extern "C" tbe_status tbe_expert_product(const uint8_t* a, int64_t a_stride, con
   P.experts = experts;
   P.kb = static_cast<int>((k + kBlock - 1) / kBlock);
   P.nb = static_cast<int>((n + kBlock - 1) / kBlock);
-  const int ob = dtype_bytes(out_dtype);
   // (a TMA store clips a row at a multiple of 16 bytes)
   P.tma_out = aligned_to(out, 16) && out_stride * ob % 16 == 0 && n * ob % 16 == 0;
   CUtensorMap a_map, a_part_map;

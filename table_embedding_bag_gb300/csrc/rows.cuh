@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <numeric>
 #include <type_traits>
 
 #include "tbe.h"
@@ -167,6 +168,32 @@ inline int dtype_bytes(int32_t dtype) {
 
 inline bool aligned_to(const void* p, size_t bytes) {
   return reinterpret_cast<uintptr_t>(p) % bytes == 0;
+}
+
+// Rows of `width` bytes, `stride` bytes apart.
+struct Bytes {
+  const void* p;
+  int64_t rows, width, stride;
+};
+inline Bytes run_of(const void* p, int64_t bytes) { return {p, 1, bytes, bytes}; }
+
+// Whether the two share memory.  Columns of one buffer beside columns of another row-wise do not;
+// where the strides differ, column ranges that meet modulo their greatest common divisor count as
+// shared.
+inline bool overlap(Bytes a, Bytes b) {
+  if (!a.p || !b.p || a.rows < 1 || b.rows < 1 || a.width < 1 || b.width < 1) return false;
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  if (pa + static_cast<uintptr_t>((a.rows - 1) * a.stride + a.width) <= pb ||
+      pb + static_cast<uintptr_t>((b.rows - 1) * b.stride + b.width) <= pa)
+    return false;
+  if (a.rows == 1 && b.rows == 1) return true;
+  const uintptr_t step =
+      static_cast<uintptr_t>(a.rows == 1   ? b.stride
+                             : b.rows == 1 ? a.stride
+                                           : std::gcd(a.stride, b.stride));
+  // b's columns, counted from the start of a's
+  const uintptr_t at = pb >= pa ? (pb - pa) % step : (step - (pa - pb) % step) % step;
+  return at < static_cast<uintptr_t>(a.width) || at + static_cast<uintptr_t>(b.width) > step;
 }
 
 }  // namespace tbe

@@ -5,7 +5,8 @@ As in the rest of the package the functions only check and marshal their
 arguments.  A call runs on the device of its tensors, which must all be on one,
 whichever device is current.  Outputs that are not given are allocated on the
 stream the call runs on.  A matrix may have any row stride; its columns must be
-contiguous.
+contiguous.  An output must not share memory with an input (no call works in
+place).
 """
 from __future__ import annotations
 
