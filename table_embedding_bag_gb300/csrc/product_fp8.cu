@@ -6,6 +6,7 @@
 #include <type_traits>
 
 #include "internal.h"
+#include "product_form.h"
 #include "rows.cuh"
 #include "tbe_experts.h"
 #include "tcgen05.cuh"
@@ -269,10 +270,6 @@ constexpr int kEpilogueWarps = 8;
 constexpr int kTmemColumns = 512;
 constexpr int kMaxStages = 5;
 constexpr int kStoreBox = 128;  // bytes of a row of a stored box
-
-// How CTAs share a tile.
-enum Share { kAlone, kPair, kSplit };
-constexpr int kMostSplit = 8;
 
 template <int kTileN, Share kShare>
 struct ProductShape {
@@ -557,7 +554,7 @@ struct ProductTile {
 };
 
 // Row tiles of all experts before each, in shared memory; the whole CTA.  Sums
-// stop at P.row_tiles, which offsets that rise do not reach.
+// stop at P.row_tiles, which offsets that rise do not pass.
 template <int kTileRows>
 __device__ __forceinline__ void build_tiles(const ProductArgs& P, ProductShared& S) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1298,9 +1295,7 @@ extern "C" tbe_status tbe_expert_product(const uint8_t* a, int64_t a_stride, con
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
         cudaSuccess)
       return TBE_ECUDA;
-    // tiles, at most (every expert's last one may be a part)
-    P.row_tiles =
-        static_cast<int>(rows / Shape::kTileRows + (experts < rows ? experts : rows));
+    P.row_tiles = static_cast<int>(most_row_tiles(rows, experts, Shape::kTileRows));
     const int64_t most = static_cast<int64_t>(P.row_tiles) * P.n_tiles;
     if (most > INT32_MAX / 8) return TBE_EUNSUPPORTED;  // the kernel counts tiles in 32 bits
     const int64_t room = sms / cluster;
@@ -1329,21 +1324,9 @@ extern "C" tbe_status tbe_expert_product(const uint8_t* a, int64_t a_stride, con
   using Pair = std::integral_constant<Share, kPair>;
   using Split = std::integral_constant<Share, kSplit>;
   return for_dtype(out_dtype, [&](auto t) {
-    const int64_t tiles =
-        (rows / kTileM + (experts < rows ? experts : rows)) * ((n + 127) / 128);
-    int split = 1;
-    while (split < kMostSplit && tiles * split * 2 <= sms && P.kb >= split * 4) split *= 2;
-    if (split > 1) return launch(t, Narrow{}, Split{}, split);
-    // Rounds of tiles over the multiprocessors (a pair takes two), times a tile's time: measured
-    // on 65536 rows of 16 experts and 4096 columns, a block of k takes a pair 0.40 us and a lone
-    // CTA 0.27, and a tile's start and end 1.43 and 0.76 us (k = 2048: 421 us in pairs, 501 alone;
-    // 5000 rows, 8 experts, 1000 x 1008: 21.6 and 18.2).
-    const int64_t parts = (experts < rows ? experts : rows) / 2;  // an expert's last tile, on average
-    const auto rounds = [](int64_t tiles, int64_t at_once) { return (tiles + at_once - 1) / at_once; };
-    const int64_t alone = rounds((rows / 128 + parts) * ((n + 127) / 128), sms);
-    const int64_t paired = rounds((rows / 256 + parts) * ((n + 255) / 256), sms / 2);
-    if (alone * (P.kb * 27 + 76) < paired * (P.kb * 40 + 143))
-      return launch(t, Narrow{}, Alone{}, 1);
-    return launch(t, Wide{}, Pair{}, 2);
+    const ProductForm form = product_form(rows, n, P.kb, experts, sms);
+    if (form.share == kSplit) return launch(t, Narrow{}, Split{}, form.cluster);
+    if (form.share == kAlone) return launch(t, Narrow{}, Alone{}, form.cluster);
+    return launch(t, Wide{}, Pair{}, form.cluster);
   });
 }
