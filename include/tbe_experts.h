@@ -109,8 +109,9 @@ tbe_status tbe_quantize_weights(const void* w, int32_t dtype, int64_t experts, i
  *   out[r, n] = rn(sum_b a_scale[r, b] * w_scale[e, n / 128, b]
  *                        * sum_{i in block b} a[r, i] * w[e, n, i])
  * for offsets[e] <= r < offsets[e + 1], and out[r] = 0 for the other rows, those
- * before offsets[0] and from offsets[E] on.  The inner sums and the sum over blocks are fp32; the two scales are
- * multiplied first, in fp32, so a product of scales below 2^-126 loses bits.
+ * before offsets[0] and from offsets[E] on.  The inner sums and the sum over
+ * blocks are fp32; the two scales are multiplied first, in fp32, so a product of
+ * scales below 2^-126 loses bits.
  * a [rows, K] e4m3 with a_scale [rows, ceil(K / 128)] (contiguous); w
  * [E, N, K] e4m3 (contiguous) with w_scale [E, ceil(N / 128), ceil(K / 128)]
  * (contiguous); offsets [E + 1], or NULL with E = 1 for all rows; out

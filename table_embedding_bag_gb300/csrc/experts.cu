@@ -437,9 +437,9 @@ __device__ __forceinline__ float group_sum(float v, int size) {
   return v;
 }
 
-// The gradients of combine, a group (a warp, or a part of one for narrow rows) a token: grad_out's row is read once for four
-// of the token's rows, whose loads are in flight together (65536 tokens x 4 rows of 2048
-// bf16: 356 us, a row after the other 405).
+// The gradients of combine, a group (a warp, or a part of one for narrow rows) a token:
+// grad_out's row is read once for four of the token's rows, whose loads are in flight together
+// (65536 tokens x 4 rows of 2048 bf16: 356 us, a row after the other 405).
 template <typename T>
 __global__ void __launch_bounds__(kMoveThreads, 4)
     combine_backward_by_token(const T* __restrict__ grad_out, const T* __restrict__ y,
@@ -749,8 +749,8 @@ extern "C" tbe_status tbe_expert_dispatch(const void* x, int32_t dtype, int64_t 
     const int lg = log_group_of(tokens, width, b, kAligned);
     dispatch_kernel<T, kAligned><<<static_cast<unsigned>(group_blocks(tokens, lg)), kMoveThreads, 0,
                             static_cast<cudaStream_t>(stream)>>>(
-        static_cast<const T*>(x), tokens, k, static_cast<int>(width), x_stride, offsets, experts, position,
-        static_cast<T*>(rows), rows_stride, lg);
+        static_cast<const T*>(x), tokens, k, static_cast<int>(width), x_stride, offsets, experts,
+        position, static_cast<T*>(rows), rows_stride, lg);
     return launched();
   });
 }

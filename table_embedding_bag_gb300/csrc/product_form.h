@@ -45,8 +45,8 @@ inline ProductForm product_form(int64_t rows, int64_t n, int64_t kb, int64_t exp
   // CTA 0.27, and a tile's start and end 1.43 and 0.76 us (k = 2048: 421 us in pairs, 501 alone;
   // 5000 rows, 8 experts, 1000 x 1008: 21.6 and 18.2).  One expert with a part of a tile: 16 rows,
   // 128000 x 4096: 120.8 in pairs, 104.4 alone; 1 row, 1024 x 128: 10.2 and 8.2.  Of 120 drawn
-  // products (up to 65536 rows, 4096 columns, k of 4096) the chosen form, splits included, takes 1.04
-  // times the best form's time on average and 1.26 times at worst.
+  // products (up to 65536 rows, 4096 columns, k of 4096) the chosen form, splits included, takes
+  // 1.04 times the best form's time on average and 1.26 times at worst.
   const auto rounds = [](int64_t t, int64_t at_once) { return (t + at_once - 1) / at_once; };
   const int64_t alone =
       rounds(likely_row_tiles(rows, experts, 128) * ((n + 127) / 128), sms) * (kb * 27 + 76);

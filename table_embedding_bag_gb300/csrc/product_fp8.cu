@@ -119,9 +119,10 @@ __device__ __forceinline__ void store8(uint8_t* row, int col, int width,
 
 // Sixteen lanes quantise a token's block of 128 columns, eight columns each; a
 // warp walks the token's blocks two at a time.  The row is read once and all its k
-// places are written.  Bound by its instructions: 8192 x 1024 bf16 to four places of 32768
-// takes 15.0 us, 3.4 TB/s, and more warps a multiprocessor do not help.  kAligned: rows and q rows allow 16- and 8-byte
-// accesses from end to end.
+// places are written.  8192 x 1024 bf16 to four places of 32768 takes 14.8 us, 3.5 TB/s (fp16
+// 14.5, fp32 12.6; rows that were not in the cache 20.9).  Neither memory nor issue is used up
+// (16384 x 2048: DRAM 33 %, issue 60 % at 40 % of the warps), and more warps a multiprocessor do
+// not help.  kAligned: rows and q rows allow 16- and 8-byte accesses from end to end.
 template <typename T, bool kAligned>
 __global__ void __launch_bounds__(256)
     dispatch_fp8_kernel(const T* __restrict__ x, int64_t tokens, int k, int width,
@@ -191,7 +192,8 @@ __global__ void __launch_bounds__(256)
 }
 
 // One CTA a 128 x 128 block of an expert's weights, read once: a thread holds eight
-// columns of eight rows, 16 rows apart.
+// columns of eight rows, 16 rows apart.  2^27 weights: fp32 103 us, 6.5 TB/s, memory; bf16 97 and
+// fp16 83 for three fifths of the bytes: the work on each value.
 template <typename T, bool kAligned>
 __global__ void __launch_bounds__(256)
     quantize_weights_kernel(const T* __restrict__ w, int64_t n, int64_t k, int nb, int kb,
@@ -246,13 +248,14 @@ __global__ void __launch_bounds__(256)
 //   kPair   two CTAs form 256 tokens x 256 columns of n: an MMA (cta_group::2) reads
 //           both CTAs' shared memory, which holds half of the tokens and half of the
 //           weight rows in each: two thirds of the bytes of a lone CTA with
-//           128 x 256 (65536 rows, 16 experts, 4096 x 4096: 765 us and 873)
+//           128 x 256 (65536 rows, 16 experts, 4096 x 4096: 778 us, and 990 in
+//           kAlone's tiles)
 //   kAlone  a CTA forms 128 tokens x 128 columns, with four accumulators: for fewer
 //           or uneven tiles
 //   kSplit  the CTAs of a cluster each form a part of the sum over blocks of one
 //           kAlone tile, for few tokens; the parts meet in shared memory and are
-//           added in the order of the ranks (one row, 4096 x 4096: 10.1 us and 17.1;
-//           128 rows, 1024 x 8192: 11.8 us and 29.5)
+//           added in the order of the ranks (nothing in the cache: one row, 4096 x 4096:
+//           14.4 us, and 16.4 in one part; 128 rows, 1024 x 8192: 17.0 and 24.1)
 //
 // Warps: 0 issues the TMA copies, 1 the MMAs; 2 and 3 bring the blocks' scales
 // to shared memory ahead of their use (an epilogue warp that waits for its own
@@ -745,8 +748,9 @@ __device__ __forceinline__ void store_rows(const ProductArgs& P, char* staging, 
   }
 }
 
-// After a wait that gave up: NaN in this CTA's share of its tiles, finished ones among them, so that
-// a product that is not whole does not pass for one.  The whole CTA, when no store is in flight.
+// After a wait that gave up: NaN in this CTA's share of its tiles, finished ones among them, so
+// that a product that is not whole does not pass for one.  The whole CTA, when no store is in
+// flight.
 template <typename T, int kTileN, int kTileRows>
 __device__ __forceinline__ void mark_lost(const ProductArgs& P, const ProductShared& S, int first,
                                           int tiles, int stride, int rank, int part, int split) {
@@ -853,8 +857,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             ok = false;
             most = issued;
             // Both CTAs' copies of a block count at rank 0's barrier, which can only be waited for
-            // if both are issued.  So the CTA that has issued fewer issues the others' counterparts;
-            // their stages are free, or the other CTA would not have filled its own.
+            // if both are issued.  So the CTA that has issued fewer issues the others'
+            // counterparts; their stages are free, or the other CTA would not have filled its own.
             if constexpr (kTwo) {
               tell();
               if (__all_sync(0xffffffffu, mbar_wait(&S.left, 0, 2 * kSpinLimit))) {
@@ -908,7 +912,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           if (elected()) {
 #pragma unroll
             for (int i = 0; i < kBlock / 32; ++i)  // 32 columns are 32 bytes: 2 in the address
-              mma_f8<kTwo>(tmem + slot * kTileN, a_desc + at + i * 2, w_desc + at + i * 2, idesc, i > 0);
+              mma_f8<kTwo>(tmem + slot * kTileN, a_desc + at + i * 2, w_desc + at + i * 2, idesc,
+                           i > 0);
             commit_to<kTwo>(&S.done[stage]);
           }
           __syncwarp();
@@ -1055,8 +1060,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       }
       if constexpr (kShare == kSplit) {
         if (on && ok) {
-          float* join = reinterpret_cast<float*>(ring) + (quarter * 32 + lane) * Shape::kJoinStride +
-                        half * kSums;
+          float* join = reinterpret_cast<float*>(ring) +
+                        (quarter * 32 + lane) * Shape::kJoinStride + half * kSums;
 #pragma unroll
           for (int i = 0; i < kSums / 2; i += 2) {
             const float2 f = pair_values(acc[i]), g = pair_values(acc[i + 1]);

@@ -6,7 +6,8 @@ arguments.  A call runs on the device of its tensors, which must all be on one,
 whichever device is current.  Outputs that are not given are allocated on the
 stream the call runs on.  A matrix may have any row stride; its columns must be
 contiguous.  An output must not share memory with an input (no call works in
-place).
+place).  Autograd is not involved: results require no gradient, and the
+gradients are calls of their own.
 """
 from __future__ import annotations
 

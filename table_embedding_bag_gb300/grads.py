@@ -1,4 +1,8 @@
-"""Binding of the gradient-norm operators (include/tbe_grads.h)."""
+"""Binding of the gradient-norm operators (include/tbe_grads.h).
+
+Autograd is not involved: the norm requires no gradient, and clipping in place
+moves no version counter.
+"""
 from __future__ import annotations
 
 import ctypes

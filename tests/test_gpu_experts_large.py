@@ -1,6 +1,6 @@
 """Batches that fill the GPU take other launches than small ones: the gradients of combine a group
-a token, four of its rows at a time, and groups of a quarter of the threads for rows, in dispatch and
-combine.  Both with dropped assignments, weights, numbers of rows that are no multiple of four,
+a token, four of its rows at a time, and groups of a quarter of the threads for rows, in dispatch
+and combine.  Both with dropped assignments, weights, numbers of rows that are no multiple of four,
 rows off 16-byte boundaries and tokens that end inside a warp, against 64-bit forms.
 
 Tolerances: as a result summed in fp32 from t terms, 2 t roundings of 2^-24 of the sum of |terms|,

@@ -62,7 +62,7 @@ def test_row_tiles(ask):
         assert 1 <= likely <= most, c
         if c[3] == 1:
             assert likely == -(-c[0] // c[4]), c
-        if c[0] >= 4 * c[3] and c[4] > 2:  # experts with several rows: within a tile for two experts
+        if c[0] >= 4 * c[3] and c[4] > 2:  # experts with several rows: a tile for two experts
             assert abs(likely - expected) <= 1 + c[3] / 2, c
 
 
