@@ -120,8 +120,8 @@ tbe_status tbe_quantize_weights(const void* w, int32_t dtype, int64_t experts, i
  * hold the same values).  K, a_stride and the addresses of a and w must be
  * multiples of 16 (16-byte copies).
  * offsets are clamped into [0, rows], whatever they hold; an expert whose end
- * lies before its start has no rows.  What a row holds that two experts claim,
- * or an expert and the rows of none, where offsets do not rise, is not defined.
+ * lies before its start has no rows.  Where offsets do not rise, what out holds
+ * is not defined (nothing outside it is written).
  * status: device int32 word, or NULL.  A bounded device wait that gave up sets
  * TBE_ERR_TIMEOUT in it, and with or without it every element of out that may
  * be lost is NaN.
