@@ -69,8 +69,8 @@ def test_one_cta_of_a_pair_gives_up(stuck_copy_lib, monkeypatch, rows, n, k, gro
         start = time.monotonic()
         tbe.tbe_expert_product(*args, status=status)
         torch.cuda.synchronize()
-        # 4096 polls and the ways out, not the bound of a wait for copies that never come
-        assert time.monotonic() - start < 1.0
+        # 4096 polls and the ways out, not the 4.7 s of a wait for copies that never come
+        assert time.monotonic() - start < 3.0
         assert int(status) & 4  # TBE_ERR_TIMEOUT
     monkeypatch.undo()
     status.zero_()
