@@ -3,7 +3,8 @@
  * Table Batched Embedding library.
  *
  * A pooled vector (a token) goes to k of E expert networks and comes back as
- * their weighted sum.  The calls below sort the tokens' assignments by expert,
+ * their weighted sum.  The calls below choose the k experts from a router's
+ * logits and give the choice's gradient, sort the tokens' assignments by expert,
  * carry the rows there and back, give the gradients of both, quantise rows
  * and weights to 8 bits, and form the experts' matrix products in 8 bits.
  *
@@ -36,6 +37,47 @@ extern "C" {
 
 #define TBE_MAX_EXPERTS 1024   /* experts of one call */
 #define TBE_SCALE_BLOCK 128    /* columns (and weight rows) that share a scale */
+#define TBE_MAX_CHOSEN 31      /* experts chosen for one token */
+
+enum { TBE_SCORE_SOFTMAX = 1, TBE_SCORE_SIGMOID = 2 };
+
+/* Chooses k experts for each token and weights them.  logits [N, E] of dtype:
+ *   s[n, e] = softmax over e, or sigmoid, of logits[n, e]
+ *   c[n, e] = s[n, e] + bias[e]                   bias fp32 [E], or NULL
+ * An expert is closed to a token where its logit or c is -inf: its score is then s as it
+ * is, and it is not chosen.  With G > 1 groups of E / G consecutive experts, a group is worth
+ * the sum of its group_best (1 or 2) largest c (of those that are open), and only the top_groups
+ * groups that are worth most are open.  The k open experts with the largest c are
+ * chosen, in that order:
+ *   ids [N, k]      of index_dtype; -1 where fewer are open (tbe_expert_sort drops those)
+ *   weights [N, k]  fp32: scale * s, or with renormalize scale * s / (sum of the chosen s);
+ *                   0 where ids is -1
+ * Ties go to the lower expert or group.  The choice is that of exact arithmetic
+ * wherever 64 bits tell the c apart: where fp32 does not, it is made again in 64 bits.
+ * Without bias and groups the logits themselves are compared.  The bias only chooses: weights
+ * are of s.  NaN ranks above everything, so a token with a NaN logit shows it in its
+ * weights; softmax of +inf is NaN as the formula gives, and a row that is closed
+ * throughout has ids -1.
+ * logits have a row stride in elements; ids and weights are contiguous.
+ * Errors: TBE_EINVAL (sizes: k > top_groups * E / G, E not a multiple of G, ...; a scale that is
+ * not finite), TBE_EUNSUPPORTED (types, E > TBE_MAX_EXPERTS, k > TBE_MAX_CHOSEN, G > 32,
+ * N >= 2^31 / k), TBE_ECUDA. */
+tbe_status tbe_expert_route(const void* logits, int32_t dtype, int64_t tokens, int32_t experts,
+                            int64_t logits_stride, const float* bias, int32_t score, int32_t k,
+                            int32_t groups, int32_t top_groups, int32_t group_best,
+                            int32_t renormalize, float scale, void* ids, int32_t index_dtype,
+                            float* weights, void* stream);
+
+/* Gradient of tbe_expert_route's weights in the logits (the choice has none):
+ *   grad_logits[n, e] = rn(sum_j grad_weights[n, j] * d weights[n, j] / d logits[n, e])
+ * for the ids [N, k] given; an id outside [0, E) takes no part, and what its
+ * grad_weights holds is not used.  An expert may be named twice.  grad_logits [N, E] of
+ * dtype. */
+tbe_status tbe_expert_route_backward(const float* grad_weights, const void* logits, int32_t dtype,
+                                     int64_t tokens, int32_t experts, int64_t logits_stride,
+                                     const void* ids, int32_t index_dtype, int32_t k,
+                                     int32_t score, int32_t renormalize, float scale,
+                                     void* grad_logits, int64_t grad_stride, void* stream);
 
 /* Sorts the assignments by expert, stably (within an expert in the order of
  * a).  ids [N, k] (contiguous, TBE_DT_I32 or TBE_DT_I64): an id outside [0, E)

@@ -15,10 +15,14 @@ import numpy as np
 import torch
 
 from . import _build
+from . import embed as _embed
 from . import experts as _experts
 from . import grads as _grads
+from . import norm as _norm
+from .embed import *  # noqa: F401,F403
 from .experts import *  # noqa: F401,F403
 from .grads import *  # noqa: F401,F403
+from .norm import *  # noqa: F401,F403
 
 __all__ = [
     "build", "TBEDesc", "Workspace", "TBEError", "tbe_workspace_size", "tbe_forward",
@@ -28,7 +32,7 @@ __all__ = [
     "TBE_NOALLOC_SCRATCH_BYTES", "TBE_ETOO_LARGE",
     "TBE_F_CHECK_BOUNDS", "TBE_F_REPAIR_OFFSETS", "TBE_F_FORCE_GENERIC", "TBE_F_LONG_TWO_LAUNCH",
     "TBE_F_PREPROCESSED", "TBE_F_MEAN", "TBE_F_ELEMENTWISE", "TBE_WS_WEIGHTED", "TBE_WS_MEAN", "TBE_ERR_INDEX_RANGE", "TBE_ERR_OFFSETS",
-    *_experts.__all__, *_grads.__all__,
+    *_embed.__all__, *_experts.__all__, *_grads.__all__, *_norm.__all__,
 ]
 
 TBE_OK, TBE_EINVAL, TBE_EWORKSPACE, TBE_EUNSUPPORTED, TBE_ECUDA, TBE_ETOO_LARGE = range(6)
@@ -117,8 +121,8 @@ def configure(lib):
               "tbe_backward_rowwise_adagrad", "tbe_workspace_view", "tbe_read_status",
               "tbe_backward_rowwise_adagrad_noalloc", "tbe_probe_set", "tbe_probe_read"):
         getattr(lib, f).restype = ctypes.c_int
-    _experts.configure(lib)
-    _grads.configure(lib)
+    for part in (_embed, _experts, _grads, _norm):
+        part.configure(lib)
     return lib
 
 

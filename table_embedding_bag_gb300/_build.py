@@ -13,7 +13,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtbe.so")
 SOURCES = ["tbe_api.cu", "forward.cu", "forward_small.cu", "forward_hot.cu", "preprocess.cu",
-           "update.cu", "hot_grad.cu", "noalloc.cu", "experts.cu", "product_fp8.cu", "grads.cu"]
+           "update.cu", "hot_grad.cu", "noalloc.cu", "experts.cu", "product_fp8.cu", "grads.cu",
+           "route.cu", "norm.cu", "embed.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "-I", INCLUDE, "-I", CSRC]

@@ -1,0 +1,718 @@
+// Token embedding: a row of a table for each token, and the table's gradient by
+// sorted tokens.  The operations are specified in include/tbe_embed.h.
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "entry.cuh"
+#include "sort.cuh"
+#include "tbe_embed.h"
+
+namespace tbe {
+namespace {
+
+// -------------------------------------------------------------------- lookup
+//
+// Memory bounds it.  A group of `1 << log_group` threads carries a token's row, up to
+// four 16-byte vectors in flight a thread; rows off 16-byte boundaries go in vectors
+// all the same (inner_span, load_vec).
+constexpr int kMoveThreads = 256;
+constexpr int kInFlight = 4;
+
+template <typename T, typename IdT, bool kAligned>
+__global__ void __launch_bounds__(kMoveThreads)
+    embed_kernel(const T* __restrict__ table, int rows, int width, int64_t table_stride,
+                 const IdT* __restrict__ ids, int tokens, float scale, T* __restrict__ out,
+                 int64_t out_stride, int log_group) {
+  constexpr int V = kVec<T>;
+  const int size = 1 << log_group, t = threadIdx.x & (size - 1);
+  const int64_t token = static_cast<int64_t>(blockIdx.x) * (kMoveThreads >> log_group) +
+                        (threadIdx.x >> log_group);
+  if (token >= tokens) return;
+  const IdT id = ids[token];
+  const bool on = id >= 0 && id < static_cast<IdT>(rows);
+  const T* src = table + (on ? static_cast<int64_t>(id) * table_stride : 0);
+  T* dst = out + token * out_stride;
+  const Span s = inner_span<T, kAligned>(dst, width);
+  for (int e0 = s.lo + t * V; e0 < s.hi; e0 += size * V * kInFlight) {
+    Pack<T, V> v[kInFlight];
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u)
+      if (on && e0 + u * size * V < s.hi) v[u] = load_vec<T, kAligned>(src + e0 + u * size * V);
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) {
+      if (e0 + u * size * V >= s.hi) continue;
+      float f[V] = {};
+      if (on) {
+        to_floats<T>(v[u], f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] *= scale;
+      }
+      store_vec(dst + e0 + u * size * V, from_floats<T>(f));
+    }
+  }
+  if constexpr (!kAligned)
+    for_ends(s, width, t, size,
+             [&](int e) { dst[e] = from_f32<T>(on ? scale * to_f32(src[e]) : 0.f); });
+}
+
+// ---------------------------------------------------------------------- sort
+//
+// Tokens sorted by row, stably, as items (row, token); tokens without a row get row V, which
+// comes last.  A radix sort from the lowest digit, each pass a counting sort
+// as the experts' (a warp counts its run of the items in its own row of shared memory, the
+// rows are scanned, and the warp walks its run again).  Up to kOneLaunch tokens
+// all passes are one launch of one cluster; above, three launches a pass over the whole GPU.
+constexpr int kDigitBits = 10;  // of a pass, at most
+constexpr int kSortUnroll = 4;
+constexpr int kOneLaunch = 131072;
+constexpr int kTokensPerCta = 2048;   // from which another CTA of the cluster pays
+constexpr int kGridCtas = 304;
+constexpr int kGridChunk = 4096;      // items of a CTA of three launches, at least
+
+struct Item {
+  int row, token;
+};
+
+template <typename IdT>
+struct FromIds {
+  const IdT* ids;
+  int rows;
+  __device__ __forceinline__ Item operator()(int64_t i) const {
+    const IdT id = ids[i];
+    return {id >= 0 && id < static_cast<IdT>(rows) ? static_cast<int>(id) : rows,
+            static_cast<int>(i)};
+  }
+};
+// Past the first pass: items that other multiprocessors wrote in this launch (read from L2).
+struct FromItems {
+  const Item* items;
+  __device__ __forceinline__ Item operator()(int64_t i) const {
+    const int2 v = __ldcg(reinterpret_cast<const int2*>(items + i));
+    return {v.x, v.y};
+  }
+};
+
+struct Digit {
+  int shift, bits;
+  __device__ __forceinline__ int buckets() const { return 1 << bits; }
+  __device__ __forceinline__ int of(const Item& it) const {
+    return (it.row >> shift) & (buckets() - 1);
+  }
+};
+
+// Every warp's counts of its run, count[warp][bucket], and total[bucket].  The whole
+// CTA; ends before a barrier.
+template <typename Source>
+__device__ __forceinline__ void count_items(const Source& from, Chunk c, Digit d, int* count,
+                                            int* total) {
+  const int buckets = d.buckets(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < kSortWarps * buckets; i += blockDim.x) count[i] = 0;
+  __syncthreads();
+  int* mine = count + warp * buckets;
+  for (int64_t a0 = c.first + lane; a0 < c.last; a0 += 32 * kSortUnroll) {
+    Item it[kSortUnroll];
+#pragma unroll
+    for (int u = 0; u < kSortUnroll; ++u)
+      if (a0 + 32 * u < c.last) it[u] = from(a0 + 32 * u);
+#pragma unroll
+    for (int u = 0; u < kSortUnroll; ++u)
+      if (a0 + 32 * u < c.last) atomicAdd(mine + d.of(it[u]), 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < buckets; e += blockDim.x) {
+    int sum = 0;
+#pragma unroll 16
+    for (int w = 0; w < kSortWarps; ++w) sum += count[w * buckets + e];
+    total[e] = sum;
+  }
+}
+
+template <typename Source>
+__device__ __forceinline__ void place_items(const Source& from, Chunk c, Digit d, int* mine,
+                                            Item* to) {
+  const int lane = threadIdx.x & 31;
+  for (int64_t a0 = c.first; a0 < c.last; a0 += 32 * kSortUnroll) {
+    Item it[kSortUnroll];
+#pragma unroll
+    for (int u = 0; u < kSortUnroll; ++u)
+      if (a0 + 32 * u + lane < c.last) it[u] = from(a0 + 32 * u + lane);
+#pragma unroll
+    for (int u = 0; u < kSortUnroll; ++u) {
+      const bool on = a0 + 32 * u + lane < c.last;
+      const int b = on ? d.of(it[u]) : -1;
+      const unsigned same = __match_any_sync(kAll, b);
+      int place = 0;
+      if (on) place = mine[b] + __popc(same & ((1u << lane) - 1));
+      __syncwarp();
+      if (on && (same >> lane) == 1u) mine[b] = place + 1;  // the highest lane of its bucket
+      __syncwarp();
+      if (on) to[place] = it[u];
+    }
+  }
+}
+
+// One pass in a cluster: smem holds total[buckets], then count[kSortWarps][buckets].
+template <typename Source>
+__device__ __forceinline__ void cluster_pass(const Source& from, int n, Digit d, int* smem,
+                                             int* warp_sum, Item* to) {
+  const int buckets = d.buckets(), ctas = gridDim.x, rank = blockIdx.x;
+  int *total = smem, *count = smem + buckets;
+  const int64_t per_warp = (static_cast<int64_t>(n) + ctas * kSortWarps * 32 - 1) /
+                           (ctas * kSortWarps * 32) * 32;
+  const Chunk chunk = warp_chunk(n, rank * kSortWarps * per_warp, per_warp);
+  count_items(from, chunk, d, count, total);
+  cluster_arrive();
+  cluster_wait();
+  // a bucket a thread: no digit has more buckets than the CTA threads
+  const int e = threadIdx.x;
+  int all = 0, before = 0;
+  if (e < buckets) {
+    int c[kSortMostCtas];
+#pragma unroll
+    for (int r = 0; r < kSortMostCtas; ++r) c[r] = r < ctas ? load_from_cta(total + e, r) : 0;
+#pragma unroll
+    for (int r = 0; r < kSortMostCtas; ++r) {
+      all += c[r];
+      before += r < rank ? c[r] : 0;
+    }
+  }
+  int sum;
+  const int at = block_scan(all, warp_sum, &sum);
+  if (e < buckets) counts_to_places(count, buckets, e, at + before);
+  __syncthreads();
+  place_items(from, chunk, d, count + (threadIdx.x >> 5) * buckets, to);
+  // the items are there for the other CTAs, and no totals are read any more
+  cluster_arrive();
+  cluster_wait();
+}
+
+struct SortPlan {
+  int n, rows, passes, bits;  // bits of a digit
+  Item* items[2];             // pass p writes items[p % 2]
+};
+
+template <typename IdT>
+__global__ void __launch_bounds__(kSortWarps * 32)
+    token_sort_kernel(const IdT* __restrict__ ids, const SortPlan plan) {
+  extern __shared__ int sort_smem[];
+  __shared__ int warp_sum[kSortWarps];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  cluster_pass(FromIds<IdT>{ids, plan.rows}, plan.n, Digit{0, plan.bits}, sort_smem, warp_sum,
+               plan.items[0]);
+  for (int p = 1; p < plan.passes; ++p)
+    cluster_pass(FromItems{plan.items[(p + 1) & 1]}, plan.n, Digit{p * plan.bits, plan.bits},
+                 sort_smem, warp_sum, plan.items[p & 1]);
+}
+
+// The three launches of a pass: totals[cta][bucket], turned into the bucket's items in the
+// CTAs before, and sums[bucket].
+template <typename Source>
+__global__ void __launch_bounds__(kSortWarps * 32)
+    token_count_kernel(const Source from, int n, Digit d, int* __restrict__ totals) {
+  extern __shared__ int sort_smem[];
+  const int buckets = d.buckets();
+  count_items(from, my_chunk(n), d, sort_smem + buckets, sort_smem);
+  for (int e = threadIdx.x; e < buckets; e += blockDim.x)  // the entries it summed: no barrier
+    totals[static_cast<int64_t>(blockIdx.x) * buckets + e] = sort_smem[e];
+}
+
+// A warp a bucket, lane l over a run of the CTAs.
+__global__ void __launch_bounds__(256)
+    token_scan_kernel(int* __restrict__ totals, int ctas, int buckets, int* __restrict__ sums) {
+  constexpr int kMost = (kGridCtas + 31) / 32;
+  const int b = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (b >= buckets) return;
+  const int per = (ctas + 31) / 32;
+  int v[kMost], sum = 0;
+#pragma unroll
+  for (int j = 0; j < kMost; ++j) {
+    const int c = lane * per + j;
+    v[j] = j < per && c < ctas ? totals[static_cast<int64_t>(c) * buckets + b] : 0;
+    sum += v[j];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kAll, incl, o);
+    if (lane >= o) incl += y;
+  }
+  int at = incl - sum;
+#pragma unroll
+  for (int j = 0; j < kMost; ++j) {
+    const int c = lane * per + j;
+    if (j < per && c < ctas) totals[static_cast<int64_t>(c) * buckets + b] = at;
+    at += v[j];
+  }
+  if (lane == 31) sums[b] = incl;
+}
+
+template <typename Source>
+__global__ void __launch_bounds__(kSortWarps * 32)
+    token_place_kernel(const Source from, int n, Digit d, const int* __restrict__ totals,
+                       const int* __restrict__ sums, Item* __restrict__ to) {
+  extern __shared__ int sort_smem[];
+  __shared__ int warp_sum[kSortWarps];
+  const int buckets = d.buckets(), e = threadIdx.x;
+  int* count = sort_smem + buckets;
+  const Chunk chunk = my_chunk(n);
+  count_items(from, chunk, d, count, sort_smem);
+  int sum;
+  const int at = block_scan(e < buckets ? sums[e] : 0, warp_sum, &sum);
+  if (e < buckets)
+    counts_to_places(count, buckets, e,
+                     at + totals[static_cast<int64_t>(blockIdx.x) * buckets + e]);
+  __syncthreads();
+  place_items(from, chunk, d, count + (threadIdx.x >> 5) * buckets, to);
+}
+
+// ------------------------------------------------------------------ gradient
+//
+// The sorted items are cut into pieces of `piece` places.  A group of threads sums a piece's
+// runs of equal rows, a vector of columns a thread, and writes the rows whose run lies
+// within the piece.  A run that crosses pieces leaves its part in each: slot 0 where it
+// began before the piece, slot 1 where it begins in it and goes on.  A second launch adds
+// those parts in the pieces' order.  Rows without tokens are cleared before.
+constexpr int kLeastPiece = 32;
+constexpr int kMostPieces = 4096;
+constexpr int kRowsInFlight = 8;
+constexpr int kJoinSegments = 8;
+
+struct SumArgs {
+  const void* grad_out;
+  const Item* items;
+  void* out;
+  float* parts;  // [pieces][2][part_width]
+  int64_t grad_stride, out_stride;
+  int n, rows, width, part_width, piece;
+  float scale;
+  bool accumulate;
+};
+
+__device__ __forceinline__ Item item_at(const Item* items, int64_t i) {
+  const int2 v = *reinterpret_cast<const int2*>(items + i);
+  return {v.x, v.y};
+}
+
+// Columns col .. col + V - 1 of a row, zeros from `width` on.
+template <typename T, bool kAligned>
+__device__ __forceinline__ Pack<T, kVec<T>> load_columns(const T* row, int col, int width) {
+  constexpr int V = kVec<T>;
+  // the aligned vectors around an inner one lie within the row
+  if constexpr (kAligned) {
+    return load_vec<T, true>(row + col);
+  } else {
+    if (col >= V && col + 2 * V <= width) return load_vec<T, false>(row + col);
+    Pack<T, V> p;
+#pragma unroll
+    for (int i = 0; i < V; ++i) p.v[i] = col + i < width ? row[col + i] : from_f32<T>(0.f);
+    return p;
+  }
+}
+
+// Rounds N sums into columns col .. of a row of the result.
+template <typename O, int N, bool kAligned>
+__device__ __forceinline__ void store_sums(const SumArgs& P, int row, int col,
+                                           const float (&sum)[N]) {
+  O* to = static_cast<O*>(P.out) + static_cast<int64_t>(row) * P.out_stride + col;
+  if constexpr (kAligned) {
+#pragma unroll
+    for (int c = 0; c < N; c += kVec<O>) {
+      float f[kVec<O>] = {};
+      if (P.accumulate) to_floats<O>(*reinterpret_cast<const Pack<O, kVec<O>>*>(to + c), f);
+#pragma unroll
+      for (int i = 0; i < kVec<O>; ++i) f[i] = fmaf(P.scale, sum[c + i], f[i]);
+      store_vec(to + c, from_floats<O>(f));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (col + i < P.width)
+        to[i] = from_f32<O>(fmaf(P.scale, sum[i], P.accumulate ? to_f32(to[i]) : 0.f));
+  }
+}
+
+template <typename T, typename O, bool kAligned>
+__global__ void __launch_bounds__(kMoveThreads)
+    embed_sum_kernel(const SumArgs P, int log_group) {
+  constexpr int V = kVec<T>;
+  const int size = 1 << log_group, t = threadIdx.x & (size - 1);
+  const int64_t piece = static_cast<int64_t>(blockIdx.x) * (kMoveThreads >> log_group) +
+                        (threadIdx.x >> log_group);
+  const int col = (blockIdx.y * size + t) * V;
+  const int64_t first = piece * P.piece;
+  if (first >= P.n || col >= P.width) return;
+  const int64_t last = first + P.piece < P.n ? first + P.piece : P.n;
+  int run = item_at(P.items, first).row;
+  if (run >= P.rows) return;
+  bool open = first > 0 && item_at(P.items, first - 1).row == run;  // it began before
+  float* parts = P.parts + piece * 2 * P.part_width + col;
+  const T* grad = static_cast<const T*>(P.grad_out);
+  float sum[V] = {};
+  const auto leave = [&](int slot) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4)
+      *reinterpret_cast<float4*>(parts + slot * P.part_width + i) =
+          make_float4(sum[i], sum[i + 1], sum[i + 2], sum[i + 3]);
+  };
+  for (int64_t i0 = first; i0 < last; i0 += kRowsInFlight) {
+    Item it[kRowsInFlight];
+    Pack<T, V> v[kRowsInFlight];
+#pragma unroll
+    for (int u = 0; u < kRowsInFlight; ++u) {
+      it[u] = i0 + u < last ? item_at(P.items, i0 + u) : Item{P.rows, 0};
+      if (it[u].row < P.rows)
+        v[u] = load_columns<T, kAligned>(grad + it[u].token * P.grad_stride, col, P.width);
+    }
+#pragma unroll
+    for (int u = 0; u < kRowsInFlight; ++u) {
+      if (i0 + u >= last) break;
+      if (it[u].row != run) {
+        if (open) leave(0);
+        else store_sums<O, V, kAligned>(P, run, col, sum);
+        open = false;
+        run = it[u].row;
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[i] = 0.f;
+      }
+      if (run >= P.rows) return;
+      float f[V];
+      to_floats<T>(v[u], f);
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum[i] += f[i];
+    }
+  }
+  if (open) leave(0);
+  else if (last < P.n && item_at(P.items, last).row == run) leave(1);
+  else store_sums<O, V, kAligned>(P, run, col, sum);
+}
+
+// Adds the parts of the run that begins in piece blockIdx.x and crosses its end, if there is
+// one: 32 threads a vector of four columns each, the pieces shared by eight segments of them.
+template <typename O>
+__global__ void __launch_bounds__(32 * kJoinSegments) embed_join_kernel(const SumArgs P) {
+  __shared__ float4 sums[kJoinSegments][32];
+  const int64_t piece = blockIdx.x;
+  const int64_t first = piece * P.piece, end = first + P.piece;
+  if (end >= P.n) return;
+  const int run = item_at(P.items, end).row;
+  if (run >= P.rows || item_at(P.items, end - 1).row != run ||
+      (first > 0 && item_at(P.items, first - 1).row == run))
+    return;
+  const int col = (blockIdx.y * 32 + threadIdx.x) * 4;
+  const bool on = col < P.part_width;
+  const auto part = [&](int64_t p, int slot) {
+    return *reinterpret_cast<const float4*>(P.parts + (p * 2 + slot) * P.part_width + col);
+  };
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  const auto add = [&](float4 v) { s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w; };
+#pragma unroll 4
+  for (int64_t p = piece + 1 + threadIdx.y;
+       p * P.piece < P.n && item_at(P.items, p * P.piece).row == run; p += kJoinSegments)
+    if (on) add(part(p, 0));
+  sums[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.y || !on) return;
+  s = part(piece, 1);
+#pragma unroll
+  for (int i = 0; i < kJoinSegments; ++i) add(sums[i][threadIdx.x]);
+  const float v[4] = {s.x, s.y, s.z, s.w};
+  store_sums<O, 4, false>(P, run, col, v);
+}
+
+// Zeros: rows of `bytes` bytes, `pitch` apart, the last of `last` bytes; `unit` bytes divide
+// them all.  May run beside the sort, whose end it waits for before its own.
+__global__ void __launch_bounds__(kMoveThreads)
+    clear_kernel(char* p, int64_t rows, int64_t bytes, int64_t pitch, int64_t last, int unit) {
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    char* row = p + r * pitch;
+    char* end = row + (r + 1 < rows ? bytes : last);
+    char* lo = row + (-reinterpret_cast<uintptr_t>(row) & 15);
+    if (lo > end) lo = end;
+    char* hi = lo + ((end - lo) & ~int64_t(15));
+    for (char* q = lo + threadIdx.x * 16; q < hi; q += kMoveThreads * 16)
+      *reinterpret_cast<uint4*>(q) = make_uint4(0, 0, 0, 0);
+    const int64_t ends = (lo - row) + (end - hi);  // less than 32 bytes
+    if (static_cast<int64_t>(threadIdx.x) * unit < ends) {
+      const int64_t at = threadIdx.x * unit;
+      char* q = at < lo - row ? row + at : hi + (at - (lo - row));
+      if (unit == 2) *reinterpret_cast<uint16_t*>(q) = 0;
+      else *reinterpret_cast<uint32_t*>(q) = 0;
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// -------------------------------------------------------------- host
+
+constexpr int64_t kMost = INT32_MAX - 1024;  // tokens and rows, counted in 32 bits
+constexpr int64_t kMostWidth = int64_t(1) << 20;
+
+int log2_up(int64_t n) {
+  int lg = 0;
+  while ((int64_t(1) << lg) < n) ++lg;
+  return lg;
+}
+
+SortPlan plan_of(int64_t tokens, int64_t rows) {
+  SortPlan p = {};
+  p.n = static_cast<int>(tokens);
+  p.rows = static_cast<int>(rows);
+  const int bits = std::max(1, log2_up(rows + 1));  // of the rows and the one past them
+  p.passes = (bits + kDigitBits - 1) / kDigitBits;
+  p.bits = (bits + p.passes - 1) / p.passes;
+  return p;
+}
+
+int64_t piece_of(int64_t tokens) {
+  int64_t piece = kLeastPiece;
+  while (piece * kMostPieces < tokens) piece *= 2;
+  return piece;
+}
+
+// The workspace's parts, in bytes from its start.
+struct Layout {
+  int64_t items[2], totals, sums, parts, bytes;
+};
+Layout layout_of(int64_t tokens, int64_t width) {
+  const auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
+  Layout l;
+  l.items[0] = 0;
+  l.items[1] = up(tokens * 8);
+  l.totals = l.items[1] + up(tokens * 8);
+  l.sums = l.totals + (tokens > kOneLaunch ? up(int64_t(kGridCtas) * 4 << kDigitBits) : 0);
+  l.parts = l.sums + (tokens > kOneLaunch ? up(int64_t(4) << kDigitBits) : 0);
+  const int64_t pieces = (tokens + piece_of(tokens) - 1) / piece_of(tokens);
+  l.bytes = l.parts + pieces * 2 * ((width + 7) / 8 * 8) * 4;
+  return l;
+}
+
+tbe_status check_sizes(int64_t tokens, int64_t rows, int64_t width) {
+  if (tokens < 0 || rows < 0 || width < 0) return TBE_EINVAL;
+  return tokens >= kMost || rows >= kMost || width > kMostWidth ? TBE_EUNSUPPORTED : TBE_OK;
+}
+
+bool check_ids(const void* ids, int32_t dtype, int64_t tokens) {
+  return !tokens || (ids && aligned_to(ids, dtype == TBE_DT_I32 ? 4 : 8));
+}
+
+cudaError_t room_for(const void* kernel, size_t smem) {
+  return smem <= 48 * 1024 ? cudaSuccess
+                           : cudaFuncSetAttribute(kernel,
+                                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                  static_cast<int>(smem));
+}
+
+template <typename IdT>
+tbe_status sort_in_cluster(const IdT* ids, const SortPlan& plan, cudaStream_t s) {
+  const auto kernel = token_sort_kernel<IdT>;
+  int ctas = 1;
+  while (ctas < kSortMostCtas && plan.n > ctas * kTokensPerCta) ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kSortWarps * 32);
+  cfg.dynamicSmemBytes = static_cast<size_t>(kSortWarps + 1) * 4 << plan.bits;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (room_for(reinterpret_cast<const void*>(kernel),
+               static_cast<size_t>(kSortWarps + 1) * 4 << kDigitBits) != cudaSuccess ||
+      (ctas > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                        1) != cudaSuccess) ||
+      cudaLaunchKernelEx(&cfg, kernel, ids, plan) != cudaSuccess)
+    return TBE_ECUDA;
+  return launched();
+}
+
+template <typename Source>
+tbe_status sort_pass(const Source& from, const SortPlan& plan, int p, int* totals, int* sums,
+                     cudaStream_t s) {
+  const Digit d = {p * plan.bits, plan.bits};
+  const int buckets = 1 << plan.bits, ctas = std::min(plan.n / kGridChunk, kGridCtas);
+  const size_t smem = static_cast<size_t>(kSortWarps + 1) * 4 << plan.bits;
+  const size_t most = static_cast<size_t>(kSortWarps + 1) * 4 << kDigitBits;
+  if (room_for(reinterpret_cast<const void*>(token_count_kernel<Source>), most) != cudaSuccess ||
+      room_for(reinterpret_cast<const void*>(token_place_kernel<Source>), most) != cudaSuccess)
+    return TBE_ECUDA;
+  token_count_kernel<Source><<<ctas, kSortWarps * 32, smem, s>>>(from, plan.n, d, totals);
+  note_launch();
+  token_scan_kernel<<<(buckets + 7) / 8, 256, 0, s>>>(totals, ctas, buckets, sums);
+  note_launch();
+  token_place_kernel<Source>
+      <<<ctas, kSortWarps * 32, smem, s>>>(from, plan.n, d, totals, sums, plan.items[p & 1]);
+  return launched();
+}
+
+template <typename IdT>
+tbe_status sort_in_grid(const IdT* ids, const SortPlan& plan, int* totals, int* sums,
+                        cudaStream_t s) {
+  tbe_status st = sort_pass(FromIds<IdT>{ids, plan.rows}, plan, 0, totals, sums, s);
+  for (int p = 1; st == TBE_OK && p < plan.passes; ++p)
+    st = sort_pass(FromItems{plan.items[(p + 1) & 1]}, plan, p, totals, sums, s);
+  return st;
+}
+
+// Zeros in a matrix; with `beside` the launch may begin before the kernel ahead of it ends.
+tbe_status clear(void* p, int64_t rows, int64_t width, int64_t stride, int bytes, bool beside,
+                 cudaStream_t s) {
+  int64_t row = width * bytes, pitch = stride * bytes, last = row;
+  if (pitch == row) {  // one block of memory: rows of 32 KB
+    const int64_t all = rows * row;
+    pitch = row = 32768;
+    rows = (all + row - 1) / row;
+    last = all - (rows - 1) * row;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(rows, 152 * 8)));
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = beside ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, clear_kernel, static_cast<char*>(p), rows, row, pitch, last,
+                         bytes) != cudaSuccess)
+    return TBE_ECUDA;
+  return launched();
+}
+
+}  // namespace
+}  // namespace tbe
+
+using namespace tbe;
+
+extern "C" tbe_status tbe_embed(const void* table, int32_t dtype, int64_t rows, int64_t width,
+                                int64_t table_stride, const void* ids, int32_t index_dtype,
+                                int64_t tokens, float scale, void* out, int64_t out_stride,
+                                void* stream) {
+  const tbe_status bad = check_sizes(tokens, rows, width);
+  if (bad != TBE_OK) return bad;
+  if (!dtype_bytes(dtype) || (index_dtype != TBE_DT_I32 && index_dtype != TBE_DT_I64))
+    return TBE_EUNSUPPORTED;
+  if (!std::isfinite(scale)) return TBE_EINVAL;
+  if (!tokens || !width) return TBE_OK;
+  const int b = dtype_bytes(dtype);
+  const Matrix in = {table, table_stride, b}, to = {out, out_stride, b};
+  if ((rows && !in.good(rows, width)) || !to.good(tokens, width) ||
+      !check_ids(ids, index_dtype, tokens) ||
+      overlap(in.span(rows, width), to.span(tokens, width)) ||
+      overlap(run_of(ids, tokens * (index_dtype == TBE_DT_I32 ? 4 : 8)), to.span(tokens, width)))
+    return TBE_EINVAL;
+  const bool vec = (!rows || in.vectors(width, 16)) && to.vectors(width, 16);
+  return for_dtype(dtype, [&](auto t) {
+    using T = decltype(t);
+    const auto go = [&](auto aligned, auto* p) {
+      constexpr bool kAligned = decltype(aligned)::value;
+      using IdT = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
+      // A thread for each vector while the tokens are few and latency counts, one for four
+      // once they fill the GPU.
+      int64_t places = (width + kVec<T> - 1) / kVec<T> + (kAligned ? 0 : 1);
+      if (tokens * places > 152 * 2048) places = (places + kInFlight - 1) / kInFlight;
+      const int lg = std::min(log2_up(places), 8);
+      const int per = kMoveThreads >> lg;
+      embed_kernel<T, IdT, kAligned>
+          <<<static_cast<unsigned>((tokens + per - 1) / per), kMoveThreads, 0,
+             static_cast<cudaStream_t>(stream)>>>(
+              static_cast<const T*>(table), static_cast<int>(rows), static_cast<int>(width),
+              table_stride, p, static_cast<int>(tokens), scale, static_cast<T*>(out), out_stride,
+              lg);
+      return launched();
+    };
+    const auto with_ids = [&](auto aligned) {
+      return index_dtype == TBE_DT_I32 ? go(aligned, static_cast<const int32_t*>(ids))
+                                       : go(aligned, static_cast<const int64_t*>(ids));
+    };
+    return vec ? with_ids(std::true_type{}) : with_ids(std::false_type{});
+  });
+}
+
+extern "C" tbe_status tbe_embed_workspace_size(int64_t tokens, int64_t rows, int64_t width,
+                                               size_t* bytes) {
+  if (!bytes) return TBE_EINVAL;
+  const tbe_status bad = check_sizes(tokens, rows, width);
+  if (bad != TBE_OK) return bad;
+  *bytes = static_cast<size_t>(layout_of(tokens, width).bytes);
+  return TBE_OK;
+}
+
+extern "C" tbe_status tbe_embed_backward(const void* grad_out, int32_t dtype, int64_t tokens,
+                                         int64_t width, int64_t grad_out_stride, const void* ids,
+                                         int32_t index_dtype, int64_t rows, float scale,
+                                         int32_t accumulate, void* grad_table, int32_t out_dtype,
+                                         int64_t grad_table_stride, void* workspace,
+                                         size_t ws_bytes, void* stream) {
+  const tbe_status bad = check_sizes(tokens, rows, width);
+  if (bad != TBE_OK) return bad;
+  if (!dtype_bytes(dtype) || (out_dtype != dtype && out_dtype != TBE_DT_F32) ||
+      (index_dtype != TBE_DT_I32 && index_dtype != TBE_DT_I64))
+    return TBE_EUNSUPPORTED;
+  if (!std::isfinite(scale)) return TBE_EINVAL;
+  if (!rows || !width || (!tokens && accumulate)) return TBE_OK;
+  const int b = dtype_bytes(dtype), ob = dtype_bytes(out_dtype);
+  const Matrix in = {grad_out, grad_out_stride, b}, to = {grad_table, grad_table_stride, ob};
+  if ((tokens && !in.good(tokens, width)) || !to.good(rows, width) ||
+      !check_ids(ids, index_dtype, tokens))
+    return TBE_EINVAL;
+  const Layout l = layout_of(tokens, width);
+  if (tokens && (!workspace || ws_bytes < static_cast<size_t>(l.bytes) || !aligned_to(workspace, 16)))
+    return TBE_EWORKSPACE;
+  const Bytes id_run = run_of(ids, tokens * (index_dtype == TBE_DT_I32 ? 4 : 8));
+  const Bytes ws = run_of(tokens ? workspace : nullptr, l.bytes);
+  const Bytes read = in.span(tokens, width), written = to.span(rows, width);
+  if (overlap(written, read) || overlap(written, id_run) || overlap(written, ws) ||
+      overlap(ws, read) || overlap(ws, id_run))
+    return TBE_EINVAL;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!tokens) return clear(grad_table, rows, width, grad_table_stride, ob, false, s);
+  char* w = static_cast<char*>(workspace);
+  SortPlan plan = plan_of(tokens, rows);
+  plan.items[0] = reinterpret_cast<Item*>(w + l.items[0]);
+  plan.items[1] = reinterpret_cast<Item*>(w + l.items[1]);
+  const bool in_cluster = tokens <= kOneLaunch;
+  const auto sort = [&](auto* p) {
+    return in_cluster ? sort_in_cluster(p, plan, s)
+                      : sort_in_grid(p, plan, reinterpret_cast<int*>(w + l.totals),
+                                     reinterpret_cast<int*>(w + l.sums), s);
+  };
+  tbe_status st = index_dtype == TBE_DT_I32 ? sort(static_cast<const int32_t*>(ids))
+                                            : sort(static_cast<const int64_t*>(ids));
+  // The clearing runs beside the cluster, which leaves most of the GPU idle.
+  if (st == TBE_OK && !accumulate)
+    st = clear(grad_table, rows, width, grad_table_stride, ob, in_cluster, s);
+  if (st != TBE_OK) return st;
+  const int64_t piece = piece_of(tokens), pieces = (tokens + piece - 1) / piece;
+  const SumArgs args = {grad_out, plan.items[(plan.passes + 1) & 1], grad_table,
+                        reinterpret_cast<float*>(w + l.parts), grad_out_stride, grad_table_stride,
+                        static_cast<int>(tokens), static_cast<int>(rows), static_cast<int>(width),
+                        static_cast<int>((width + 7) / 8 * 8), static_cast<int>(piece), scale,
+                        accumulate != 0};
+  return for_dtype(dtype, [&](auto t) {
+    using T = decltype(t);
+    const auto go = [&](auto aligned, auto o) {
+      constexpr bool kAligned = decltype(aligned)::value;
+      using O = decltype(o);
+      const int64_t places = (width + kVec<T> - 1) / kVec<T>;
+      const int lg = std::min(log2_up(places), 8);
+      const int per = kMoveThreads >> lg;
+      const dim3 grid(static_cast<unsigned>((pieces + per - 1) / per),
+                      static_cast<unsigned>((places + (1 << lg) - 1) >> lg));
+      embed_sum_kernel<T, O, kAligned><<<grid, kMoveThreads, 0, s>>>(args, lg);
+      note_launch();
+      if (pieces > 1)
+        embed_join_kernel<O><<<dim3(static_cast<unsigned>(pieces - 1),
+                                    static_cast<unsigned>((width + 127) / 128)),
+                               dim3(32, kJoinSegments), 0, s>>>(args);
+      return launched();
+    };
+    const auto to_type = [&](auto aligned) {
+      return out_dtype == dtype ? go(aligned, T{}) : go(aligned, float{});
+    };
+    const bool vec = in.vectors(width, 16) && to.vectors(width, 16);
+    return vec ? to_type(std::true_type{}) : to_type(std::false_type{});
+  });
+}

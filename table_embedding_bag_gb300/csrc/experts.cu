@@ -5,12 +5,11 @@
 
 #include "internal.h"
 #include "rows.cuh"
+#include "sort.cuh"
 #include "tbe_experts.h"
 
 namespace tbe {
 namespace {
-
-constexpr unsigned kAll = 0xffffffffu;
 
 // ---------------------------------------------------------------------- sort
 //
@@ -27,10 +26,8 @@ constexpr unsigned kAll = 0xffffffffu;
 // CTA writes last.  Both measured (64 experts): 65536 assignments 9.0 us in one
 // launch and 11.8 in three, 131072 13.3 and 13.2, 262144 21.7 and 12.6, a million 70
 // and 25 us.
-constexpr int kSortWarps = 32;
 constexpr int kSortUnroll = 4;      // rounds of 32 assignments whose loads are in flight
 constexpr int kSortPerCta = 2048;   // assignments from which another CTA pays
-constexpr int kSortMostCtas = 16;
 constexpr int kSortOneLaunch = 131072;
 constexpr int kSortGridChunk = 4096;  // assignments of a CTA of three launches, at least
 constexpr int kSortGridCtas = 304;
@@ -40,30 +37,6 @@ static_assert(kSortGridChunk > TBE_MAX_EXPERTS, "a CTA's totals fit its part of 
 template <typename IdT>
 __device__ __forceinline__ int expert_of(IdT e, int experts) {
   return e >= 0 && e < static_cast<IdT>(experts) ? static_cast<int>(e) : experts;
-}
-
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-__device__ __forceinline__ int load_from_cta(const int* p, int rank) {
-  const unsigned addr = static_cast<unsigned>(__cvta_generic_to_shared(p));
-  unsigned remote;
-  int v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
-  return v;
-}
-
-// Assignments [first, last) of a warp.
-struct Chunk {
-  int64_t first, last;
-};
-__device__ __forceinline__ Chunk warp_chunk(int64_t n, int64_t cta_first, int64_t per_warp) {
-  const int64_t first = cta_first + (threadIdx.x >> 5) * per_warp;
-  return {first, first + per_warp < n ? first + per_warp : n};
 }
 
 // Every warp's counts of its chunk, count[warp][expert], and their sums over
@@ -89,16 +62,6 @@ __device__ __forceinline__ void count_chunks(const IdT* ids, Chunk c, int expert
 #pragma unroll 16
     for (int w = 0; w < kSortWarps; ++w) sum += count[w * buckets + e];
     total[e] = sum;
-  }
-}
-
-// Turns expert e's counts into every warp's first place, from `at` on.
-__device__ __forceinline__ void counts_to_places(int* count, int buckets, int e, int at) {
-#pragma unroll 16
-  for (int w = 0; w < kSortWarps; ++w) {
-    const int c = count[w * buckets + e];
-    count[w * buckets + e] = at;
-    at += c;
   }
 }
 
@@ -130,29 +93,6 @@ __device__ __forceinline__ void rank_chunk(const IdT* ids, Chunk c, int experts,
       }
     }
   }
-}
-
-// Exclusive scan over the CTA's threads, and the sum; kSortWarps warps.
-__device__ __forceinline__ int block_scan(int v, int* warp_sum, int* sum) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int incl = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(kAll, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) warp_sum[warp] = incl;
-  __syncthreads();
-  int sums = warp_sum[lane];  // scanned by every warp
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(kAll, sums, o);
-    if (lane >= o) sums += y;
-  }
-  const int before = warp ? __shfl_sync(kAll, sums, warp - 1) : 0;
-  *sum = __shfl_sync(kAll, sums, 31);
-  __syncthreads();
-  return before + incl - v;
 }
 
 template <typename IdT>
@@ -210,17 +150,6 @@ __global__ void __launch_bounds__(kSortWarps * 32)
 // The three launches.  The CTAs have equal parts of the assignments (the first n % ctas one
 // more), and a CTA's totals, then its first places, stand at the start of its part of position
 // until it ranks them.
-__device__ __forceinline__ int64_t cta_first(int n, int c, int ctas) {
-  const int rest = n % ctas;
-  return static_cast<int64_t>(n / ctas) * c + (c < rest ? c : rest);
-}
-__device__ __forceinline__ Chunk my_chunk(int n) {
-  const int64_t first = cta_first(n, blockIdx.x, gridDim.x);
-  const int64_t last = cta_first(n, blockIdx.x + 1, gridDim.x);
-  const int64_t per_warp = (last - first + kSortWarps * 32 - 1) / (kSortWarps * 32) * 32;
-  return warp_chunk(last, first, per_warp);
-}
-
 template <typename IdT>
 __global__ void __launch_bounds__(kSortWarps * 32)
     expert_count_kernel(const IdT* __restrict__ ids, int n, int experts,

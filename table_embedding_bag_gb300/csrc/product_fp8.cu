@@ -1,12 +1,11 @@
 // 8-bit rows and weights with a scale for each block of 128, and the experts'
 // products on them.  The operations are specified in include/tbe_experts.h.
 #include <cuda.h>
-#include <cuda_fp8.h>
-
 #include <type_traits>
 
 #include "internal.h"
 #include "product_form.h"
+#include "quantize.cuh"
 #include "rows.cuh"
 #include "tbe_experts.h"
 #include "tcgen05.cuh"
@@ -14,45 +13,9 @@
 namespace tbe {
 namespace {
 
-constexpr int kBlock = TBE_SCALE_BLOCK;
-constexpr float kInvMax = 1.f / 448.f;  // one over the largest e4m3 value, rounded to fp32
-constexpr float kTinyScale = 0x1p-126f;
 // Rows and columns are counted in 32 bits, and a block or a tile that begins inside a matrix may
 // end past it.
 constexpr int64_t kMostRows = INT32_MAX - 512;
-
-__device__ __forceinline__ float block_scale(float amax) {
-  return fmaxf(amax * kInvMax, kTinyScale);
-}
-
-__device__ __forceinline__ uint2 to_e4m3(const float (&v)[8], float f) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * f, v[2 * i + 1] * f), __NV_SATFINITE,
-                                    __NV_E4M3);
-  return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
-}
-
-// e4m3(x / s) of eight values, as a division in fp32 gives it.  The quotient lies
-// between x times a little less and a little more than 1 / s (2^-21 of it is more than
-// the errors on the way add up to: 2^-23 of the approximate reciprocal and three
-// roundings of 2^-24), and rounding is monotonic, so where both give the same e4m3
-// values the quotients do too.  Where they differ (one lane in some thousands) the values
-// are divided.  (8192 x 1024 bf16 to four places: 15.0 us, with divisions throughout 17.2.)
-__device__ __forceinline__ Pack<uint8_t, 8> quantized(const float (&x)[8], float s) {
-  float inv;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-  uint2 q = to_e4m3(x, inv * (1.f - 0x1p-21f));
-  const uint2 more = to_e4m3(x, inv * (1.f + 0x1p-21f));
-  if (q.x != more.x || q.y != more.y) {
-    float d[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) d[i] = __fdiv_rn(x[i], s);
-    q = to_e4m3(d, 1.f);
-  }
-  return *reinterpret_cast<const Pack<uint8_t, 8>*>(&q);
-}
 
 // Eight consecutive values of a row.
 template <typename T>

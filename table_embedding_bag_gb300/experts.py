@@ -1,5 +1,6 @@
-"""Binding of the expert-layer operators (include/tbe_experts.h): sort, dispatch
-and combine with their gradients, 8-bit quantising, and the experts' products.
+"""Binding of the expert-layer operators (include/tbe_experts.h): routing, sort,
+dispatch and combine with their gradients, 8-bit quantising, and the experts'
+products.
 
 As in the rest of the package the functions only check and marshal their
 arguments.  A call runs on the device of its tensors, which must all be on one,
@@ -16,19 +17,27 @@ import ctypes
 import torch
 
 __all__ = [
-    "tbe_expert_sort", "tbe_expert_dispatch", "tbe_expert_dispatch_fp8", "tbe_expert_combine",
+    "tbe_expert_route", "tbe_expert_route_backward", "tbe_expert_sort", "tbe_expert_dispatch", "tbe_expert_dispatch_fp8", "tbe_expert_combine",
     "tbe_expert_combine_backward", "tbe_expert_dispatch_backward", "tbe_quantize_rows",
-    "tbe_quantize_weights", "tbe_expert_product", "TBE_MAX_EXPERTS", "TBE_SCALE_BLOCK",
+    "tbe_quantize_weights", "tbe_expert_product", "TBE_MAX_EXPERTS", "TBE_MAX_CHOSEN",
+    "TBE_SCALE_BLOCK",
 ]
 
 TBE_MAX_EXPERTS = 1024
+TBE_MAX_CHOSEN = 31
 TBE_SCALE_BLOCK = 128
+_SCORE = {"softmax": 1, "sigmoid": 2}
 _ROW_DT = {torch.float16: 1, torch.bfloat16: 4, torch.float32: 5}
 _ID_DT = {torch.int32: 2, torch.int64: 3}
 
 
 def configure(lib):
     P, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+    f32 = ctypes.c_float
+    lib.tbe_expert_route.argtypes = [P, i32, i64, i32, i64, P, i32, i32, i32, i32, i32, i32, f32,
+                                     P, i32, P, P]
+    lib.tbe_expert_route_backward.argtypes = [P, P, i32, i64, i32, i64, P, i32, i32, i32, i32, f32,
+                                              P, i64, P]
     lib.tbe_expert_sort.argtypes = [P, i32, i64, i32, i32, P, P, P, P]
     lib.tbe_expert_dispatch.argtypes = [P, i32, i64, i32, i64, i64, P, i32, P, P, i64, P]
     lib.tbe_expert_dispatch_fp8.argtypes = [P, i32, i64, i32, i64, i64, P, i32, P, P, i64, P, P]
@@ -37,7 +46,7 @@ def configure(lib):
                                                 P, i64, P, P]
     lib.tbe_quantize_weights.argtypes = [P, i32, i64, i64, i64, P, P, P]
     lib.tbe_expert_product.argtypes = [P, i64, P, P, P, P, i64, i64, i64, i32, P, i32, i64, P, P]
-    for f in ("sort", "dispatch", "dispatch_fp8", "combine", "combine_backward", "product"):
+    for f in ("route", "route_backward", "sort", "dispatch", "dispatch_fp8", "combine", "combine_backward", "product"):
         getattr(lib, f"tbe_expert_{f}").restype = ctypes.c_int
     lib.tbe_quantize_weights.restype = ctypes.c_int
 
@@ -159,6 +168,102 @@ def _experts(offsets, device):
     if offsets.get_device() != device or device < 0:
         _refuse_device(offsets, "offsets", device)
     return n
+
+
+_sizes = {}  # bytes that a size function gave, by its arguments
+
+
+def _workspace(lib, call, sizes, ws, stream, like):
+    """The scratch of a call whose size function is `call`: ws, checked, or a new one."""
+    need = _sizes.get((call, sizes))
+    if need is None:
+        n = ctypes.c_size_t(0)
+        _ok(call, getattr(lib, call)(*sizes, ctypes.byref(n)))
+        if len(_sizes) >= 4096:
+            _sizes.clear()
+        need = _sizes[call, sizes] = n.value
+    if ws is None:
+        return _empty(stream, max(need, 1), torch.uint8, like)
+    if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.numel() < need:
+        raise ValueError(f"ws must be a contiguous uint8 tensor of at least {need} entries")
+    if ws.get_device() != like.get_device():
+        _refuse_device(ws, "ws", like.get_device())
+    return ws
+
+
+def _score(score):
+    if score not in _SCORE:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    return _SCORE[score]
+
+
+def tbe_expert_route(logits, k, bias=None, score="softmax", groups=1, top_groups=1, group_best=1,
+                     renormalize=True, scale=1.0, ids=None, weights=None, stream=None):
+    """Chooses k experts for each row of logits [tokens, experts] and weights them:
+    (ids [tokens, k] int32, or int64 where ids is given so, weights [tokens, k] fp32).
+
+    Scores are the softmax or sigmoid of the logits; the k largest of score + bias (fp32
+    [experts]) are chosen, ties to the lower expert.  groups > 1: of the groups of
+    consecutive experts only the top_groups are open whose group_best (1 or 2) largest sum to
+    most.  A logit or bias of -inf closes an expert; where fewer than k are open the id is -1
+    and the weight 0.  Weights are scale * score, over the chosen scores' sum with
+    renormalize; the bias only chooses."""
+    device = logits.get_device()
+    ls = _matrix(logits, "logits", device, _ROW_DT)
+    tokens, experts = logits.shape
+    if not 1 <= experts <= TBE_MAX_EXPERTS:
+        raise ValueError(f"there must be 1 to {TBE_MAX_EXPERTS} experts")
+    if groups < 1 or experts % groups or not 1 <= top_groups <= groups or groups > 32:
+        raise ValueError("groups must divide the experts, at most 32, with 1 <= top_groups <= "
+                         "groups")
+    if group_best not in (1, 2):
+        raise ValueError("group_best must be 1 or 2")
+    if not 1 <= k <= min(TBE_MAX_CHOSEN, top_groups * (experts // groups)):
+        raise ValueError(f"k must lie in [1, {TBE_MAX_CHOSEN}] and within the open groups' experts")
+    if bias is not None:
+        _dense(bias, "bias", device, torch.float32, (experts,))
+    if ids is None:
+        ids = _empty(stream, (tokens, k), torch.int32, logits)
+    else:
+        if ids.dtype not in _ID_DT:
+            raise TypeError("ids must be int32 or int64")
+        _dense(ids, "ids", device, ids.dtype, (tokens, k))
+    if weights is None:
+        weights = _empty(stream, (tokens, k), torch.float32, logits)
+    else:
+        _dense(weights, "weights", device, torch.float32, (tokens, k))
+    _ok("tbe_expert_route", _lib(device).tbe_expert_route(
+        logits.data_ptr(), _ROW_DT[logits.dtype], tokens, experts, ls,
+        None if bias is None else bias.data_ptr(), _score(score), k, groups, top_groups,
+        group_best, bool(renormalize), float(scale), ids.data_ptr(), _ID_DT[ids.dtype],
+        weights.data_ptr(), _stream_of(stream, device)))
+    return ids, weights
+
+
+def tbe_expert_route_backward(grad_weights, logits, ids, score="softmax", renormalize=True,
+                              scale=1.0, out=None, stream=None):
+    """Gradient of tbe_expert_route's weights in the logits, for the ids it chose (the
+    choice itself has none): [tokens, experts] of logits' type."""
+    device = logits.get_device()
+    ls = _matrix(logits, "logits", device, _ROW_DT)
+    tokens, experts = logits.shape
+    if ids.dtype not in _ID_DT:
+        raise TypeError("ids must be int32 or int64")
+    if ids.dim() != 2 or not 1 <= ids.shape[1] <= TBE_MAX_CHOSEN:
+        raise ValueError(f"ids must have the shape [tokens, k], k from 1 to {TBE_MAX_CHOSEN}")
+    k = ids.shape[1]
+    _dense(ids, "ids", device, ids.dtype, (tokens, k))
+    _dense(grad_weights, "grad_weights", device, torch.float32, (tokens, k))
+    os_ = experts
+    if out is None:
+        out = _empty(stream, (tokens, experts), logits.dtype, logits)
+    else:
+        os_ = _matrix(out, "out", device, (logits.dtype,), experts, tokens)
+    _ok("tbe_expert_route_backward", _lib(device).tbe_expert_route_backward(
+        grad_weights.data_ptr(), logits.data_ptr(), _ROW_DT[logits.dtype], tokens, experts, ls,
+        ids.data_ptr(), _ID_DT[ids.dtype], k, _score(score), bool(renormalize), float(scale),
+        out.data_ptr(), os_, _stream_of(stream, device)))
+    return out
 
 
 def tbe_expert_sort(ids, num_experts, offsets=None, source=None, position=None, stream=None):
