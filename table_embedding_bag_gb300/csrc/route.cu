@@ -23,30 +23,46 @@ struct RouteArgs {
   float scale;
   bool sigmoid, renormalize, wide_ids;
   bool by_logits;  // the choices' order is that of the logits
+  // how a row's lanes share its experts: `group_lanes` consecutive lanes a group (a power of
+  // two), `lane_experts` consecutive experts of it a lane
+  int group_lanes, lane_experts;
+  bool vectors;  // lane_experts is the kernel's V, and all of a lane's experts exist and are aligned
 };
 
-// Values in their order as integers: 0 for an expert that is closed, NaN above all.
-__device__ __forceinline__ uint32_t order_of(float c) {
-  const uint32_t b = __float_as_uint(c + 0.f);  // -0 is 0
-  if (c != c) return 0xffffffffu;
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
+constexpr float kClosed = -INFINITY;  // as a choice
+
+// Choices in 64 bits in their order as integers: NaN above all, 0 for a closed expert is
+// the caller's.
 __device__ __forceinline__ unsigned long long order_of(double c) {
   const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(c + 0.0));
   if (c != c) return ~0ull;
   return b >> 63 ? ~b : b | 1ull << 63;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
+// Over the L lanes (a power of two) that share a row.  Maxima pass over NaN.
+template <int L>
+__device__ __forceinline__ float row_max(float v) {
+  if constexpr (L == 32) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+  } else {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+    for (int o = L / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+    return v;
+  }
+}
+template <int L, typename F>
+__device__ __forceinline__ F row_sum(F v) {
+#pragma unroll
+  for (int o = L / 2; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
   return v;
 }
-template <typename F>
-__device__ __forceinline__ F warp_sum(F v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-  return v;
+// Whether a lane of this one's row says so.
+template <int L>
+__device__ __forceinline__ bool row_any(bool v) {
+  const unsigned all = __ballot_sync(kAll, v);
+  return (all >> (threadIdx.x & 31 & ~(L - 1)) & (kAll >> (32 - L))) != 0;
 }
 
 // What a row's scores need besides the logit: softmax's largest logit and sum.
@@ -58,42 +74,31 @@ __device__ __forceinline__ float score_of(float l, bool sigmoid, RowScale r) {
   return sigmoid ? __fdividef(1.f, 1.f + __expf(-l)) : __fdividef(__expf(l - r.top), r.sum);
 }
 
-// The groups (a bit each) that are worth most: lane g holds group g's worth as an integer in
-// order, 0 where no expert of it is open.
-template <typename Order>
-__device__ __forceinline__ unsigned best_groups(Order mine, int groups, int top) {
-  const int lane = threadIdx.x & 31;
-  int rank = 0;
-  for (int g = 0; g < groups; ++g) {
-    const Order o = __shfl_sync(kAll, mine, g);
-    rank += o > mine || (o == mine && g < lane);
-  }
-  return __ballot_sync(kAll, lane < groups && mine != 0 && rank < top);
-}
-
-// The choice again in 64 bits, without a thought for speed: some rows in a thousand need it.
-// c: room for the row's choices.  Returns lane j's expert, -1 for none.
+// A row's choice again in 64 bits, by the whole warp and without a thought for speed: a few rows in
+// ten thousand need it (see `step` below).  c: room for the row's choices.  Returns lane j's
+// expert, -1 for none.
 template <typename T>
 __device__ __noinline__ int choose_exactly(const RouteArgs& P, const T* logits, double* c) {
   const int lane = threadIdx.x & 31, size = P.experts / P.groups;
-  const double closed = -INFINITY;
-  double top = closed, sum = 0.0;
-  if (!P.sigmoid) {
-    float m = -INFINITY;
+  const double closed = kClosed;
+  double top = 0.0, sum = 1.0;
+  if (!P.sigmoid && !P.by_logits) {
+    float m = kClosed;
     for (int e = lane; e < P.experts; e += 32) m = fmaxf(m, to_f32(logits[e]));
-    top = warp_max(m);
+    top = row_max<32>(m);
+    sum = 0.0;
     for (int e = lane; e < P.experts; e += 32)
       sum += exp(static_cast<double>(to_f32(logits[e])) - top);
-    sum = warp_sum(sum);
+    sum = row_sum<32>(sum);
   }
   for (int e = lane; e < P.experts; e += 32) {
     const double l = to_f32(logits[e]);
-    double v = P.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - top) / sum;
+    double v = P.by_logits ? l : P.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - top) / sum;
     if (P.bias) v += P.bias[e];
     c[e] = l == closed ? closed : v;
   }
   __syncwarp();
-  unsigned open = kAll;
+  unsigned open = kAll;  // groups
   if (P.groups > 1) {
     unsigned long long worth = 0;
     if (lane < P.groups) {
@@ -106,7 +111,12 @@ __device__ __noinline__ int choose_exactly(const RouteArgs& P, const T* logits, 
       if (first != closed)
         worth = order_of(P.group_best > 1 && second != closed ? first + second : first);
     }
-    open = best_groups(worth, P.groups, P.top_groups);
+    int rank = 0;
+    for (int g = 0; g < P.groups; ++g) {
+      const unsigned long long o = __shfl_sync(kAll, worth, g);
+      rank += o > worth || (o == worth && g < lane);
+    }
+    open = __ballot_sync(kAll, worth != 0 && rank < P.top_groups);
   }
   int mine = -1;
   for (int r = 0; r < P.k; ++r) {
@@ -129,71 +139,191 @@ __device__ __noinline__ int choose_exactly(const RouteArgs& P, const T* logits, 
     if (lane == 0) c[at] = closed;
     __syncwarp();
   }
+  __syncwarp();
   return mine;
 }
 
-// Weights of the chosen, before the scale: lane j has expert j's logit, `on` where there is one.
+// Weights of the chosen, before the scale: lane j of a row has the j-th expert's logit, `on`
+// where there is one.
+template <int L>
 __device__ __forceinline__ float weight_of(float l, bool on, bool sigmoid, bool renormalize,
                                            RowScale r) {
   if (!renormalize) {
     if (!on) return 0.f;
     return sigmoid ? __fdiv_rn(1.f, 1.f + expf(-l)) : __fdiv_rn(expf(l - r.top), r.sum);
   }
-  const float top = warp_max(on ? l : -INFINITY);
-  if (!sigmoid && r.sum != r.sum) return on ? r.sum : 0.f;  // a NaN among the row's scores
+  const float top = row_max<L>(on ? l : kClosed);
   // sigmoid(l) is exp(l) to the last bit where no logit is above -60, and exp(l - top) does not
   // underflow
   const float p = !on                        ? 0.f
                   : sigmoid && !(top < -60.f) ? __fdiv_rn(1.f, 1.f + expf(-l))
                                               : expf(l - top);
-  const float sum = warp_sum(p);
-  return on ? __fdiv_rn(p, sum) : 0.f;
+  const float sum = row_sum<L>(p);
+  if (!on) return 0.f;
+  // a NaN among the row's scores makes every softmax weight one
+  return !sigmoid && r.sum != r.sum ? r.sum : __fdiv_rn(p, sum);
 }
 
-// A warp a token: lane i holds the logits of V consecutive experts from i V on.
-template <typename T, int V>
-__global__ void __launch_bounds__(256) route_kernel(const RouteArgs P) {
-  extern __shared__ double route_smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t token = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp;
-  if (token >= P.tokens) return;
-  const T* logits = static_cast<const T*>(P.logits) + token * P.stride;
-  double* room = route_smem + static_cast<int64_t>(warp) * P.experts;
-  const int e0 = lane * V;
-  float l[V];
+// The K experts with the largest choices, in their order: lane j of a row gets the j-th (-1 for
+// none).  Takes what it has chosen out of c.  One expert a round.
+template <int V, int L>
+__device__ __forceinline__ int choose_in_rounds(float (&c)[V], int e0, int K) {
+  const int lane = threadIdx.x & 31, first = lane & ~(L - 1), place = lane & (L - 1);
+  float most = c[0];
 #pragma unroll
-  for (int v = 0; v < V; ++v) l[v] = e0 + v < P.experts ? to_f32(logits[e0 + v]) : -INFINITY;
+  for (int v = 1; v < V; ++v) most = fmaxf(most, c[v]);
+  int mine = -1;
+  for (int r = 0; r < K; ++r) {
+    const float best = row_max<L>(most);
+    const unsigned who = __ballot_sync(kAll, most == best && best != kClosed);
+    if (!who) break;
+    const unsigned row = who >> first & (kAll >> (32 - L));
+    const int winner = row ? __ffs(row) - 1 : -1;
+    int at = 0;
+    if (place == winner) {
+#pragma unroll
+      for (int v = V - 1; v >= 0; --v)
+        if (c[v] == best) at = v;
+      most = kClosed;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (v == at) c[v] = kClosed;
+        most = fmaxf(most, c[v]);
+      }
+      at += e0;
+    }
+    at = __shfl_sync(kAll, at, first + (row ? winner : 0));
+    if (place == r && row) mine = at;
+  }
+  return mine;
+}
+
+struct Candidate {
+  float c;
+  int e;
+};
+
+// The same for a row of a whole warp with many experts a lane.  The K-th largest of the lanes'
+// largest choices bounds the K-th choice from below, so only choices from there on are
+// candidates, a few more than K; they are moved to shared memory, ranked
+// against one another, a lane each, and put in order.  (65536 rows, eight of 256 in four of
+// eight groups with a bias: in rounds a lane must look its V choices over for
+// every expert chosen.)
+template <int V>
+__device__ __forceinline__ int choose_by_bound(float (&c)[V], int e0, int K, Candidate* room) {
+  const int lane = threadIdx.x & 31;
+  float left = c[0];
+#pragma unroll
+  for (int v = 1; v < V; ++v) left = fmaxf(left, c[v]);
+  float bound = kClosed;
+  for (int r = 0; r < K; ++r) {
+    bound = row_max<32>(left);
+    if (left == bound) left = kClosed;
+  }
+  int count = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) count += c[v] >= bound && c[v] != kClosed;
+  int upto = count;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kAll, upto, o);
+    if (lane >= o) upto += y;
+  }
+  const int all = __shfl_sync(kAll, upto, 31);
+  if (all > 32) return choose_in_rounds<V, 32>(c, e0, K);  // many alike, or few lanes open
+  int at = upto - count;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (c[v] >= bound && c[v] != kClosed) room[at++] = {c[v], e0 + v};
+  __syncwarp();
+  const Candidate my = lane < all ? room[lane] : Candidate{kClosed, 0};
+  int rank = 0;
+  for (int j = 0; j < all; ++j) {  // in the order of the experts
+    const float other = room[j].c;
+    rank += other > my.c || (other == my.c && j < lane);
+  }
+  __syncwarp();
+  if (lane < all) room[rank].e = my.e;
+  __syncwarp();
+  const int mine = lane < all && lane < K ? room[lane].e : -1;
+  __syncwarp();
+  return mine;
+}
+
+// A row's experts are shared by L lanes, V consecutive ones a lane at most; 32 / L rows a warp.
+template <typename T, int V, int L>
+__global__ void __launch_bounds__(256) route_kernel(const RouteArgs P) {
+  constexpr int kRows = 32 / L;
+  constexpr bool kBound = L == 32 && V >= 4;
+  extern __shared__ double route_smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, place = lane & (L - 1);
+  const int64_t token0 = (static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp) * kRows;
+  if (token0 >= P.tokens) return;
+  const int64_t token = token0 + lane / L;
+  const bool live = token < P.tokens;
+  const T* logits = static_cast<const T*>(P.logits) + (live ? token : token0) * P.stride;
+  double* room = route_smem + static_cast<int64_t>(warp) * (P.experts + 32);
+
+  // this lane's experts: e0 .. e0 + mine - 1, of its group
+  const int size = P.experts / P.groups, group = place / P.group_lanes;
+  const int in_group = (place & (P.group_lanes - 1)) * P.lane_experts;
+  const int e0 = group * size + in_group;
+  int count = size - in_group < P.lane_experts ? size - in_group : P.lane_experts;
+  if (!live || group >= P.groups) count = 0;
+  float c[V];
+  {
+    constexpr int kPart = V * sizeof(T) < 16 ? V : 16 / static_cast<int>(sizeof(T));
+    if (P.vectors && count > 0) {
+#pragma unroll
+      for (int v = 0; v < V; v += kPart) {
+        const Pack<T, kPart> p = *reinterpret_cast<const Pack<T, kPart>*>(logits + e0 + v);
+#pragma unroll
+        for (int i = 0; i < kPart; ++i) c[v + i] = to_f32(p.v[i]);
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) c[v] = v < count ? to_f32(logits[e0 + v]) : kClosed;
+    }
+  }
 
   RowScale scale = {0.f, 1.f};
   if (!P.sigmoid && !(P.by_logits && P.renormalize)) {
-    float top = l[0];
+    float top = c[0];
 #pragma unroll
-    for (int v = 1; v < V; ++v) top = fmaxf(top, l[v]);
-    scale.top = warp_max(top);
+    for (int v = 1; v < V; ++v) top = fmaxf(top, c[v]);
+    scale.top = row_max<L>(top);
     float part[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) part[v] = __expf(l[v] - scale.top);
+    for (int v = 0; v < V; ++v) part[v] = __expf(c[v] - scale.top);
 #pragma unroll
     for (int o = V / 2; o; o >>= 1)
 #pragma unroll
       for (int v = 0; v < o; ++v) part[v] += part[v + o];
-    scale.sum = warp_sum(part[0]);
+    scale.sum = row_sum<L>(part[0]);
   }
 
-  const auto choice_of = [&](float v, int e) {
-    if (P.by_logits) return v;
-    const float s = score_of(v, P.sigmoid, scale);
-    return P.bias ? s + P.bias[e] : s;
-  };
-  uint32_t key[V];
+  // from logits to choices
+  bool odd = false;  // NaN
+  if (!P.by_logits) {
+    float b[V];
+    constexpr int kPart = V < 4 ? V : 4;
+    if (P.bias && P.vectors && count > 0) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    key[v] = 0;
-    if (e0 + v < P.experts && l[v] != -INFINITY) {
-      const float c = choice_of(l[v], e0 + v);
-      if (c != -INFINITY) key[v] = order_of(c);
+      for (int v = 0; v < V; v += kPart) {
+        const Pack<float, kPart> p = *reinterpret_cast<const Pack<float, kPart>*>(P.bias + e0 + v);
+#pragma unroll
+        for (int i = 0; i < kPart; ++i) b[v + i] = p.v[i];
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) b[v] = P.bias && v < count ? P.bias[e0 + v] : 0.f;
     }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      c[v] = c[v] == kClosed ? kClosed : score_of(c[v], P.sigmoid, scale) + b[v];
   }
+#pragma unroll
+  for (int v = 0; v < V; ++v) odd |= c[v] != c[v];
 
   // Two choices closer than this may be the other way round in exact arithmetic.  A
   // score is off by at most 35 units of 2^-24 of the row's largest possible score
@@ -201,92 +331,76 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteArgs P) {
   // where exp(x) |x| <= 0.37 and the mean of |x| over the row is at most log 1024, and
   // the sum's ten additions; sigmoid: 6), a sum with the bias by half a unit of its own.
   const float step = (P.sigmoid ? 1.f : __fdividef(1.f, scale.sum)) * 0x1p-17f;
-  bool unsure = false;
+  bool unsure = row_any<L>(odd);
 
   if (P.groups > 1) {
-    const int size = P.experts / P.groups;
-    float* c = reinterpret_cast<float*>(room);
-    uint32_t* o = reinterpret_cast<uint32_t*>(room) + P.experts;
+    float first = kClosed, second = kClosed;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (e0 + v < P.experts) {
-        c[e0 + v] = key[v] ? choice_of(l[v], e0 + v) : -INFINITY;
-        o[e0 + v] = key[v];
-      }
-    __syncwarp();
-    float worth = -INFINITY;
-    uint32_t rank = 0;
-    if (lane < P.groups) {
-      uint32_t first = 0, second = 0;
-      float a = 0.f, b = 0.f;
-      for (int i = 0; i < size; ++i) {
-        const uint32_t k = o[lane * size + i];
-        if (k > first) second = first, b = a, first = k, a = c[lane * size + i];
-        else if (k > second) second = k, b = c[lane * size + i];
-      }
-      if (first) {
-        worth = P.group_best > 1 && second ? a + b : a;
-        rank = order_of(worth);
-      }
+    for (int v = 0; v < V; ++v) {
+      second = fmaxf(second, fminf(first, c[v]));
+      first = fmaxf(first, c[v]);
     }
-    const unsigned open = best_groups(rank, P.groups, P.top_groups);
-    if (!P.by_logits && __popc(open) < P.groups) {
+    for (int o = P.group_lanes >> 1; o; o >>= 1) {
+      const float f = __shfl_xor_sync(kAll, first, o), s = __shfl_xor_sync(kAll, second, o);
+      second = fmaxf(fmaxf(second, s), fminf(first, f));
+      first = fmaxf(first, f);
+    }
+    const float worth = P.group_best > 1 && second != kClosed ? first + second : first;
+    int rank = 0;
+    for (int o = P.group_lanes; o < L; o += P.group_lanes) {
+      const float other = __shfl_xor_sync(kAll, worth, o);
+      rank += other > worth || (other == worth && (place ^ o) < place);
+    }
+    const bool open = worth != kClosed && rank < P.top_groups;
+    if (!P.by_logits) {
       // the least worth that is taken and the largest that is left
-      const bool in = open >> lane & 1;
-      const bool left = lane < P.groups && !in && rank;
-      const float last = -warp_max(in ? -worth : -INFINITY), next = warp_max(left ? worth : -INFINITY);
-      const bool odd = __any_sync(kAll, (in || left) && !(fabsf(worth) < INFINITY));
-      unsure = __any_sync(kAll, left) &&
-               (odd || !(last - next > 2.f * step + 0x1p-21f * fmaxf(fabsf(last), fabsf(next))));
+      const bool left = worth != kClosed && !open;
+      const float last = -row_max<L>(open ? -worth : kClosed), next = row_max<L>(left ? worth : kClosed);
+      unsure |= next != kClosed &&
+                !(last - next > 2.f * step + 0x1p-21f * fmaxf(fabsf(last), fabsf(next)));
     }
+    if (!open) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (e0 + v < P.experts && !(open >> ((e0 + v) / size) & 1)) key[v] = 0;
-    __syncwarp();
+      for (int v = 0; v < V; ++v) c[v] = kClosed;
+    }
   }
 
-  int mine = -1;  // lane j: the j-th expert
-  const int rounds = P.by_logits ? P.k : P.k + 1;
-  for (int r = 0; r < rounds && !unsure; ++r) {
-    uint32_t most = key[0];
-#pragma unroll
-    for (int v = 1; v < V; ++v) most = max(most, key[v]);
-    const uint32_t best = __reduce_max_sync(kAll, most);
-    if (!best) break;
-    const int winner = __ffs(__ballot_sync(kAll, most == best)) - 1;
-    int at = 0;
-    if (lane == winner) {
-#pragma unroll
-      for (int v = V - 1; v >= 0; --v)
-        if (key[v] == best) at = v;
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (v == at) key[v] = 0;
-    }
-    at = __shfl_sync(kAll, at, winner);
-    if (lane == r) mine = winner * V + at;
+  const int K = P.by_logits ? P.k : P.k + 1;
+  int mine;  // lane j of the row: the j-th expert
+  if constexpr (kBound) {
+    mine = K <= 16 ? choose_by_bound<V>(c, e0, K, reinterpret_cast<Candidate*>(room))
+                   : choose_in_rounds<V, L>(c, e0, K);
+  } else {
+    mine = choose_in_rounds<V, L>(c, e0, K);
   }
   float chosen = mine >= 0 ? to_f32(logits[mine]) : 0.f;
-  if (!P.by_logits && !unsure) {
+  if (!P.by_logits) {
     // neighbours in the order that fp32 does not tell apart; the same logit and bias tie
     // in any arithmetic
     const float b = P.bias && mine >= 0 ? P.bias[mine] : 0.f;
-    const float c = mine >= 0 ? choice_of(chosen, mine) : 0.f;
+    const float s = mine >= 0 ? score_of(chosen, P.sigmoid, scale) + b : 0.f;
     const float lp = __shfl_up_sync(kAll, chosen, 1), bp = __shfl_up_sync(kAll, b, 1);
-    const float cp = __shfl_up_sync(kAll, c, 1);
-    const bool near = lane > 0 && mine >= 0 &&
-                      !(cp - c > step + 0x1p-22f * fmaxf(fabsf(c), fabsf(cp))) &&
-                      !(lp == chosen && bp == b);
-    unsure = __any_sync(kAll, near);
+    const float sp = __shfl_up_sync(kAll, s, 1);
+    unsure |= row_any<L>(place > 0 && mine >= 0 &&
+                         !(sp - s > step + 0x1p-22f * fmaxf(fabsf(s), fabsf(sp))) &&
+                         !(lp == chosen && bp == b));
   }
-  if (unsure) {
-    mine = choose_exactly(P, logits, room);
+  const unsigned again = __ballot_sync(kAll, unsure);
+  if (again) {
+#pragma unroll 1
+    for (int r = 0; r < kRows; ++r) {
+      if (!(again >> (r * L) & 1)) continue;
+      const int64_t t = token0 + r < P.tokens ? token0 + r : token0;
+      const int found = choose_exactly(P, static_cast<const T*>(P.logits) + t * P.stride, room);
+      const int my = __shfl_sync(kAll, found, place);
+      if (lane / L == r) mine = my;
+    }
     chosen = mine >= 0 ? to_f32(logits[mine]) : 0.f;
   }
-  if (lane >= P.k) mine = -1;  // the one past the last
-  const float w = weight_of(chosen, mine >= 0, P.sigmoid, P.renormalize, scale);
-  if (lane < P.k) {
-    const int64_t at = token * P.k + lane;
+  if (place >= P.k) mine = -1;  // the one past the last
+  const float w = weight_of<L>(chosen, mine >= 0, P.sigmoid, P.renormalize, scale);
+  if (place < P.k && live) {
+    const int64_t at = token * P.k + place;
     if (P.wide_ids) static_cast<int64_t*>(P.ids)[at] = mine;
     else static_cast<int*>(P.ids)[at] = mine;
     P.weights[at] = mine >= 0 ? P.scale * w : 0.f;
@@ -304,70 +418,81 @@ struct RouteGradArgs {
   bool vectors;  // the rows of grad allow 16-byte stores from end to end
 };
 
-// A warp a token: lane j forms the gradient of the j-th expert's logit, the row is
-// put together in shared memory and stored.
-template <typename T>
+// L lanes a token, lane j for its j-th expert.  Most of a row does not depend on what is
+// read, so it is written at once, and the chosen experts' gradients follow over it: the loads'
+// and sums' latencies pass while the stores are on their way.
+template <typename T, int L>
 __global__ void __launch_bounds__(256) route_backward_kernel(const RouteGradArgs P) {
-  extern __shared__ float grad_smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t token = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp;
-  if (token >= P.tokens) return;
-  const T* logits = static_cast<const T*>(P.logits) + token * P.stride;
-  T* grad = static_cast<T*>(P.grad) + token * P.grad_stride;
-  float* row = grad_smem + warp * P.experts;
-  for (int e = lane; e < P.experts; e += 32) row[e] = 0.f;
+  constexpr int V = kVec<T>;
+  const int lane = threadIdx.x & 31, place = lane & (L - 1);
+  const int64_t token = static_cast<int64_t>(blockIdx.x) * (256 / L) + threadIdx.x / L;
+  const bool live = token < P.tokens;  // the others take part in the sums
+  const T* logits = static_cast<const T*>(P.logits) + (live ? token : 0) * P.stride;
+  T* grad = static_cast<T*>(P.grad) + (live ? token : 0) * P.grad_stride;
+  const int experts = live ? P.experts : 0;
+  const bool whole = !P.sigmoid && !P.renormalize;  // every logit has a gradient
+  // value(i): the gradient of expert i's logit were it not chosen
+  const auto fill = [&](auto value) {
+    if (P.vectors) {
+      for (int i = place * V; i < experts; i += L * V) {
+        float f[V];
+#pragma unroll
+        for (int u = 0; u < V; ++u) f[u] = value(i + u);
+        store_vec(grad + i, from_floats<T>(f));
+      }
+    } else {
+      for (int i = place; i < experts; i += L) grad[i] = from_f32<T>(value(i));
+    }
+  };
+  if (!whole) fill([](int) { return 0.f; });
   int64_t id = -1;
-  if (lane < P.k) {
-    const int64_t at = token * P.k + lane;
+  if (live && place < P.k) {
+    const int64_t at = token * P.k + place;
     id = P.wide_ids ? static_cast<const int64_t*>(P.ids)[at] : static_cast<const int*>(P.ids)[at];
   }
-  const bool on = id >= 0 && id < P.experts;
-  const int e = on ? static_cast<int>(id) : -1 - lane;  // no two lanes' alike
+  const bool on = id >= 0 && id < experts;
+  const int e = on ? static_cast<int>(id) : -1;
   const float l = on ? to_f32(logits[e]) : 0.f;
-  const float g = on ? P.scale * P.grad_weights[token * P.k + lane] : 0.f;
+  const float g = on ? P.scale * P.grad_weights[token * P.k + place] : 0.f;
   RowScale scale = {0.f, 1.f};
-  const bool whole = !P.sigmoid && !P.renormalize;  // every logit has a gradient
   if (whole) {
-    float top = -INFINITY;
-    for (int i = lane; i < P.experts; i += 32) top = fmaxf(top, to_f32(logits[i]));
-    scale.top = warp_max(top);
+    float top = kClosed;
+    for (int i = place; i < experts; i += L) top = fmaxf(top, to_f32(logits[i]));
+    scale.top = row_max<L>(top);
     float sum = 0.f;
-    for (int i = lane; i < P.experts; i += 32) sum += expf(to_f32(logits[i]) - scale.top);
-    scale.sum = warp_sum(sum);
+    for (int i = place; i < experts; i += L) sum += expf(to_f32(logits[i]) - scale.top);
+    scale.sum = row_sum<L>(sum);
   }
-  const float p = weight_of(l, on, P.sigmoid, P.renormalize, scale);
-  const float mean = P.sigmoid && !P.renormalize ? 0.f : warp_sum(g * p);
-  float d = g;
-  if (!whole) {
-    d = p * (g - mean);
+  const float p = weight_of<L>(l, on, P.sigmoid, P.renormalize, scale);
+  const float mean = P.sigmoid && !P.renormalize ? 0.f : row_sum<L>(g * p);
+  if (whole)
+    fill([&](int i) {  // zeros where every expert is closed
+      return scale.top == kClosed
+                 ? 0.f
+                 : __fdiv_rn(expf(to_f32(logits[i]) - scale.top), scale.sum) * -mean;
+    });
+  // where an expert is named more than once, the first lane that does adds up the others' in
+  // their order; softmax's mean counts once
+  const unsigned same = __match_any_sync(kAll, on ? (lane & ~(L - 1)) << 16 | e : -1 - lane);
+  const bool first = (same & ((1u << lane) - 1)) == 0;
+  float of_score = g;
+  if (__any_sync(kAll, !first)) {
+    of_score = 0.f;
+    for (int j = 0; j < 32; ++j) {
+      const float v = __shfl_sync(kAll, g, j);
+      if (same >> j & 1) of_score += v;
+    }
+  }
+  float d;
+  if (whole) {
+    d = p * (of_score - mean);
+  } else {
+    // as many times the mean as the expert is named
+    d = p * (of_score - static_cast<float>(__popc(same)) * mean);
     if (P.sigmoid) d *= __fdiv_rn(1.f, 1.f + expf(l));  // 1 - sigmoid(l)
   }
   __syncwarp();
-  const unsigned same = __match_any_sync(kAll, e);
-  if (__any_sync(kAll, on && __popc(same) > 1)) {
-    for (int j = 0; j < P.k; ++j) {  // an expert named twice: in the order of j
-      if (lane == j && on) row[e] += d;
-      __syncwarp();
-    }
-  } else if (on) {
-    row[e] = d;
-  }
-  __syncwarp();
-  const auto value = [&](int i) {
-    if (!whole) return row[i];
-    if (scale.top == -INFINITY) return 0.f;  // every expert is closed
-    return __fdiv_rn(expf(to_f32(logits[i]) - scale.top), scale.sum) * (row[i] - mean);
-  };
-  if (P.vectors) {
-    for (int i = lane * kVec<T>; i < P.experts; i += 32 * kVec<T>) {
-      float f[kVec<T>];
-#pragma unroll
-      for (int u = 0; u < kVec<T>; ++u) f[u] = value(i + u);
-      store_vec(grad + i, from_floats<T>(f));
-    }
-  } else {
-    for (int i = lane; i < P.experts; i += 32) grad[i] = from_f32<T>(value(i));
-  }
+  if (on && first) grad[e] = from_f32<T>(d);
 }
 
 // -------------------------------------------------------------- host
@@ -385,22 +510,44 @@ tbe_status check_route(int32_t dtype, int64_t tokens, int32_t experts, int32_t s
 
 int id_bytes(int32_t index_dtype) { return index_dtype == TBE_DT_I32 ? 4 : 8; }
 
+// How rows are shared: as few lanes as hold the chosen ones (and the next) with at most eight
+// experts each, so that a warp's reductions serve several rows.
 template <typename T>
-tbe_status launch_route(const RouteArgs& args, cudaStream_t s) {
-  // choices in 64 bits, or as fp32 and its order
-  const size_t row = args.by_logits && args.groups == 1 ? 0 : args.experts * sizeof(double);
-  const int warps = args.experts > 512 ? 4 : 8;
-  const unsigned ctas = static_cast<unsigned>((args.tokens + warps - 1) / warps);
-  const auto go = [&](auto v) {
-    route_kernel<T, decltype(v)::value><<<ctas, warps * 32, warps * row, s>>>(args);
+tbe_status launch_route(RouteArgs args, cudaStream_t s) {
+  const int size = args.experts / args.groups;
+  int slots = 1;  // groups, rounded up to a power of two
+  while (slots < args.groups) slots *= 2;
+  int lanes = 8;
+  const int kept = args.by_logits ? args.k : args.k + 1;
+  const auto each = [&] { return lanes < slots ? INT32_MAX : (size + lanes / slots - 1) / (lanes / slots); };
+  while (lanes < 32 && (lanes < kept || each() > 8)) lanes *= 2;
+  args.group_lanes = lanes / slots;
+  args.lane_experts = each();
+  const auto go = [&](auto v, auto l) {
+    constexpr int V = decltype(v)::value, L = decltype(l)::value;
+    constexpr int kPart = V * sizeof(T) < 16 ? V : 16 / static_cast<int>(sizeof(T));
+    args.vectors = args.lane_experts == V && size % V == 0 && args.stride % kPart == 0 &&
+                   aligned_to(args.logits, kPart * sizeof(T)) && aligned_to(args.bias, 16);
+    const int warps = args.experts > 512 ? 4 : 8, rows = warps * (32 / L);
+    route_kernel<T, V, L><<<static_cast<unsigned>((args.tokens + int64_t(rows) - 1) / rows),
+                            warps * 32, warps * (args.experts + 32) * sizeof(double), s>>>(args);
     return launched();
   };
-  if (args.experts <= 32) return go(std::integral_constant<int, 1>{});
-  if (args.experts <= 64) return go(std::integral_constant<int, 2>{});
-  if (args.experts <= 128) return go(std::integral_constant<int, 4>{});
-  if (args.experts <= 256) return go(std::integral_constant<int, 8>{});
-  if (args.experts <= 512) return go(std::integral_constant<int, 16>{});
-  return go(std::integral_constant<int, 32>{});
+  const auto with = [&](auto l) {
+    constexpr int L = decltype(l)::value;
+    if (args.lane_experts <= 2) return go(std::integral_constant<int, 2>{}, l);
+    if (args.lane_experts <= 4) return go(std::integral_constant<int, 4>{}, l);
+    if (L < 32 || args.lane_experts <= 8) return go(std::integral_constant<int, 8>{}, l);
+    if constexpr (L == 32) {
+      if (args.lane_experts <= 16) return go(std::integral_constant<int, 16>{}, l);
+      if (args.lane_experts <= 32) return go(std::integral_constant<int, 32>{}, l);
+      return go(std::integral_constant<int, 64>{}, l);  // groups that leave lanes idle
+    }
+    return TBE_EUNSUPPORTED;
+  };
+  if (lanes == 8) return with(std::integral_constant<int, 8>{});
+  if (lanes == 16) return with(std::integral_constant<int, 16>{});
+  return with(std::integral_constant<int, 32>{});
 }
 
 }  // namespace
@@ -435,7 +582,7 @@ extern "C" tbe_status tbe_expert_route(const void* logits, int32_t dtype, int64_
   const RouteArgs args = {logits, bias, ids, weights, logits_stride, static_cast<int>(tokens),
                           experts, k, groups, top_groups, group_best, scale,
                           score == TBE_SCORE_SIGMOID, renormalize != 0, index_dtype == TBE_DT_I64,
-                          !bias && (groups == 1 || group_best == 1)};
+                          !bias && (groups == 1 || group_best == 1), 0, 0, false};
   return for_dtype(dtype, [&](auto t) {
     return launch_route<decltype(t)>(args, static_cast<cudaStream_t>(stream));
   });
@@ -466,10 +613,16 @@ extern "C" tbe_status tbe_expert_route_backward(const float* grad_weights, const
                               score == TBE_SCORE_SIGMOID, renormalize != 0,
                               index_dtype == TBE_DT_I64, out.vectors(experts, 16)};
   return for_dtype(dtype, [&](auto t) {
-    constexpr int kWarps = 8;
-    route_backward_kernel<decltype(t)>
-        <<<static_cast<unsigned>((tokens + kWarps - 1) / kWarps), kWarps * 32,
-           kWarps * experts * sizeof(float), static_cast<cudaStream_t>(stream)>>>(args);
-    return launched();
+    using T = decltype(t);
+    const auto go = [&](auto lanes) {
+      constexpr int L = decltype(lanes)::value, kRows = 256 / L;
+      route_backward_kernel<T, L>
+          <<<static_cast<unsigned>((tokens + kRows - 1) / kRows), 256, 0,
+             static_cast<cudaStream_t>(stream)>>>(args);
+      return launched();
+    };
+    if (k <= 8) return go(std::integral_constant<int, 8>{});
+    if (k <= 16) return go(std::integral_constant<int, 16>{});
+    return go(std::integral_constant<int, 32>{});
   });
 }
