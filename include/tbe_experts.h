@@ -54,7 +54,7 @@ enum { TBE_SCORE_SOFTMAX = 1, TBE_SCORE_SIGMOID = 2 };
  *                   0 where ids is -1
  * Ties go to the lower expert or group.  The choice is that of exact arithmetic
  * wherever 64 bits tell the c apart: where fp32 does not, it is made again in 64 bits.
- * Without bias and groups the logits themselves are compared.  The bias only chooses: weights
+ * Without a bias the experts' logits themselves are compared.  The bias only chooses: weights
  * are of s.  NaN ranks above everything, so a token with a NaN logit shows it in its
  * weights; softmax of +inf is NaN as the formula gives, and a row that is closed
  * throughout has ids -1.

@@ -22,7 +22,7 @@ struct RouteArgs {
   int tokens, experts, k, groups, top_groups, group_best;
   float scale;
   bool sigmoid, renormalize, wide_ids;
-  bool by_logits;  // the choices' order is that of the logits
+  bool by_logits;  // no bias: the choices' order is that of the logits, which are compared
   // how a row's lanes share its experts: `group_lanes` consecutive lanes a group (a power of
   // two), `lane_experts` consecutive experts of it a lane
   int group_lanes, lane_experts;
@@ -37,6 +37,9 @@ __device__ __forceinline__ unsigned long long order_of(double c) {
   const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(c + 0.0));
   if (c != c) return ~0ull;
   return b >> 63 ? ~b : b | 1ull << 63;
+}
+__device__ __forceinline__ double value_of(unsigned long long o) {  // NaN of ~0
+  return __longlong_as_double(static_cast<long long>(o >> 63 ? o & ~(1ull << 63) : ~o));
 }
 
 // Over the L lanes (a power of two) that share a row.  Maxima pass over NaN.
@@ -70,19 +73,32 @@ struct RowScale {
   float top, sum;
 };
 
-__device__ __forceinline__ float score_of(float l, bool sigmoid, RowScale r) {
-  return sigmoid ? __fdividef(1.f, 1.f + __expf(-l)) : __fdividef(__expf(l - r.top), r.sum);
+// exp(x), off by 4 + 1.6 |x| units of 2^-24; 0 below 2^-126.
+__device__ __forceinline__ float exp_near(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+__device__ __forceinline__ float reciprocal_near(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
-// A row's choice again in 64 bits, by the whole warp and without a thought for speed: a few rows in
-// ten thousand need it (see `step` below).  c: room for the row's choices.  Returns lane j's
-// expert, -1 for none.
+// `inverse`: one over softmax's sum.
+__device__ __forceinline__ float score_of(float l, bool sigmoid, float top, float inverse) {
+  return sigmoid ? reciprocal_near(1.f + exp_near(-l)) : exp_near(l - top) * inverse;
+}
+
+// A row's choice again in 64 bits, by the whole warp: few rows need it (see `step` below), but
+// the last of them ends the launch.  room: the row's choices as integers in their order, 0 where
+// an expert is closed.  Returns lane j's expert, -1 for none.
 template <typename T>
-__device__ __noinline__ int choose_exactly(const RouteArgs& P, const T* logits, double* c) {
+__device__ __noinline__ int choose_exactly(const RouteArgs& P, const T* logits,
+                                           unsigned long long* room) {
   const int lane = threadIdx.x & 31, size = P.experts / P.groups;
-  const double closed = kClosed;
   double top = 0.0, sum = 1.0;
-  if (!P.sigmoid && !P.by_logits) {
+  if (!P.sigmoid) {
     float m = kClosed;
     for (int e = lane; e < P.experts; e += 32) m = fmaxf(m, to_f32(logits[e]));
     top = row_max<32>(m);
@@ -91,54 +107,89 @@ __device__ __noinline__ int choose_exactly(const RouteArgs& P, const T* logits, 
       sum += exp(static_cast<double>(to_f32(logits[e])) - top);
     sum = row_sum<32>(sum);
   }
+  const auto score = [&](double l) {
+    return P.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - top) / sum;
+  };
   for (int e = lane; e < P.experts; e += 32) {
     const double l = to_f32(logits[e]);
-    double v = P.by_logits ? l : P.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - top) / sum;
-    if (P.bias) v += P.bias[e];
-    c[e] = l == closed ? closed : v;
+    const double c = P.by_logits || l == kClosed ? l : score(l) + P.bias[e];
+    room[e] = c == kClosed ? 0 : order_of(c);
   }
   __syncwarp();
-  unsigned open = kAll;  // groups
   if (P.groups > 1) {
     unsigned long long worth = 0;
     if (lane < P.groups) {
-      double first = closed, second = closed;
+      unsigned long long first = 0, second = 0;
       for (int i = 0; i < size; ++i) {
-        const double v = c[lane * size + i];
-        if (order_of(v) > order_of(first)) second = first, first = v;
-        else if (order_of(v) > order_of(second)) second = v;
+        const unsigned long long o = room[lane * size + i];
+        second = max(second, min(first, o));
+        first = max(first, o);
       }
-      if (first != closed)
-        worth = order_of(P.group_best > 1 && second != closed ? first + second : first);
+      if (first) {
+        const bool two = P.group_best > 1;
+        double w = value_of(first);
+        if (two && P.by_logits) w = score(w);
+        if (two && second) w += P.by_logits ? score(value_of(second)) : value_of(second);
+        worth = order_of(w);
+      }
     }
     int rank = 0;
     for (int g = 0; g < P.groups; ++g) {
       const unsigned long long o = __shfl_sync(kAll, worth, g);
       rank += o > worth || (o == worth && g < lane);
     }
-    open = __ballot_sync(kAll, worth != 0 && rank < P.top_groups);
+    const unsigned open = __ballot_sync(kAll, worth != 0 && rank < P.top_groups);
+    for (int g = 0; g < P.groups; ++g)
+      if (!(open >> g & 1))
+        for (int i = lane; i < size; i += 32) room[g * size + i] = 0;
+    __syncwarp();
   }
-  int mine = -1;
-  for (int r = 0; r < P.k; ++r) {
-    unsigned long long best = 0;
-    int at = 0;
+  unsigned long long best = 0;  // this lane's largest
+  int at = 0;
+  const auto look = [&] {
+    best = 0;
     for (int e = lane; e < P.experts; e += 32) {
-      const double v = c[e];
-      const unsigned long long o = v == closed || !(open >> (e / size) & 1) ? 0 : order_of(v);
+      const unsigned long long o = room[e];
       if (o > best) best = o, at = e;
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const unsigned long long other = __shfl_xor_sync(kAll, best, o);
-      const int where = __shfl_xor_sync(kAll, at, o);
-      if (other > best || (other == best && where < at)) best = other, at = where;
+  };
+  look();
+  int mine = -1;
+  for (int r = 0; r < P.k; ++r) {
+    // the largest, its upper and then its lower half, and of those alike the lowest expert
+    const unsigned hi = __reduce_max_sync(kAll, static_cast<unsigned>(best >> 32));
+    const bool in = best >> 32 == hi;
+    const unsigned lo = __reduce_max_sync(kAll, in ? static_cast<unsigned>(best) : 0u);
+    if (!hi) break;  // an open choice has bits there
+    const bool tied = in && static_cast<unsigned>(best) == lo;
+    const int e = static_cast<int>(__reduce_min_sync(kAll, tied ? at : INT32_MAX));
+    if (lane == r) mine = e;
+    if (tied && at == e) {
+      room[e] = 0;
+      look();
     }
-    if (!best) break;
-    if (lane == r) mine = at;
-    __syncwarp();
-    if (lane == 0) c[at] = closed;
-    __syncwarp();
   }
+  __syncwarp();
+  return mine;
+}
+
+// The candidates of rows of L lanes, lane j with expert `mine` (-1: none) of logit l and bias b,
+// put in the order of their sigmoid choices in 64 bits.  room: 32 entries.
+template <int L>
+__device__ __noinline__ int order_exactly(int mine, float l, float b, int* room) {
+  const int lane = threadIdx.x & 31, first = lane & ~(L - 1);
+  const double c = mine >= 0 ? 1.0 / (1.0 + exp(-static_cast<double>(l))) + b : kClosed;
+  int rank = 0;
+  for (int j = 0; j < L; ++j) {
+    const double other = __shfl_sync(kAll, c, first + j);
+    const int e = __shfl_sync(kAll, mine, first + j);
+    // those that are none keep their places at the end
+    rank += other > c || (other == c && (mine >= 0 ? e >= 0 && e < mine : first + j < lane));
+  }
+  __syncwarp();
+  room[first + rank] = mine;
+  __syncwarp();
+  mine = room[lane];
   __syncwarp();
   return mine;
 }
@@ -198,31 +249,39 @@ __device__ __forceinline__ int choose_in_rounds(float (&c)[V], int e0, int K) {
   return mine;
 }
 
-struct Candidate {
-  float c;
-  int e;
+// A warp's shared memory, in doubles: a row's choices in 64 bits, or candidates (read in 16
+// bytes).
+__host__ __device__ constexpr int room_of(int experts) { return (experts + 33) & ~1; }
+
+// Room for candidates.
+struct Candidates {
+  float c[32];
+  int e[32];
 };
 
 // The same for a row of a whole warp with many experts a lane.  The K-th largest of the lanes'
 // largest choices bounds the K-th choice from below, so only choices from there on are
 // candidates, a few more than K; they are moved to shared memory, ranked
-// against one another, a lane each, and put in order.  (65536 rows, eight of 256 in four of
-// eight groups with a bias: in rounds a lane must look its V choices over for
-// every expert chosen.)
+// against one another, a lane each, and put in order: lane j gets the j-th, past K too.
+// *bound: no other choice is above it.
 template <int V>
-__device__ __forceinline__ int choose_by_bound(float (&c)[V], int e0, int K, Candidate* room) {
+__device__ __forceinline__ int choose_by_bound(float (&c)[V], int e0, int K, Candidates& room,
+                                               float* bound) {
   const int lane = threadIdx.x & 31;
   float left = c[0];
 #pragma unroll
   for (int v = 1; v < V; ++v) left = fmaxf(left, c[v]);
-  float bound = kClosed;
+  float least = kClosed;
+#pragma unroll 4
   for (int r = 0; r < K; ++r) {
-    bound = row_max<32>(left);
-    if (left == bound) left = kClosed;
+    least = row_max<32>(left);
+    if (left == least) left = kClosed;
   }
+  *bound = least;
+  if (least == kClosed) least = -3.402823466e38f;  // open ones only
   int count = 0;
 #pragma unroll
-  for (int v = 0; v < V; ++v) count += c[v] >= bound && c[v] != kClosed;
+  for (int v = 0; v < V; ++v) count += c[v] >= least;
   int upto = count;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -230,39 +289,48 @@ __device__ __forceinline__ int choose_by_bound(float (&c)[V], int e0, int K, Can
     if (lane >= o) upto += y;
   }
   const int all = __shfl_sync(kAll, upto, 31);
-  if (all > 32) return choose_in_rounds<V, 32>(c, e0, K);  // many alike, or few lanes open
+  if (all > 32) return -2;  // many alike, or few lanes open
+  room.c[lane] = kClosed;
+  __syncwarp();
   int at = upto - count;
 #pragma unroll
   for (int v = 0; v < V; ++v)
-    if (c[v] >= bound && c[v] != kClosed) room[at++] = {c[v], e0 + v};
+    if (c[v] >= least) {
+      room.c[at] = c[v];
+      room.e[at++] = e0 + v;
+    }
   __syncwarp();
-  const Candidate my = lane < all ? room[lane] : Candidate{kClosed, 0};
+  const float mine = room.c[lane];
+  const int e = lane < all ? room.e[lane] : -1;
   int rank = 0;
-  for (int j = 0; j < all; ++j) {  // in the order of the experts
-    const float other = room[j].c;
-    rank += other > my.c || (other == my.c && j < lane);
+  for (int j = 0; j < all; j += 4) {  // they stand in the order of the experts
+    const float4 o = *reinterpret_cast<const float4*>(room.c + j);
+    rank += o.x > mine || (o.x == mine && j < lane);
+    rank += o.y > mine || (o.y == mine && j + 1 < lane);
+    rank += o.z > mine || (o.z == mine && j + 2 < lane);
+    rank += o.w > mine || (o.w == mine && j + 3 < lane);
   }
   __syncwarp();
-  if (lane < all) room[rank].e = my.e;
+  if (lane < all) room.e[rank] = e;
   __syncwarp();
-  const int mine = lane < all && lane < K ? room[lane].e : -1;
+  const int sorted = lane < all ? room.e[lane] : -1;
   __syncwarp();
-  return mine;
+  return sorted;
 }
 
 // A row's experts are shared by L lanes, V consecutive ones a lane at most; 32 / L rows a warp.
 template <typename T, int V, int L>
-__global__ void __launch_bounds__(256) route_kernel(const RouteArgs P) {
+__global__ void __launch_bounds__(256) route_kernel(const __grid_constant__ RouteArgs P) {
   constexpr int kRows = 32 / L;
   constexpr bool kBound = L == 32 && V >= 4;
-  extern __shared__ double route_smem[];
+  extern __shared__ __align__(16) double route_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, place = lane & (L - 1);
   const int64_t token0 = (static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp) * kRows;
   if (token0 >= P.tokens) return;
   const int64_t token = token0 + lane / L;
   const bool live = token < P.tokens;
   const T* logits = static_cast<const T*>(P.logits) + (live ? token : token0) * P.stride;
-  double* room = route_smem + static_cast<int64_t>(warp) * (P.experts + 32);
+  double* room = route_smem + warp * room_of(P.experts);
 
   // this lane's experts: e0 .. e0 + mine - 1, of its group
   const int size = P.experts / P.groups, group = place / P.group_lanes;
@@ -287,27 +355,29 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteArgs P) {
   }
 
   RowScale scale = {0.f, 1.f};
-  if (!P.sigmoid && !(P.by_logits && P.renormalize)) {
+  float inverse = 1.f;
+  const bool by_score = !P.by_logits || (P.groups > 1 && P.group_best > 1);
+  if (!P.sigmoid && (by_score || !P.renormalize)) {
     float top = c[0];
 #pragma unroll
     for (int v = 1; v < V; ++v) top = fmaxf(top, c[v]);
     scale.top = row_max<L>(top);
     float part[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) part[v] = __expf(c[v] - scale.top);
+    for (int v = 0; v < V; ++v) part[v] = exp_near(c[v] - scale.top);
 #pragma unroll
     for (int o = V / 2; o; o >>= 1)
 #pragma unroll
       for (int v = 0; v < o; ++v) part[v] += part[v + o];
     scale.sum = row_sum<L>(part[0]);
+    inverse = reciprocal_near(scale.sum);
   }
 
   // from logits to choices
-  bool odd = false;  // NaN
   if (!P.by_logits) {
     float b[V];
     constexpr int kPart = V < 4 ? V : 4;
-    if (P.bias && P.vectors && count > 0) {
+    if (P.vectors && count > 0) {
 #pragma unroll
       for (int v = 0; v < V; v += kPart) {
         const Pack<float, kPart> p = *reinterpret_cast<const Pack<float, kPart>*>(P.bias + e0 + v);
@@ -316,22 +386,31 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteArgs P) {
       }
     } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) b[v] = P.bias && v < count ? P.bias[e0 + v] : 0.f;
+      for (int v = 0; v < V; ++v) b[v] = v < count ? P.bias[e0 + v] : 0.f;
     }
+    if (P.sigmoid) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      c[v] = c[v] == kClosed ? kClosed : score_of(c[v], P.sigmoid, scale) + b[v];
+      for (int v = 0; v < V; ++v)
+        c[v] = c[v] == kClosed ? kClosed : score_of(c[v], true, 0.f, 0.f) + b[v];
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        c[v] = c[v] == kClosed ? kClosed : score_of(c[v], false, scale.top, inverse) + b[v];
+    }
   }
+  bool odd = scale.sum != scale.sum && scale.top != kClosed;  // NaN
 #pragma unroll
   for (int v = 0; v < V; ++v) odd |= c[v] != c[v];
+  odd = odd && (count > 0);
 
-  // Two choices closer than this may be the other way round in exact arithmetic.  A
-  // score is off by at most 35 units of 2^-24 of the row's largest possible score
-  // (softmax: the exponentials of logit and sum, 4 + 2 |x| units each at x below the top,
-  // where exp(x) |x| <= 0.37 and the mean of |x| over the row is at most log 1024, and
-  // the sum's ten additions; sigmoid: 6), a sum with the bias by half a unit of its own.
-  const float step = (P.sigmoid ? 1.f : __fdividef(1.f, scale.sum)) * 0x1p-17f;
-  bool unsure = row_any<L>(odd);
+  // Two choices closer than this may be the other way round in exact arithmetic.  In units of
+  // 2^-24 of the row's largest possible score, a score is off by at most 7 with sigmoid
+  // (the exponential's 4 + 1.6 |l| times s (1 - s), the sum's 1 and the reciprocal's 2)
+  // and by 35 with softmax (the exponentials of logit and sum at x below the top, where
+  // exp(x) |x| <= 0.37 and the mean of |x| over the row is at most log 1024, the sum's ten
+  // additions, reciprocal and product); its sum with the bias by half a unit of its own.
+  const float step = P.sigmoid ? 0x1p-20f : 0x1p-17f * inverse;
+  bool unsure = row_any<L>(odd), near = false;
 
   if (P.groups > 1) {
     float first = kClosed, second = kClosed;
@@ -345,17 +424,24 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteArgs P) {
       second = fmaxf(fmaxf(second, s), fminf(first, f));
       first = fmaxf(first, f);
     }
-    const float worth = P.group_best > 1 && second != kClosed ? first + second : first;
+    float worth = first;
+    if (P.group_best > 1 && first != kClosed) {
+      if (P.by_logits) worth = score_of(first, P.sigmoid, scale.top, inverse);
+      if (second != kClosed)
+        worth += P.by_logits ? score_of(second, P.sigmoid, scale.top, inverse) : second;
+    }
     int rank = 0;
+#pragma unroll 2
     for (int o = P.group_lanes; o < L; o += P.group_lanes) {
       const float other = __shfl_xor_sync(kAll, worth, o);
       rank += other > worth || (other == worth && (place ^ o) < place);
     }
     const bool open = worth != kClosed && rank < P.top_groups;
-    if (!P.by_logits) {
+    if (by_score) {
       // the least worth that is taken and the largest that is left
       const bool left = worth != kClosed && !open;
-      const float last = -row_max<L>(open ? -worth : kClosed), next = row_max<L>(left ? worth : kClosed);
+      const float last = -row_max<L>(open ? -worth : kClosed);
+      const float next = row_max<L>(left ? worth : kClosed);
       unsure |= next != kClosed &&
                 !(last - next > 2.f * step + 0x1p-21f * fmaxf(fabsf(last), fabsf(next)));
     }
@@ -366,24 +452,40 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteArgs P) {
   }
 
   const int K = P.by_logits ? P.k : P.k + 1;
-  int mine;  // lane j of the row: the j-th expert
+  int mine = -2;  // lane j of the row: the j-th expert
+  float bound = kClosed;
   if constexpr (kBound) {
-    mine = K <= 16 ? choose_by_bound<V>(c, e0, K, reinterpret_cast<Candidate*>(room))
-                   : choose_in_rounds<V, L>(c, e0, K);
-  } else {
-    mine = choose_in_rounds<V, L>(c, e0, K);
+    if (K <= 16) mine = choose_by_bound<V>(c, e0, K, *reinterpret_cast<Candidates*>(room), &bound);
   }
+  const bool in_rounds = mine == -2;
+  if (in_rounds) mine = choose_in_rounds<V, L>(c, e0, K);
   float chosen = mine >= 0 ? to_f32(logits[mine]) : 0.f;
   if (!P.by_logits) {
     // neighbours in the order that fp32 does not tell apart; the same logit and bias tie
     // in any arithmetic
-    const float b = P.bias && mine >= 0 ? P.bias[mine] : 0.f;
-    const float s = mine >= 0 ? score_of(chosen, P.sigmoid, scale) + b : 0.f;
+    const float b = mine >= 0 ? P.bias[mine] : 0.f;
+    const float s = mine >= 0 ? score_of(chosen, P.sigmoid, scale.top, inverse) + b : kClosed;
     const float lp = __shfl_up_sync(kAll, chosen, 1), bp = __shfl_up_sync(kAll, b, 1);
     const float sp = __shfl_up_sync(kAll, s, 1);
-    unsure |= row_any<L>(place > 0 && mine >= 0 &&
-                         !(sp - s > step + 0x1p-22f * fmaxf(fabsf(s), fabsf(sp))) &&
-                         !(lp == chosen && bp == b));
+    const auto far = [&](float more, float less) {
+      return more - less > step + 0x1p-22f * fmaxf(fabsf(less), fabsf(more));
+    };
+    near = row_any<L>(place > 0 && place < K && mine >= 0 && !far(sp, s) &&
+                      !(lp == chosen && bp == b)) && !unsure;
+    if (__any_sync(kAll, near)) {
+      // the candidates suffice where the last that is taken is above all others for certain
+      const int edge = (lane & ~(L - 1)) + P.k - 1;
+      const float last = __shfl_sync(kAll, s, edge);
+      const float next = in_rounds ? __shfl_sync(kAll, s, edge + 1 < 32 ? edge + 1 : 31) : bound;
+      const bool enough = P.sigmoid && (next == kClosed || far(last, next));
+      const int sorted = order_exactly<L>(mine, chosen, b, reinterpret_cast<int*>(room));
+      if (near && enough) {
+        mine = sorted;
+        chosen = mine >= 0 ? to_f32(logits[mine]) : 0.f;
+      } else {
+        unsure |= near;
+      }
+    }
   }
   const unsigned again = __ballot_sync(kAll, unsure);
   if (again) {
@@ -391,7 +493,8 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteArgs P) {
     for (int r = 0; r < kRows; ++r) {
       if (!(again >> (r * L) & 1)) continue;
       const int64_t t = token0 + r < P.tokens ? token0 + r : token0;
-      const int found = choose_exactly(P, static_cast<const T*>(P.logits) + t * P.stride, room);
+      const int found = choose_exactly(P, static_cast<const T*>(P.logits) + t * P.stride,
+                                       reinterpret_cast<unsigned long long*>(room));
       const int my = __shfl_sync(kAll, found, place);
       if (lane / L == r) mine = my;
     }
@@ -422,7 +525,7 @@ struct RouteGradArgs {
 // read, so it is written at once, and the chosen experts' gradients follow over it: the loads'
 // and sums' latencies pass while the stores are on their way.
 template <typename T, int L>
-__global__ void __launch_bounds__(256) route_backward_kernel(const RouteGradArgs P) {
+__global__ void __launch_bounds__(256) route_backward_kernel(const __grid_constant__ RouteGradArgs P) {
   constexpr int V = kVec<T>;
   const int lane = threadIdx.x & 31, place = lane & (L - 1);
   const int64_t token = static_cast<int64_t>(blockIdx.x) * (256 / L) + threadIdx.x / L;
@@ -530,7 +633,7 @@ tbe_status launch_route(RouteArgs args, cudaStream_t s) {
                    aligned_to(args.logits, kPart * sizeof(T)) && aligned_to(args.bias, 16);
     const int warps = args.experts > 512 ? 4 : 8, rows = warps * (32 / L);
     route_kernel<T, V, L><<<static_cast<unsigned>((args.tokens + int64_t(rows) - 1) / rows),
-                            warps * 32, warps * (args.experts + 32) * sizeof(double), s>>>(args);
+                            warps * 32, warps * room_of(args.experts) * sizeof(double), s>>>(args);
     return launched();
   };
   const auto with = [&](auto l) {
@@ -582,7 +685,7 @@ extern "C" tbe_status tbe_expert_route(const void* logits, int32_t dtype, int64_
   const RouteArgs args = {logits, bias, ids, weights, logits_stride, static_cast<int>(tokens),
                           experts, k, groups, top_groups, group_best, scale,
                           score == TBE_SCORE_SIGMOID, renormalize != 0, index_dtype == TBE_DT_I64,
-                          !bias && (groups == 1 || group_best == 1), 0, 0, false};
+                          !bias, 0, 0, false};
   return for_dtype(dtype, [&](auto t) {
     return launch_route<decltype(t)>(args, static_cast<cudaStream_t>(stream));
   });
