@@ -1,9 +1,12 @@
 // Root-mean-square norm with the residual's addition, in the rows' type or in
 // 8 bits, and its gradients.  The operations are specified in include/tbe_norm.h.
 //
-// A row is read once into the registers of the threads that share it (32 to 512 of them), its
-// squares are summed, and its outputs are formed from the registers: memory bounds both
-// directions.
+// Memory bounds both directions.  A row is shared by 32 to 512 threads, which read it once: its
+// squares are summed, and its outputs are formed from registers.  The threads walk rows a grid
+// apart, and each copies its own part of the next rows to a ring in shared memory
+// (cp.async, private to the thread, so nothing but its own copies is waited for): loads are always
+// on their way, whatever the row at hand waits for.
+#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
@@ -16,8 +19,8 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kNormThreads = 512;     // threads of a CTA, at most
-constexpr int kNormCta = 256;         // and as a rule
 constexpr int kNormParts = 152 * 8;   // partial sums of grad_weight, at most
+constexpr int kNormShared = 220 * 1024;
 constexpr int kSumSegments = 32;
 
 struct NormArgs {
@@ -43,47 +46,93 @@ struct Units {
 };
 
 template <typename T, int V>
-__device__ __forceinline__ void unit_floats(const Pack<T, V>& p, float (&f)[V]) {
-  if constexpr (V == 1) f[0] = to_f32(p.v[0]);
-  else to_floats<T>(p, f);
-}
-template <typename T, int V>
-__device__ __forceinline__ Pack<T, V> unit_of(const float (&f)[V]) {
-  if constexpr (V == 1) return {from_f32<T>(f[0])};
-  else return from_floats<T>(f);
-}
-template <typename T, int V>
 __device__ __forceinline__ Pack<T, V> load_unit(const T* row, int col, bool on) {
   if (on) return *reinterpret_cast<const Pack<T, V>*>(row + col);
-  float zero[V] = {};
-  return unit_of<T, V>(zero);
+  Pack<T, V> zero;
+#pragma unroll
+  for (int i = 0; i < V; ++i) zero.v[i] = from_f32<T>(0.f);
+  return zero;
 }
 template <typename T, int V>
 __device__ __forceinline__ void store_unit(T* row, int col, const Pack<T, V>& p) {
   *reinterpret_cast<Pack<T, V>*>(row + col) = p;
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void load_weight(const void* weight, bool w32, int col, bool on,
-                                            float (&w)[V]) {
-  if (!weight || !on) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) w[i] = 1.f;
-  } else if (sizeof(T) == 4 || w32) {
-    const float* p = static_cast<const float*>(weight) + col;
-    if constexpr (V == 1) {
-      w[0] = *p;
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; i += 4) {
-        const float4 q = *reinterpret_cast<const float4*>(p + i);
-        w[i] = q.x, w[i + 1] = q.y, w[i + 2] = q.z, w[i + 3] = q.w;
-      }
-    }
+// A thread's values are computed on two at a time (one instruction for two multiplications or
+// additions): pair i of its units, two neighbours in a vector, or two single elements.
+template <typename T, int V, int NV>
+__device__ __forceinline__ float2 pair_at(const Pack<T, V> (&p)[NV], int i) {
+  if constexpr (V == 1) {
+    return make_float2(to_f32(p[2 * i].v[0]), to_f32(p[2 * i + 1].v[0]));
+  } else if constexpr (sizeof(T) == 4) {
+    const Pack<T, V>& u = p[i / (V / 2)];
+    return make_float2(u.v[i % (V / 2) * 2], u.v[i % (V / 2) * 2 + 1]);
   } else {
-    unit_floats<T, V>(load_unit<T, V>(static_cast<const T*>(weight), col, true), w);
+    const uint32_t w = reinterpret_cast<const uint32_t*>(&p[i / (V / 2)])[i % (V / 2)];
+    if constexpr (std::is_same_v<T, __half>)
+      return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    else  // a bf16 is the upper half of an fp32
+      return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
 }
+template <typename T, int V, int NV>
+__device__ __forceinline__ void set_pair(Pack<T, V> (&p)[NV], int i, float2 f) {
+  if constexpr (V == 1) {
+    p[2 * i].v[0] = from_f32<T>(f.x);
+    p[2 * i + 1].v[0] = from_f32<T>(f.y);
+  } else if constexpr (sizeof(T) == 4) {
+    Pack<T, V>& u = p[i / (V / 2)];
+    u.v[i % (V / 2) * 2] = f.x;
+    u.v[i % (V / 2) * 2 + 1] = f.y;
+  } else {
+    uint32_t& w = reinterpret_cast<uint32_t*>(&p[i / (V / 2)])[i % (V / 2)];
+    if constexpr (std::is_same_v<T, __half>) {
+      const __half2 h = __floats2half2_rn(f.x, f.y);
+      w = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+      w = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+}
+__device__ __forceinline__ float2 both(float f) { return make_float2(f, f); }
+
+// The thread's part of the weight.  In the rows' type it stays in registers; in fp32 beside
+// 16-bit rows it is read for each row.
+template <typename T, bool kAligned, int NV>
+struct Weight {
+  using U = Units<T, kAligned>;
+  static constexpr int V = U::V;
+  Pack<T, V> own[NV];
+  const float* wide;
+  int width;
+
+  __device__ __forceinline__ Weight(const void* weight, bool w32, int width_) : width(width_) {
+    wide = sizeof(T) == 2 && weight && w32 ? static_cast<const float*>(weight) : nullptr;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const bool on = weight && !wide && U::col(j) < width;
+      own[j] = load_unit<T, V>(static_cast<const T*>(weight), U::col(j), on);
+      if (!on)
+#pragma unroll
+        for (int i = 0; i < V; ++i) own[j].v[i] = from_f32<T>(1.f);
+    }
+  }
+  __device__ __forceinline__ float2 at(int i) const {
+    if constexpr (sizeof(T) == 2) {
+      if (wide) {
+        if constexpr (V == 1) {
+          const int a = U::col(2 * i), b = U::col(2 * i + 1);
+          return make_float2(a < width ? wide[a] : 1.f, b < width ? wide[b] : 1.f);
+        } else {
+          const int col = U::col(i / (V / 2)) + i % (V / 2) * 2;
+          return col < width ? *reinterpret_cast<const float2*>(wide + col) : both(1.f);
+        }
+      }
+    }
+    return pair_at(own, i);
+  }
+};
 
 // Sums over the threads of a row; the whole CTA calls it.  `part` has room for the CTA's warps.
 template <int N>
@@ -107,94 +156,153 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*part)[N]) {
     for (int i = 0; i < N; ++i) v[i] += mine[w][i];
 }
 
-template <typename T, bool kFp8, bool kAligned, int NV>
-__global__ void __launch_bounds__(kNormThreads) rms_norm_kernel(const NormArgs P) {
+// Rows of each of kIn matrices on their way to this thread, kDeep of them a matrix.
+template <typename T, bool kAligned, int NV, int kIn>
+struct Ahead {
   using U = Units<T, kAligned>;
-  constexpr int V = U::V;
-  __shared__ float part[kNormThreads / 32][1];
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-  const bool live = row < P.rows;  // the others take part in the barriers
-  const T* x = static_cast<const T*>(P.x) + row * P.xs;
-  Pack<T, V> v[NV];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) v[j] = load_unit<T, V>(x, U::col(j), live && U::col(j) < P.width);
-  if (P.residual) {
-    const T* r = static_cast<const T*>(P.residual) + row * P.rs;
-    T* h = static_cast<T*>(P.h) + row * P.hs;
-    Pack<T, V> b[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) b[j] = load_unit<T, V>(r, U::col(j), live && U::col(j) < P.width);
+  static constexpr int kDeep = NV <= 2 ? 4 : NV == 4 ? 2 : 1;
+  static constexpr int kBytes = kDeep * kIn * NV * 16;  // of shared memory a thread
+  uint4* slots;  // this thread's first; the CTA's threads lie side by side
+
+  __device__ __forceinline__ uint4* slot(int stage, int in, int j) const {
+    return slots + ((stage * kIn + in) * NV + j) * (blockDim.x * blockDim.y);
+  }
+  __device__ __forceinline__ void start(int stage, int in, const void* matrix, int64_t stride,
+                                        int64_t row, int width) const {
+    const T* from = static_cast<const T*>(matrix) + row * stride;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      float f[V], g[V];
-      unit_floats<T, V>(v[j], f);
-      unit_floats<T, V>(b[j], g);
-#pragma unroll
-      for (int i = 0; i < V; ++i) f[i] += g[i];
-      v[j] = unit_of<T, V>(f);  // the sum as it is held
-      if (P.h && live && U::col(j) < P.width) store_unit<T, V>(h, U::col(j), v[j]);
+      const int col = U::col(j), bytes = col < width ? 16 : 0;  // the rest are zeros
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(static_cast<unsigned>(
+                       __cvta_generic_to_shared(slot(stage, in, j)))),
+                   "l"(from + (bytes ? col : 0)), "r"(bytes)
+                   : "memory");
     }
   }
-  float sum[1] = {0.f};
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    float f[V];
-    unit_floats<T, V>(v[j], f);
-#pragma unroll
-    for (int i = 0; i < V; ++i) sum[0] = fmaf(f[i], f[i], sum[0]);
+  static __device__ __forceinline__ void close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // All but the last kDeep - 1 groups are there.
+  static __device__ __forceinline__ void wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDeep - 1) : "memory");
   }
-  row_sums(sum, part);
-  const float u = rsqrtf(__fdiv_rn(sum[0], static_cast<float>(P.width)) + P.eps);
-  if constexpr (!kFp8) {
-    T* y = static_cast<T*>(P.y) + row * P.ys;
+  __device__ __forceinline__ Pack<T, kVec<T>> unit(int stage, int in, int j) const {
+    return *reinterpret_cast<const Pack<T, kVec<T>>*>(slot(stage, in, j));
+  }
+  __device__ __forceinline__ void read(int stage, int in, Pack<T, kVec<T>> (&v)[NV]) const {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int col = U::col(j);
-      if (!live || col >= P.width) continue;
-      float f[V], w[V];
-      unit_floats<T, V>(v[j], f);
-      load_weight<T, V>(P.weight, P.w32, col, true, w);
-#pragma unroll
-      for (int i = 0; i < V; ++i) f[i] = f[i] * u * w[i];
-      store_unit<T, V>(y, col, unit_of<T, V>(f));
+    for (int j = 0; j < NV; ++j) v[j] = unit(stage, in, j);
+  }
+};
+
+extern __shared__ uint4 norm_ring[];
+
+// kIn: 2 with a residual; rows off 16 bytes, which are loaded where they are needed, ask for it.
+template <typename T, bool kFp8, bool kAligned, int NV, int kIn>
+__global__ void __launch_bounds__(kNormThreads)
+    rms_norm_kernel(const __grid_constant__ NormArgs P) {
+  using U = Units<T, kAligned>;
+  constexpr int V = U::V, kPairs = NV * V / 2;
+  using Ring = Ahead<T, kAligned, NV, kIn>;
+  __shared__ float parts[2][kNormThreads / 32][1];
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const Ring ring = {norm_ring + threadIdx.y * blockDim.x + threadIdx.x};
+  const auto start = [&](int stage, int64_t r) {
+    if (r < P.rows) {
+      ring.start(stage, 0, P.x, P.xs, r, P.width);
+      if (kIn == 2) ring.start(stage, 1, P.residual, P.rs, r, P.width);
     }
-  } else {
-    constexpr int kUnits = kAligned ? 1 : 4;          // units of a thread in a block of 128
-    constexpr int kLanes = kAligned ? kBlock / V : 32;  // lanes that share it
-    uint8_t* q = static_cast<uint8_t*>(P.y) + row * P.ys;
-    float* scale = P.scale + row * ((P.width + kBlock - 1) / kBlock);
+    ring.close();
+  };
+  if constexpr (kAligned) {
 #pragma unroll
-    for (int j = 0; j < NV; j += kUnits) {
-      float f[kUnits * V];
-      float amax = 0.f;
+    for (int k = 0; k < Ring::kDeep; ++k) start(k, row + k * step);
+  }
+  const Weight<T, kAligned, NV> weight(P.weight, P.w32, P.width);
+  int stage = 0, turn = 0;
+  // as many rounds for all rows of the CTA
+  for (int64_t first = row - threadIdx.y; first < P.rows; first += step, row += step, turn ^= 1) {
+    const bool live = row < P.rows;  // the others take part in the barriers
+    Pack<T, V> v[NV];                // zeros from `width` on
+    if constexpr (kAligned) {
+      ring.wait();
+      ring.read(stage, 0, v);
+    } else {
+      const T* x = static_cast<const T*>(P.x) + row * P.xs;
 #pragma unroll
-      for (int k = 0; k < kUnits; ++k) {
-        const int col = U::col(j + k);
-        float g[V], w[V];
-        unit_floats<T, V>(v[j + k], g);
-        load_weight<T, V>(P.weight, P.w32, col, col < P.width, w);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float y = live && col < P.width ? g[i] * u * w[i] : 0.f;
-          f[k * V + i] = y;
-          amax = fmaxf(amax, fabsf(y));  // passes over NaN
-        }
-      }
-#pragma unroll
-      for (int o = kLanes / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, o));
-      const float s = block_scale(amax);
-      const auto e = quantized(f, s);
-      const int col = U::col(j);
-      const int first = col - (threadIdx.x % kLanes) * V;  // of the block
-      if (!live || first >= P.width) continue;
+      for (int j = 0; j < NV; ++j)
+        v[j] = load_unit<T, V>(x, U::col(j), live && U::col(j) < P.width);
+    }
+    if (kIn == 2 && (kAligned || P.residual)) {
+      Pack<T, V> b[NV];
       if constexpr (kAligned) {
-        if (col < P.width) *reinterpret_cast<Pack<uint8_t, V>*>(q + col) = e;
+        ring.read(stage, 1, b);
       } else {
+        const T* r = static_cast<const T*>(P.residual) + row * P.rs;
 #pragma unroll
-        for (int k = 0; k < kUnits; ++k)
-          if (U::col(j + k) < P.width) q[U::col(j + k)] = e.v[k];
+        for (int j = 0; j < NV; ++j)
+          b[j] = load_unit<T, V>(r, U::col(j), live && U::col(j) < P.width);
       }
-      if (threadIdx.x % kLanes == 0) scale[first / kBlock] = s;
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i)  // the sum as it is held
+        set_pair(v, i, __fadd2_rn(pair_at(v, i), pair_at(b, i)));
+      if (P.h && live) {
+        T* h = static_cast<T*>(P.h) + row * P.hs;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (U::col(j) < P.width) store_unit<T, V>(h, U::col(j), v[j]);
+      }
+    }
+    float2 squares = both(0.f);
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) squares = __ffma2_rn(pair_at(v, i), pair_at(v, i), squares);
+    float sum[1] = {squares.x + squares.y};
+    row_sums(sum, parts[turn]);
+    if constexpr (kAligned) {  // all of the row's slots have been read
+      start(stage, row + Ring::kDeep * step);
+      stage = stage + 1 == Ring::kDeep ? 0 : stage + 1;
+    }
+    const float2 u = both(rsqrtf(__fdiv_rn(sum[0], static_cast<float>(P.width)) + P.eps));
+    if constexpr (!kFp8) {
+      T* y = static_cast<T*>(P.y) + row * P.ys;
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i)
+        set_pair(v, i, __fmul2_rn(__fmul2_rn(pair_at(v, i), u), weight.at(i)));
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (live && U::col(j) < P.width) store_unit<T, V>(y, U::col(j), v[j]);
+    } else {
+      constexpr int kUnits = kAligned ? 1 : 4;          // units of a thread in a block of 128
+      constexpr int kLanes = kAligned ? kBlock / V : 32;  // lanes that share it
+      constexpr int kHeld = kUnits * V;                 // values of a thread in it
+      uint8_t* q = static_cast<uint8_t*>(P.y) + row * P.ys;
+      float* scale = P.scale + row * ((P.width + kBlock - 1) / kBlock);
+#pragma unroll
+      for (int j = 0; j < NV; j += kUnits) {
+        float f[kHeld], amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < kHeld / 2; ++k) {
+          const int i = j * V / 2 + k;
+          const float2 y = __fmul2_rn(__fmul2_rn(pair_at(v, i), u), weight.at(i));
+          f[2 * k] = y.x;
+          f[2 * k + 1] = y.y;
+          amax = fmaxf(amax, fmaxf(fabsf(y.x), fabsf(y.y)));  // passes over NaN
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, o));
+        const float s = block_scale(amax);
+        const auto e = quantized(f, s);
+        const int col = U::col(j);
+        const int first_col = col - (threadIdx.x % kLanes) * V;  // of the block
+        if (!live || first_col >= P.width) continue;
+        if constexpr (kAligned) {
+          if (col < P.width) *reinterpret_cast<Pack<uint8_t, V>*>(q + col) = e;
+        } else {
+#pragma unroll
+          for (int k = 0; k < kUnits; ++k)
+            if (U::col(j + k) < P.width) q[U::col(j + k)] = e.v[k];
+        }
+        if (threadIdx.x % kLanes == 0) scale[first_col / kBlock] = s;
+      }
     }
   }
 }
@@ -209,77 +317,125 @@ struct NormGradArgs {
   float eps;
 };
 
-// A group of threads walks rows a grid apart and keeps its columns' part of
-// grad_weight in registers.
-template <typename T, bool kAligned, int NV>
-__global__ void __launch_bounds__(kNormThreads) rms_norm_backward_kernel(const NormGradArgs P) {
+// Each thread keeps its columns' part of grad_weight in registers, and its part of the row
+// too, unless that is so much that registers run out: then both passes over it read the ring
+// (65536 x 2048 bf16 shared by 64 threads: 285 us with the row in registers).  kIn: 3 with a
+// gradient that arrives at h.
+template <typename T, bool kAligned, int NV, int kIn>
+__global__ void __launch_bounds__(kNormThreads)
+    rms_norm_backward_kernel(const __grid_constant__ NormGradArgs P) {
   using U = Units<T, kAligned>;
-  constexpr int V = U::V;
+  constexpr int V = U::V, kPairs = NV * V / 2;
+  constexpr int kStep = V == 1 ? 2 : 1, kIn1 = kStep * V / 2;  // units taken at once, their pairs
+  constexpr bool kHold = !kAligned || kPairs < 16;
+  using Ring = Ahead<T, kAligned, NV, kIn>;
   __shared__ float parts[2][kNormThreads / 32][2];
-  float acc[NV][V] = {};
-  int turn = 0;
-  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * blockDim.y; row0 < P.rows;
-       row0 += static_cast<int64_t>(gridDim.x) * blockDim.y, turn ^= 1) {
-    const int64_t row = row0 + threadIdx.y;
+  float2 acc[kPairs];
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) acc[i] = both(0.f);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const Ring ring = {norm_ring + threadIdx.y * blockDim.x + threadIdx.x};
+  const auto start = [&](int stage, int64_t r) {
+    if (r < P.rows) {
+      ring.start(stage, 0, P.h, P.hs, r, P.width);
+      ring.start(stage, 1, P.gy, P.gys, r, P.width);
+      if (kIn == 3) ring.start(stage, 2, P.gh, P.ghs, r, P.width);
+    }
+    ring.close();
+  };
+  if constexpr (kAligned) {
+#pragma unroll
+    for (int k = 0; k < Ring::kDeep; ++k) start(k, row + k * step);
+  }
+  const Weight<T, kAligned, NV> weight(P.weight, P.w32, P.width);
+  int stage = 0, turn = 0;
+  for (int64_t first = row - threadIdx.y; first < P.rows; first += step, row += step, turn ^= 1) {
     const bool live = row < P.rows;
-    const T* h = static_cast<const T*>(P.h) + row * P.hs;
-    const T* gy = static_cast<const T*>(P.gy) + row * P.gys;
-    const T* gh = static_cast<const T*>(P.gh) + row * P.ghs;
-    T* gx = static_cast<T*>(P.gx) + row * P.gxs;
-    Pack<T, V> a[NV], b[NV], c[NV];
+    const T* from[3] = {static_cast<const T*>(P.h) + row * P.hs,
+                        static_cast<const T*>(P.gy) + row * P.gys,
+                        P.gh ? static_cast<const T*>(P.gh) + row * P.ghs : nullptr};
+    if constexpr (kAligned) ring.wait();
+    Pack<T, V> held[kIn][kHold ? NV : 1];
+    if constexpr (kHold) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const bool on = live && U::col(j) < P.width;
-      a[j] = load_unit<T, V>(h, U::col(j), on);
-      b[j] = load_unit<T, V>(gy, U::col(j), on);
+      for (int in = 0; in < kIn; ++in)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          if constexpr (kAligned) held[in][j] = ring.unit(stage, in, j);
+          else
+            held[in][j] = load_unit<T, V>(from[in], U::col(j),
+                                          live && from[in] && U::col(j) < P.width);
+        }
     }
-    if (P.gh) {
+    const auto take = [&](int in, int j, Pack<T, V> (&v)[kStep]) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        c[j] = load_unit<T, V>(gh, U::col(j), live && U::col(j) < P.width);
-    }
-    float sum[2] = {0.f, 0.f};  // squares of h; d times h
+      for (int k = 0; k < kStep; ++k) {
+        if constexpr (kHold) v[k] = held[in][j + k];
+        else v[k] = ring.unit(stage, in, j + k);
+      }
+    };
+    float2 squares = both(0.f), dots = both(0.f);  // of h; of d and h
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float f[V], g[V], w[V];
-      unit_floats<T, V>(a[j], f);
-      unit_floats<T, V>(b[j], g);
-      load_weight<T, V>(P.weight, P.w32, U::col(j), U::col(j) < P.width, w);
+    for (int j = 0; j < NV; j += kStep) {
+      Pack<T, V> a[kStep], b[kStep];
+      take(0, j, a);
+      take(1, j, b);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        sum[0] = fmaf(f[i], f[i], sum[0]);
-        sum[1] = fmaf(g[i] * w[i], f[i], sum[1]);
+      for (int i = 0; i < kIn1; ++i) {
+        const float2 f = pair_at(a, i);
+        squares = __ffma2_rn(f, f, squares);
+        dots = __ffma2_rn(__fmul2_rn(pair_at(b, i), weight.at(j * V / 2 + i)), f, dots);
       }
     }
+    // what the slots of no row hold must not reach the sums
+    float sum[2] = {live ? squares.x + squares.y : 0.f, live ? dots.x + dots.y : 0.f};
     row_sums(sum, parts[turn]);
+    const int used = stage;
+    if constexpr (kAligned) {
+      if (kHold) start(used, row + Ring::kDeep * step);
+      if (kHold) stage = stage + 1 == Ring::kDeep ? 0 : stage + 1;
+    }
     const float width = static_cast<float>(P.width);
-    const float u = rsqrtf(__fdiv_rn(sum[0], width) + P.eps);
-    const float mean = __fdiv_rn(sum[1] * u, width);
+    const float2 u = both(rsqrtf(__fdiv_rn(sum[0], width) + P.eps));
+    const float2 mean = both(-__fdiv_rn(sum[1] * u.x, width));
+    T* gx = static_cast<T*>(P.gx) + row * P.gxs;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int col = U::col(j);
-      if (!live || col >= P.width) continue;
-      float f[V], g[V], w[V], r[V] = {};
-      unit_floats<T, V>(a[j], f);
-      unit_floats<T, V>(b[j], g);
-      load_weight<T, V>(P.weight, P.w32, col, true, w);
-      if (P.gh) unit_floats<T, V>(c[j], r);
+    for (int j = 0; j < NV; j += kStep) {
+      Pack<T, V> a[kStep], b[kStep], c[kStep];
+      take(0, j, a);
+      take(1, j, b);
+      if constexpr (kIn == 3) take(2, j, c);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float unit = f[i] * u;
-        acc[j][i] = fmaf(g[i], unit, acc[j][i]);
-        r[i] = fmaf(u, g[i] * w[i] - unit * mean, r[i]);
+      for (int i = 0; i < kIn1; ++i) {
+        const int at = j * V / 2 + i;
+        const float2 unit = __fmul2_rn(pair_at(a, i), u), g = pair_at(b, i);
+        if (live) acc[at] = __ffma2_rn(g, unit, acc[at]);
+        const float2 d = __ffma2_rn(unit, mean, __fmul2_rn(g, weight.at(at)));
+        if constexpr (kIn == 3) set_pair(a, i, __ffma2_rn(u, d, pair_at(c, i)));
+        else set_pair(a, i, __fmul2_rn(u, d));
       }
-      store_unit<T, V>(gx, col, unit_of<T, V>(r));
+#pragma unroll
+      for (int k = 0; k < kStep; ++k)
+        if (live && U::col(j + k) < P.width) store_unit<T, V>(gx, U::col(j + k), a[k]);
+    }
+    if constexpr (kAligned && !kHold) {
+      start(used, row + Ring::kDeep * step);
+      stage = stage + 1 == Ring::kDeep ? 0 : stage + 1;
     }
   }
   if (!P.partial) return;
   float* to = P.partial + (static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y) * P.width;
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (U::col(j) < P.width) to[U::col(j) + i] = acc[j][i];
+  for (int i = 0; i < kPairs; ++i) {
+    if constexpr (V == 1) {
+      if (U::col(2 * i) < P.width) to[U::col(2 * i)] = acc[i].x;
+      if (U::col(2 * i + 1) < P.width) to[U::col(2 * i + 1)] = acc[i].y;
+    } else {
+      const int col = U::col(i / (V / 2)) + i % (V / 2) * 2;
+      if (col < P.width) to[col] = acc[i].x, to[col + 1] = acc[i].y;
+    }
+  }
 }
 
 // Sums of the columns of [parts][width], 32 columns a CTA: every segment of the
@@ -314,28 +470,82 @@ tbe_status check_norm(int32_t dtype, const void* weight, int32_t weight_dtype, i
   return TBE_OK;
 }
 
+// Vectors of a thread, at most: TBE_MAX_NORM_WIDTH columns over kNormThreads threads.
+template <typename T>
+constexpr int kMostUnits = TBE_MAX_NORM_WIDTH / kVec<T> / kNormThreads;
+
 struct Shape {
   int threads, units, rows;  // of a row, of a thread, of a CTA
 };
 
-// How a row is shared: `units` vectors or elements a row, `least` to `most` of them a thread.
+// How a row of `units` vectors or elements is shared: `wanted` of them a thread where that
+// leaves at least a warp and at most kNormThreads, `least` to `most` in the end; and rows
+// of a CTA, up to `cta` threads and while there are several CTAs a multiprocessor.
 Shape shape_of(int64_t rows, int64_t units, int least, int most, int wanted) {
   int threads = 32;
   while (threads < kNormThreads && threads * wanted < units) threads *= 2;
   int per = least;
   while (per * threads < units && per < most) per *= 2;
-  Shape s = {threads, per, 1};
-  while (s.rows * s.threads < kNormCta && s.rows * 152 * 4 < rows) s.rows *= 2;
+  return {threads, per, 1};
+}
+Shape with_rows(Shape s, int64_t rows, int cta) {
+  while (s.rows * s.threads < cta && s.rows * 152 * 4 < rows) s.rows *= 2;
   return s;
 }
 
+// Forward: four vectors a thread (65536 x 2048 bf16 with a residual to 8 bits: one 178 us, two 167,
+// four 153; 16384 x 8192: two 184, four 159), but one while the rows are few and latency counts.
+// Rows of one warp share a CTA of 256 threads; the others' barriers would tie rows to one another
+// (153 us with a row a CTA, 160 with four).
+Shape forward_shape(int64_t rows, int64_t vectors, int most) {
+  const Shape s = shape_of(rows, vectors, 1, most, rows < 152 * 4 ? 1 : 4);
+  return with_rows(s, rows, s.threads == 32 ? 256 : s.threads);
+}
+// Backward: two vectors a thread (65536 x 2048 bf16: one 199 us, two 161, four 222), in CTAs of
+// 256 threads for wide rows (128 threads: 172 us), of 64 or 128 for narrow ones (65536 x 1024
+// fp16: 68 us, 256 threads 73; x 256 bf16: 30 and 32).
+Shape backward_shape(int64_t rows, int64_t vectors, int most) {
+  const Shape s = shape_of(rows, vectors, 1, most, 2);
+  return with_rows(s, rows, s.threads == 32 ? 128 : s.threads == 64 ? 64 : 256);
+}
+
+// CTAs of a launch: as many as fit the GPU with `bytes` of shared memory and as many registers a
+// thread, or fewer.
+int64_t ctas_of(const Shape& s, int64_t rows, int bytes, int registers) {
+  const int threads = s.threads * s.rows;
+  const int regs = 65536 / ((registers + 7) / 8 * 8) / threads;
+  const int fit = std::max(1, std::min({regs, 2048 / threads, kNormShared / (bytes * threads + 1024), 32}));
+  return std::min<int64_t>((rows + s.rows - 1) / s.rows, int64_t(152) * fit);
+}
+
+template <typename Args>
+int registers_of(void (*kernel)(Args)) {
+  cudaFuncAttributes a;
+  return cudaFuncGetAttributes(&a, kernel) == cudaSuccess ? a.numRegs : 128;
+}
+
+template <typename Args>
+tbe_status launch_norm(void (*kernel)(Args), const Args& args, const Shape& s, int64_t ctas,
+                       int bytes, void* stream) {
+  const int smem = bytes * s.threads * s.rows;
+  if (smem > 40 * 1024 &&  // beside what is declared in the kernels
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return TBE_ECUDA;
+  kernel<<<static_cast<unsigned>(ctas), dim3(s.threads, s.rows), smem,
+           static_cast<cudaStream_t>(stream)>>>(args);
+  return launched();
+}
+
+template <int N>
+using Int = std::integral_constant<int, N>;
+
 // Calls f with the number of units of a thread as a constant.
-template <int kLeast, typename F>
+template <int kLeast, int kMost, typename F>
 void for_units(int units, F f) {
-  if (units == kLeast) f(std::integral_constant<int, kLeast>{});
-  else if (units == kLeast * 2) f(std::integral_constant<int, kLeast * 2>{});
-  else if (units == kLeast * 4) f(std::integral_constant<int, kLeast * 4>{});
-  else f(std::integral_constant<int, kLeast * 8>{});
+  if (units == kLeast) f(Int<kLeast>{});
+  else if (units == kLeast * 2) f(Int<kLeast * 2>{});
+  else if (units == kLeast * 4 || kMost == kLeast * 4) f(Int<kLeast * 4>{});
+  else f(Int<kMost>{});
 }
 
 template <bool kFp8>
@@ -370,17 +580,25 @@ tbe_status run_norm(const void* x, const void* residual, const void* weight, int
                          weight_dtype == TBE_DT_F32, eps};
   return for_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    const auto go = [&](auto aligned, const Shape& s) {
+    const auto go = [&](auto aligned, auto in, const Shape& s) {
       constexpr bool kAligned = decltype(aligned)::value;
-      for_units<kAligned ? 1 : 4>(s.units, [&](auto n) {
-        rms_norm_kernel<T, kFp8, kAligned, decltype(n)::value>
-            <<<static_cast<unsigned>((rows + s.rows - 1) / s.rows), dim3(s.threads, s.rows), 0,
-               static_cast<cudaStream_t>(stream)>>>(args);
+      constexpr int kIn = decltype(in)::value;
+      tbe_status st = TBE_OK;
+      for_units<kAligned ? 1 : 4, kAligned ? kMostUnits<T> : 32>(s.units, [&](auto n) {
+        constexpr int NV = decltype(n)::value;
+        constexpr int kBytes = kAligned ? Ahead<T, kAligned, NV, kIn>::kBytes : 0;
+        const auto kernel = rms_norm_kernel<T, kFp8, kAligned, NV, kIn>;
+        static const int registers = registers_of(kernel);
+        const int64_t ctas = kAligned ? ctas_of(s, rows, kBytes, registers) : (rows + s.rows - 1) / s.rows;
+        st = launch_norm(kernel, args, s, ctas, kBytes, stream);
       });
-      return launched();
+      return st;
     };
-    if (vec) return go(std::true_type{}, shape_of(rows, width / kVec<T>, 1, 8, rows < 608 ? 1 : 4));
-    return go(std::false_type{}, shape_of(rows, width, 4, 32, 8));
+    const auto with = [&](auto in) {
+      return go(std::true_type{}, in, forward_shape(rows, width / kVec<T>, kMostUnits<T>));
+    };
+    if (!vec) return go(std::false_type{}, Int<2>{}, with_rows(shape_of(rows, width, 4, 32, 8), rows, 256));
+    return residual ? with(Int<2>{}) : with(Int<1>{});
   });
 }
 
@@ -454,27 +672,36 @@ extern "C" tbe_status tbe_rms_norm_backward(const void* grad_y, const void* h, c
     const bool vec = in[0].vectors(width, 16) && in[1].vectors(width, 16) &&
                      (!grad_h || in[2].vectors(width, 16)) && out.vectors(width, 16) &&
                      aligned_to(weight, 16);
-    NormGradArgs args = {grad_y, h, weight, grad_h, grad_x,
+    const NormGradArgs args = {grad_y, h, weight, grad_h, grad_x,
                          grad_weight ? static_cast<float*>(workspace) : nullptr,
                          grad_y_stride, h_stride, grad_h_stride, grad_x_stride,
                          static_cast<int>(rows), static_cast<int>(width),
                          weight_dtype == TBE_DT_F32, eps};
     const tbe_status st = for_dtype(dtype, [&](auto t) {
       using T = decltype(t);
-      const auto go = [&](auto aligned, Shape sh) {
+      const auto go = [&](auto aligned, auto in, Shape sh) {
         constexpr bool kAligned = decltype(aligned)::value;
+        constexpr int kIn = decltype(in)::value;
         while (sh.rows > rows) sh.rows /= 2;
-        const int64_t groups = rows / sh.rows, most = kNormParts / sh.rows;
-        const int ctas = static_cast<int>(groups < most ? groups : most);
-        parts = ctas * sh.rows;
-        for_units<kAligned ? 1 : 4>(sh.units, [&](auto n) {
-          rms_norm_backward_kernel<T, kAligned, decltype(n)::value>
-              <<<ctas, dim3(sh.threads, sh.rows), 0, s>>>(args);
+        tbe_status st = TBE_OK;
+        for_units<kAligned ? 1 : 4, kAligned ? kMostUnits<T> : 32>(sh.units, [&](auto n) {
+          constexpr int NV = decltype(n)::value;
+          constexpr int kBytes = kAligned ? Ahead<T, kAligned, NV, kIn>::kBytes : 0;
+          // whole groups of rows only, so that the parts are no more than the rows
+          const auto kernel = rms_norm_backward_kernel<T, kAligned, NV, kIn>;
+          static const int registers = registers_of(kernel);
+          const int64_t ctas = std::min({ctas_of(sh, rows, kBytes, registers), rows / sh.rows,
+                                         int64_t(kNormParts / sh.rows)});
+          parts = static_cast<int>(ctas) * sh.rows;
+          st = launch_norm(kernel, args, sh, ctas, kBytes, s);
         });
-        return launched();
+        return st;
       };
-      if (vec) return go(std::true_type{}, shape_of(rows, width / kVec<T>, 1, 8, 1));
-      return go(std::false_type{}, shape_of(rows, width, 4, 32, 4));
+      const auto with = [&](auto in) {
+        return go(std::true_type{}, in, backward_shape(rows, width / kVec<T>, kMostUnits<T>));
+      };
+      if (!vec) return go(std::false_type{}, Int<3>{}, with_rows(shape_of(rows, width, 4, 32, 4), rows, 256));
+      return grad_h ? with(Int<3>{}) : with(Int<2>{});
     });
     if (st != TBE_OK) return st;
   }
