@@ -268,15 +268,20 @@ __global__ void __launch_bounds__(kSortWarps * 32)
 
 // ------------------------------------------------------------------ gradient
 //
-// The sorted items are cut into pieces of `piece` places.  A group of threads sums a piece's
-// runs of equal rows, a vector of columns a thread, and writes the rows whose run lies
-// within the piece.  A run that crosses pieces leaves its part in each: slot 0 where it
-// began before the piece, slot 1 where it begins in it and goes on.  A second launch adds
-// those parts in the pieces' order.  Rows without tokens are cleared before.
-constexpr int kLeastPiece = 32;
-constexpr int kMostPieces = 4096;
-constexpr int kRowsInFlight = 8;
-constexpr int kJoinSegments = 8;
+// The sorted items are cut into pieces of `piece` places.  A group of threads sums the runs
+// of equal rows that begin in its piece, a vector of columns a thread, and writes their
+// rows.  A run that crosses a boundary belongs to the piece it begins in, which follows it into
+// the next one; but where it crosses two boundaries it is long, and each of its pieces leaves
+// its part: slot 0 where the run began before the piece, slot 1 where it begins in it.  A second
+// launch adds those parts in the pieces' order.  Rows without tokens are cleared before.
+//
+// What bounds it is how many rows' loads are on their way, so each thread copies its own columns of
+// the next rows to a ring in shared memory (cp.async) while it adds the row at hand.
+constexpr int kLeastPiece = 8, kMostPiece = 64;
+constexpr int kSumGroups = 152 * 8;  // groups that fill the GPU
+constexpr int kJoinPieces = 8;       // pieces whose ends a CTA looks at
+constexpr int kJoinSegments = 4;
+constexpr int kJoinLanes = 64;       // vectors of four columns of a CTA
 
 struct SumArgs {
   const void* grad_out;
@@ -292,22 +297,6 @@ struct SumArgs {
 __device__ __forceinline__ Item item_at(const Item* items, int64_t i) {
   const int2 v = *reinterpret_cast<const int2*>(items + i);
   return {v.x, v.y};
-}
-
-// Columns col .. col + V - 1 of a row, zeros from `width` on.
-template <typename T, bool kAligned>
-__device__ __forceinline__ Pack<T, kVec<T>> load_columns(const T* row, int col, int width) {
-  constexpr int V = kVec<T>;
-  // the aligned vectors around an inner one lie within the row
-  if constexpr (kAligned) {
-    return load_vec<T, true>(row + col);
-  } else {
-    if (col >= V && col + 2 * V <= width) return load_vec<T, false>(row + col);
-    Pack<T, V> p;
-#pragma unroll
-    for (int i = 0; i < V; ++i) p.v[i] = col + i < width ? row[col + i] : from_f32<T>(0.f);
-    return p;
-  }
 }
 
 // Rounds N sums into columns col .. of a row of the result.
@@ -332,92 +321,195 @@ __device__ __forceinline__ void store_sums(const SumArgs& P, int row, int col,
   }
 }
 
+// Whether the run of `row` that crosses the boundary `at` between two pieces crosses the boundary
+// before or behind it too.  row_at(i): the row of the i-th place.
+template <typename RowAt>
+__device__ __forceinline__ bool is_long(const SumArgs& P, int64_t at, int row, RowAt row_at) {
+  return (at + P.piece < P.n && row_at(at + P.piece) == row) ||
+         (at > P.piece && row_at(at - P.piece - 1) == row);
+}
+
+// Rows of grad_out on their way to a thread: its vector of each, or where rows are off 16
+// bytes, the two aligned vectors around it.  (16 bytes that hold a byte of a row lie in its
+// allocation; what is not the row's is not used.)
+template <typename T, bool kAligned>
+struct RowsAhead {
+  static constexpr int V = kVec<T>, kSlots = kAligned ? 1 : 2;
+  static constexpr int kDeep = kAligned ? 8 : 6;
+  static constexpr int kBytes = kDeep * kSlots * 16;  // a thread
+  uint4* slots;  // this thread's first; the CTA's threads lie side by side
+
+  __device__ __forceinline__ uint4* slot(int stage, int k) const {
+    return slots + (stage * kSlots + k) * kMoveThreads;
+  }
+  __device__ __forceinline__ void start(int stage, const T* row, int col, int width) const {
+    if constexpr (kAligned) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<unsigned>(
+                       __cvta_generic_to_shared(slot(stage, 0)))),
+                   "l"(row + col)
+                   : "memory");
+    } else {
+      const T* from = row + col - lead<T>(row + col);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (from + k * V < row + width)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(static_cast<unsigned>(
+                           __cvta_generic_to_shared(slot(stage, k)))),
+                       "l"(from + k * V)
+                       : "memory");
+    }
+  }
+  static __device__ __forceinline__ void close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // All but the last kDeep - 1 rows are there.
+  static __device__ __forceinline__ void wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDeep - 1) : "memory");
+  }
+  // The thread's columns; what lies past the row's end is not defined.
+  __device__ __forceinline__ Pack<T, V> read(int stage, const T* row, int col) const {
+    if constexpr (kAligned) {
+      return *reinterpret_cast<const Pack<T, V>*>(slot(stage, 0));
+    } else {
+      const uint4 o = cut_row(*slot(stage, 0), *slot(stage, 1),
+                              lead<T>(row + col) * static_cast<int>(sizeof(T)));
+      return *reinterpret_cast<const Pack<T, V>*>(&o);
+    }
+  }
+};
+
+extern __shared__ uint4 embed_ring[];
+
 template <typename T, typename O, bool kAligned>
 __global__ void __launch_bounds__(kMoveThreads)
-    embed_sum_kernel(const SumArgs P, int log_group) {
+    embed_sum_kernel(const __grid_constant__ SumArgs P, int log_group) {
   constexpr int V = kVec<T>;
+  using Ring = RowsAhead<T, kAligned>;
+  const int groups = kMoveThreads >> log_group;
   const int size = 1 << log_group, t = threadIdx.x & (size - 1);
-  const int64_t piece = static_cast<int64_t>(blockIdx.x) * (kMoveThreads >> log_group) +
-                        (threadIdx.x >> log_group);
+  // the items of the CTA's pieces, of the one before and of the one behind
+  Item* window = reinterpret_cast<Item*>(embed_ring + Ring::kDeep * Ring::kSlots * kMoveThreads);
+  const int64_t piece0 = static_cast<int64_t>(blockIdx.x) * groups;
+  const int64_t base = (piece0 - 1) * P.piece - 1;
+  for (int i = threadIdx.x; i < (groups + 2) * P.piece + 2; i += kMoveThreads)
+    window[i] = base + i >= 0 && base + i < P.n ? item_at(P.items, base + i) : Item{P.rows, 0};
+  __syncthreads();
+  const auto item = [&](int64_t i) { return window[i - base]; };
+  const auto row_at = [&](int64_t i) { return window[i - base].row; };
+
+  const int64_t piece = piece0 + (threadIdx.x >> log_group);
   const int col = (blockIdx.y * size + t) * V;
   const int64_t first = piece * P.piece;
   if (first >= P.n || col >= P.width) return;
   const int64_t last = first + P.piece < P.n ? first + P.piece : P.n;
-  int run = item_at(P.items, first).row;
+  int run = row_at(first);
   if (run >= P.rows) return;
-  bool open = first > 0 && item_at(P.items, first - 1).row == run;  // it began before
-  float* parts = P.parts + piece * 2 * P.part_width + col;
+  int skip = -1;      // a row that the piece before sums
+  bool open = false;  // the run has a part before this one
+  if (first > 0 && row_at(first - 1) == run) {
+    open = is_long(P, first, run, row_at);
+    if (!open) skip = run;
+  }
+  const int tail = row_at(last - 1);
+  bool leaves = false;  // the last run's part goes on in the next piece
+  int64_t end = last;
+  if (last < P.n && tail < P.rows && row_at(last) == tail) {
+    leaves = is_long(P, last, tail, row_at);
+    while (!leaves && end < P.n && row_at(end) == tail) ++end;  // at most a piece on
+  }
   const T* grad = static_cast<const T*>(P.grad_out);
+  const Ring ring = {embed_ring + threadIdx.x};
+  const auto start = [&](int stage, int64_t i) {
+    if (i < end) {
+      const Item it = item(i);
+      if (it.row < P.rows && it.row != skip)
+        ring.start(stage, grad + it.token * P.grad_stride, col, P.width);
+    }
+    ring.close();
+  };
+#pragma unroll
+  for (int k = 0; k < Ring::kDeep; ++k) start(k, first + k);
+
   float sum[V] = {};
   const auto leave = [&](int slot) {
+    float* parts = P.parts + (piece * 2 + slot) * P.part_width + col;
 #pragma unroll
     for (int i = 0; i < V; i += 4)
-      *reinterpret_cast<float4*>(parts + slot * P.part_width + i) =
-          make_float4(sum[i], sum[i + 1], sum[i + 2], sum[i + 3]);
+      *reinterpret_cast<float4*>(parts + i) = make_float4(sum[i], sum[i + 1], sum[i + 2], sum[i + 3]);
   };
-  for (int64_t i0 = first; i0 < last; i0 += kRowsInFlight) {
-    Item it[kRowsInFlight];
-    Pack<T, V> v[kRowsInFlight];
+  const auto finish = [&] {  // the run ends here
+    if (open) leave(0);
+    else if (run != skip) store_sums<O, V, kAligned>(P, run, col, sum);
+    open = false;
+  };
+  int stage = 0;
+  for (int64_t i = first; i < end; ++i) {
+    const Item it = item(i);
+    if (it.row >= P.rows) break;  // no more tokens of rows
+    if (it.row != run) {
+      finish();
+      run = it.row;
 #pragma unroll
-    for (int u = 0; u < kRowsInFlight; ++u) {
-      it[u] = i0 + u < last ? item_at(P.items, i0 + u) : Item{P.rows, 0};
-      if (it[u].row < P.rows)
-        v[u] = load_columns<T, kAligned>(grad + it[u].token * P.grad_stride, col, P.width);
+      for (int c = 0; c < V; ++c) sum[c] = 0.f;
     }
-#pragma unroll
-    for (int u = 0; u < kRowsInFlight; ++u) {
-      if (i0 + u >= last) break;
-      if (it[u].row != run) {
-        if (open) leave(0);
-        else store_sums<O, V, kAligned>(P, run, col, sum);
-        open = false;
-        run = it[u].row;
-#pragma unroll
-        for (int i = 0; i < V; ++i) sum[i] = 0.f;
-      }
-      if (run >= P.rows) return;
+    ring.wait();
+    if (run != skip) {
       float f[V];
-      to_floats<T>(v[u], f);
+      to_floats<T>(ring.read(stage, grad + it.token * P.grad_stride, col), f);
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum[i] += f[i];
+      for (int c = 0; c < V; ++c) sum[c] += f[c];
     }
+    start(stage, i + Ring::kDeep);
+    stage = stage + 1 == Ring::kDeep ? 0 : stage + 1;
   }
-  if (open) leave(0);
-  else if (last < P.n && item_at(P.items, last).row == run) leave(1);
-  else store_sums<O, V, kAligned>(P, run, col, sum);
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (leaves) leave(open ? 0 : 1);
+  else finish();
 }
 
-// Adds the parts of the run that begins in piece blockIdx.x and crosses its end, if there is
-// one: 32 threads a vector of four columns each, the pieces shared by eight segments of them.
+// Adds the parts of the long runs.  A CTA looks at the ends of kJoinPieces pieces, a lane each,
+// for long runs that begin before them, and forms kJoinLanes * 4 columns of each, the
+// run's pieces shared by kJoinSegments segments of threads.
 template <typename O>
-__global__ void __launch_bounds__(32 * kJoinSegments) embed_join_kernel(const SumArgs P) {
-  __shared__ float4 sums[kJoinSegments][32];
-  const int64_t piece = blockIdx.x;
-  const int64_t first = piece * P.piece, end = first + P.piece;
-  if (end >= P.n) return;
-  const int run = item_at(P.items, end).row;
-  if (run >= P.rows || item_at(P.items, end - 1).row != run ||
-      (first > 0 && item_at(P.items, first - 1).row == run))
-    return;
-  const int col = (blockIdx.y * 32 + threadIdx.x) * 4;
+__global__ void __launch_bounds__(kJoinLanes * kJoinSegments)
+    embed_join_kernel(const __grid_constant__ SumArgs P) {
+  __shared__ float4 sums[kJoinSegments][kJoinLanes];
+  const int lane = threadIdx.x & 31, segment = threadIdx.x / kJoinLanes;
+  const int col = (blockIdx.y * kJoinLanes + threadIdx.x % kJoinLanes) * 4;
   const bool on = col < P.part_width;
-  const auto part = [&](int64_t p, int slot) {
-    return *reinterpret_cast<const float4*>(P.parts + (p * 2 + slot) * P.part_width + col);
-  };
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  const auto add = [&](float4 v) { s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w; };
-#pragma unroll 4
-  for (int64_t p = piece + 1 + threadIdx.y;
-       p * P.piece < P.n && item_at(P.items, p * P.piece).row == run; p += kJoinSegments)
-    if (on) add(part(p, 0));
-  sums[threadIdx.y][threadIdx.x] = s;
-  __syncthreads();
-  if (threadIdx.y || !on) return;
-  s = part(piece, 1);
+  const auto row_at = [&](int64_t i) { return i < P.n ? item_at(P.items, i).row : P.rows; };
+  const int64_t piece0 = static_cast<int64_t>(blockIdx.x) * kJoinPieces;
+  const int64_t end = (piece0 + lane + 1) * P.piece;
+  const int run_here = lane < kJoinPieces ? row_at(end) : P.rows;
+  const bool found = run_here < P.rows && row_at(end - 1) == run_here &&
+                     (end == P.piece || row_at(end - P.piece - 1) != run_here) &&
+                     is_long(P, end, run_here, row_at);
+  for (unsigned todo = __ballot_sync(kAll, found); todo; todo &= todo - 1) {
+    const int64_t piece = piece0 + __ffs(todo) - 1;
+    const int run = __shfl_sync(kAll, run_here, __ffs(todo) - 1);
+    int more = 0;  // pieces behind, looked through 32 at a time
+    for (unsigned all = kAll; all == kAll;) {
+      all = __ballot_sync(kAll, row_at((piece + 1 + more + lane) * P.piece) == run);
+      more += __popc(all);
+    }
+    const auto part = [&](int64_t p, int slot) {
+      return *reinterpret_cast<const float4*>(P.parts + (p * 2 + slot) * P.part_width + col);
+    };
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    const auto add = [&](float4 v) { s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w; };
+    if (on) {
+#pragma unroll 8
+      for (int k = 1 + segment; k <= more; k += kJoinSegments) add(part(piece + k, 0));
+    }
+    __syncthreads();  // the sums of the run before have been read
+    sums[segment][threadIdx.x % kJoinLanes] = s;
+    __syncthreads();
+    if (segment == 0 && on) {
+      s = part(piece, 1);
 #pragma unroll
-  for (int i = 0; i < kJoinSegments; ++i) add(sums[i][threadIdx.x]);
-  const float v[4] = {s.x, s.y, s.z, s.w};
-  store_sums<O, 4, false>(P, run, col, v);
+      for (int i = 0; i < kJoinSegments; ++i) add(sums[i][threadIdx.x]);
+      const float v[4] = {s.x, s.y, s.z, s.w};
+      store_sums<O, 4, false>(P, run, col, v);
+    }
+  }
 }
 
 // Zeros: rows of `bytes` bytes, `pitch` apart, the last of `last` bytes; `unit` bytes divide
@@ -464,9 +556,12 @@ SortPlan plan_of(int64_t tokens, int64_t rows) {
   return p;
 }
 
-int64_t piece_of(int64_t tokens) {
+// Places of a piece: few while that leaves the GPU idle, more as the tokens are more, since a
+// long run has a part in each.
+int64_t piece_of(int64_t tokens, int64_t width) {
+  const int64_t groups = (width + 2047) / 2048;  // of a piece, at most
   int64_t piece = kLeastPiece;
-  while (piece * kMostPieces < tokens) piece *= 2;
+  while (piece < kMostPiece && tokens * groups > 2 * piece * kSumGroups) piece *= 2;
   return piece;
 }
 
@@ -482,7 +577,7 @@ Layout layout_of(int64_t tokens, int64_t width) {
   l.totals = l.items[1] + up(tokens * 8);
   l.sums = l.totals + (tokens > kOneLaunch ? up(int64_t(kGridCtas) * 4 << kDigitBits) : 0);
   l.parts = l.sums + (tokens > kOneLaunch ? up(int64_t(4) << kDigitBits) : 0);
-  const int64_t pieces = (tokens + piece_of(tokens) - 1) / piece_of(tokens);
+  const int64_t piece = piece_of(tokens, width), pieces = (tokens + piece - 1) / piece;
   l.bytes = l.parts + pieces * 2 * ((width + 7) / 8 * 8) * 4;
   return l;
 }
@@ -497,7 +592,7 @@ bool check_ids(const void* ids, int32_t dtype, int64_t tokens) {
 }
 
 cudaError_t room_for(const void* kernel, size_t smem) {
-  return smem <= 48 * 1024 ? cudaSuccess
+  return smem <= 40 * 1024 ? cudaSuccess  // beside what is declared in the kernels
                            : cudaFuncSetAttribute(kernel,
                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                   static_cast<int>(smem));
@@ -685,7 +780,7 @@ extern "C" tbe_status tbe_embed_backward(const void* grad_out, int32_t dtype, in
   if (st == TBE_OK && !accumulate)
     st = clear(grad_table, rows, width, grad_table_stride, ob, in_cluster, s);
   if (st != TBE_OK) return st;
-  const int64_t piece = piece_of(tokens), pieces = (tokens + piece - 1) / piece;
+  const int64_t piece = piece_of(tokens, width), pieces = (tokens + piece - 1) / piece;
   const SumArgs args = {grad_out, plan.items[(plan.passes + 1) & 1], grad_table,
                         reinterpret_cast<float*>(w + l.parts), grad_out_stride, grad_table_stride,
                         static_cast<int>(tokens), static_cast<int>(rows), static_cast<int>(width),
@@ -701,12 +796,17 @@ extern "C" tbe_status tbe_embed_backward(const void* grad_out, int32_t dtype, in
       const int per = kMoveThreads >> lg;
       const dim3 grid(static_cast<unsigned>((pieces + per - 1) / per),
                       static_cast<unsigned>((places + (1 << lg) - 1) >> lg));
-      embed_sum_kernel<T, O, kAligned><<<grid, kMoveThreads, 0, s>>>(args, lg);
+      const auto kernel = embed_sum_kernel<T, O, kAligned>;
+      const size_t smem = RowsAhead<T, kAligned>::kBytes * kMoveThreads +
+                          ((per + 2) * piece + 2) * sizeof(Item);
+      if (room_for(reinterpret_cast<const void*>(kernel), smem) != cudaSuccess) return TBE_ECUDA;
+      kernel<<<grid, kMoveThreads, smem, s>>>(args, lg);
+      if (pieces < 3) return launched();  // no run is long
       note_launch();
-      if (pieces > 1)
-        embed_join_kernel<O><<<dim3(static_cast<unsigned>(pieces - 1),
-                                    static_cast<unsigned>((width + 127) / 128)),
-                               dim3(32, kJoinSegments), 0, s>>>(args);
+      embed_join_kernel<O><<<dim3(static_cast<unsigned>((pieces + kJoinPieces - 1) / kJoinPieces),
+                                  static_cast<unsigned>((width + 4 * kJoinLanes - 1) /
+                                                        (4 * kJoinLanes))),
+                             kJoinLanes * kJoinSegments, 0, s>>>(args);
       return launched();
     };
     const auto to_type = [&](auto aligned) {
