@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kMoveThreads)
 constexpr int kDigitBits = 10;  // of a pass, at most
 constexpr int kSortUnroll = 4;
 constexpr int kOneLaunch = 131072;
-constexpr int kTokensPerCta = 2048;   // from which another CTA of the cluster pays
+constexpr int kTokensPerCta = 1024;   // from which another CTA of the cluster pays (4097: 12.4 us at 2048)
 constexpr int kGridCtas = 304;
 constexpr int kGridChunk = 4096;      // items of a CTA of three launches, at least
 
@@ -280,8 +280,8 @@ __global__ void __launch_bounds__(kSortWarps * 32)
 constexpr int kLeastPiece = 8, kMostPiece = 64;
 constexpr int kSumGroups = 152 * 8;  // groups that fill the GPU
 constexpr int kJoinPieces = 8;       // pieces whose ends a CTA looks at
-constexpr int kJoinSegments = 4;
-constexpr int kJoinLanes = 64;       // vectors of four columns of a CTA
+constexpr int kJoinSegments = 8;
+constexpr int kJoinLanes = 32;       // vectors of four columns of a CTA
 
 struct SumArgs {
   const void* grad_out;
@@ -389,6 +389,8 @@ __global__ void __launch_bounds__(kMoveThreads)
   Item* window = reinterpret_cast<Item*>(embed_ring + Ring::kDeep * Ring::kSlots * kMoveThreads);
   const int64_t piece0 = static_cast<int64_t>(blockIdx.x) * groups;
   const int64_t base = (piece0 - 1) * P.piece - 1;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int i = threadIdx.x; i < (groups + 2) * P.piece + 2; i += kMoveThreads)
     window[i] = base + i >= 0 && base + i < P.n ? item_at(P.items, base + i) : Item{P.rows, 0};
   __syncthreads();
@@ -482,6 +484,8 @@ __global__ void __launch_bounds__(kJoinLanes * kJoinSegments)
   const bool found = run_here < P.rows && row_at(end - 1) == run_here &&
                      (end == P.piece || row_at(end - P.piece - 1) != run_here) &&
                      is_long(P, end, run_here, row_at);
+  // The items were there when the sums began; the sums' parts and rows are now.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   for (unsigned todo = __ballot_sync(kAll, found); todo; todo &= todo - 1) {
     const int64_t piece = piece0 + __ffs(todo) - 1;
     const int run = __shfl_sync(kAll, run_here, __ffs(todo) - 1);
@@ -510,6 +514,120 @@ __global__ void __launch_bounds__(kJoinLanes * kJoinSegments)
       store_sums<O, 4, false>(P, run, col, v);
     }
   }
+}
+
+// -------------------------------------------------------- gradient, few tokens
+//
+// In one launch, without a sort: every CTA reads all ids.  The first CTAs have a token each, and
+// the one with a row's first token lists the row's tokens in their order and sums them; a
+// CTA's groups of threads take equal parts of a long list, added in their order.  The other
+// CTAs clear the rows of their range that have no token.
+constexpr int kFewTokens = 512;
+constexpr int kFewRows = 32768;  // of a clearing CTA, at most: a bit each in its shared memory
+
+template <typename IdT>
+struct FewArgs {
+  SumArgs sum;  // of which items, parts, part_width and piece are not used
+  const IdT* ids;
+  int range;  // rows of a clearing CTA
+};
+
+template <typename T, typename O, typename IdT, bool kAligned>
+__global__ void __launch_bounds__(kMoveThreads)
+    embed_few_kernel(const __grid_constant__ FewArgs<IdT> A, int log_group) {
+  constexpr int V = kVec<T>, kInBatch = 8;
+  const SumArgs& P = A.sum;
+  __shared__ int list[kFewTokens];
+  __shared__ unsigned found[kFewTokens / 32];
+  extern __shared__ float few_sums[];  // [groups][size * V]
+  const FromIds<IdT> from = {A.ids, P.rows};
+  const int groups = kMoveThreads >> log_group, size = 1 << log_group;
+  const int group = threadIdx.x >> log_group, t = threadIdx.x & (size - 1);
+  const int lane = threadIdx.x & 31;
+  if (static_cast<int>(blockIdx.x) >= P.n) {
+    const int64_t r0 = (static_cast<int64_t>(blockIdx.x - P.n) * gridDim.y + blockIdx.y) * A.range;
+    if (r0 >= P.rows) return;
+    const int rows = static_cast<int>(P.rows - r0 < A.range ? P.rows - r0 : A.range);
+    // which of them have tokens, a bit each
+    unsigned* has = reinterpret_cast<unsigned*>(few_sums);
+    for (int i = threadIdx.x; i < (A.range + 31) / 32; i += kMoveThreads) has[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < P.n; i += kMoveThreads) {
+      const int64_t r = from(i).row - r0;
+      if (r >= 0 && r < rows) atomicOr(has + (r >> 5), 1u << (r & 31));
+    }
+    __syncthreads();
+    Pack<O, kVec<O>> zero;
+#pragma unroll
+    for (int i = 0; i < kVec<O>; ++i) zero.v[i] = from_f32<O>(0.f);
+    for (int r = group; r < rows; r += groups) {
+      if (has[r >> 5] >> (r & 31) & 1) continue;
+      O* row = static_cast<O*>(P.out) + (r0 + r) * P.out_stride;
+      const Span s = inner_span<O, kAligned>(row, P.width);
+      for (int e = s.lo + t * kVec<O>; e < s.hi; e += size * kVec<O>) store_vec(row + e, zero);
+      for_ends(s, P.width, t, size, [&](int e) { row[e] = from_f32<O>(0.f); });
+    }
+    return;
+  }
+  const int token = blockIdx.x, run = from(token).row;
+  if (run >= P.rows) return;
+  bool before = false;
+  for (int i0 = 0; i0 < P.n; i0 += kMoveThreads) {
+    const int i = i0 + threadIdx.x;
+    const bool same = i < P.n && from(i).row == run;
+    before |= same && i < token;
+    const unsigned all = __ballot_sync(kAll, same);
+    if (lane == 0 && i < kFewTokens) found[i >> 5] = all;
+  }
+  if (__syncthreads_or(before)) return;  // an earlier token's CTA does it
+  int count = 0;
+  for (int w = 0; w < (P.n + 31) / 32; ++w) {
+    const unsigned all = found[w];
+    if (w % (kMoveThreads / 32) == static_cast<int>(threadIdx.x >> 5) && all >> lane & 1)
+      list[count + __popc(all & ((1u << lane) - 1))] = w * 32 + lane;
+    count += __popc(all);
+  }
+  __syncthreads();
+  // this group's part of the list
+  const int per = (count + groups - 1) / groups, first = group * per;
+  const int last = first + per < count ? first + per : count;
+  const int col = (blockIdx.y * size + t) * V;
+  const T* grad = static_cast<const T*>(P.grad_out);
+  float sum[V] = {};
+  for (int i0 = first; i0 < last && col < P.width; i0 += kInBatch) {
+    Pack<T, V> v[kInBatch];
+#pragma unroll
+    for (int u = 0; u < kInBatch; ++u) {
+      if (i0 + u >= last) break;
+      const T* row = grad + list[i0 + u] * P.grad_stride;
+      if constexpr (kAligned) {
+        v[u] = load_vec<T, true>(row + col);
+      } else if (col >= V && col + 2 * V <= P.width) {
+        v[u] = load_vec<T, false>(row + col);  // the aligned vectors around it lie in the row
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[u].v[i] = col + i < P.width ? row[col + i] : from_f32<T>(0.f);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kInBatch; ++u) {
+      if (i0 + u >= last) break;
+      float f[V];
+      to_floats<T>(v[u], f);
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum[i] += f[i];
+    }
+  }
+  if (count > 1 && groups > 1) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) few_sums[(group * V + i) * size + t] = sum[i];
+    __syncthreads();
+    if (group == 0)
+      for (int g = 1; g < groups; ++g)
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[i] += few_sums[(g * V + i) * size + t];
+  }
+  if (group == 0 && col < P.width) store_sums<O, V, kAligned>(P, run, col, sum);
 }
 
 // Zeros: rows of `bytes` bytes, `pitch` apart, the last of `last` bytes; `unit` bytes divide
@@ -571,8 +689,8 @@ struct Layout {
 };
 Layout layout_of(int64_t tokens, int64_t width) {
   const auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
-  Layout l;
-  l.items[0] = 0;
+  Layout l = {};
+  if (tokens <= kFewTokens) return l;
   l.items[1] = up(tokens * 8);
   l.totals = l.items[1] + up(tokens * 8);
   l.sums = l.totals + (tokens > kOneLaunch ? up(int64_t(kGridCtas) * 4 << kDigitBits) : 0);
@@ -651,7 +769,28 @@ tbe_status sort_in_grid(const IdT* ids, const SortPlan& plan, int* totals, int* 
   return st;
 }
 
-// Zeros in a matrix; with `beside` the launch may begin before the kernel ahead of it ends.
+// A launch; with `beside` it may begin before the kernel ahead of it ends, and waits for that one's
+// results itself.
+template <typename... Args>
+tbe_status launch(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, bool beside,
+                  cudaStream_t s, std::common_type_t<Args>... args) {
+  if (room_for(reinterpret_cast<const void*>(kernel), smem) != cudaSuccess) return TBE_ECUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = beside ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return TBE_ECUDA;
+  note_launch();
+  return TBE_OK;
+}
+
+// Zeros in a matrix.
 tbe_status clear(void* p, int64_t rows, int64_t width, int64_t stride, int bytes, bool beside,
                  cudaStream_t s) {
   int64_t row = width * bytes, pitch = stride * bytes, last = row;
@@ -661,19 +800,8 @@ tbe_status clear(void* p, int64_t rows, int64_t width, int64_t stride, int bytes
     rows = (all + row - 1) / row;
     last = all - (rows - 1) * row;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(rows, 152 * 8)));
-  cfg.blockDim = dim3(kMoveThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = beside ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, clear_kernel, static_cast<char*>(p), rows, row, pitch, last,
-                         bytes) != cudaSuccess)
-    return TBE_ECUDA;
-  return launched();
+  return launch(clear_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(rows, 152 * 8))),
+                kMoveThreads, 0, beside, s, static_cast<char*>(p), rows, row, pitch, last, bytes);
 }
 
 }  // namespace
@@ -754,16 +882,51 @@ extern "C" tbe_status tbe_embed_backward(const void* grad_out, int32_t dtype, in
       !check_ids(ids, index_dtype, tokens))
     return TBE_EINVAL;
   const Layout l = layout_of(tokens, width);
-  if (tokens && (!workspace || ws_bytes < static_cast<size_t>(l.bytes) || !aligned_to(workspace, 16)))
+  if (l.bytes && (!workspace || ws_bytes < static_cast<size_t>(l.bytes) || !aligned_to(workspace, 16)))
     return TBE_EWORKSPACE;
   const Bytes id_run = run_of(ids, tokens * (index_dtype == TBE_DT_I32 ? 4 : 8));
-  const Bytes ws = run_of(tokens ? workspace : nullptr, l.bytes);
+  const Bytes ws = run_of(l.bytes ? workspace : nullptr, l.bytes);
   const Bytes read = in.span(tokens, width), written = to.span(rows, width);
   if (overlap(written, read) || overlap(written, id_run) || overlap(written, ws) ||
       overlap(ws, read) || overlap(ws, id_run))
     return TBE_EINVAL;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (!tokens) return clear(grad_table, rows, width, grad_table_stride, ob, false, s);
+  const bool vec = in.vectors(width, 16) && to.vectors(width, 16);
+  const auto for_types = [&](auto f) {  // f(row type, result's type, aligned)
+    return for_dtype(dtype, [&](auto t) {
+      const auto with = [&](auto o) {
+        return vec ? f(t, o, std::true_type{}) : f(t, o, std::false_type{});
+      };
+      return out_dtype == dtype ? with(t) : with(float{});
+    });
+  };
+  if (tokens <= kFewTokens) {
+    return for_types([&](auto t, auto o, auto aligned) {
+      using T = decltype(t);
+      using O = decltype(o);
+      constexpr bool kAligned = decltype(aligned)::value;
+      const int64_t places = (width + kVec<T> - 1) / kVec<T>;
+      const int lg = std::min(log2_up(places), 8), size = 1 << lg;
+      const auto go = [&](auto* p) {
+        using IdT = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
+        FewArgs<IdT> few = {{grad_out, nullptr, grad_table, nullptr, grad_out_stride,
+                             grad_table_stride, static_cast<int>(tokens), static_cast<int>(rows),
+                             static_cast<int>(width), 0, 0, scale, accumulate != 0},
+                            p, 0};
+        // about 64 KB a clearing CTA
+        const int64_t slices = (places + size - 1) / size;
+        few.range = static_cast<int>(std::clamp<int64_t>(65536 / (width * ob), 1, kFewRows));
+        const int64_t ranges = accumulate ? 0 : (rows + few.range - 1) / few.range;
+        const dim3 grid(static_cast<unsigned>(tokens + (ranges + slices - 1) / slices),
+                        static_cast<unsigned>(slices));
+        return launch(embed_few_kernel<T, O, IdT, kAligned>, grid, kMoveThreads,
+                      kMoveThreads * kVec<T> * sizeof(float), false, s, few, lg);
+      };
+      return index_dtype == TBE_DT_I32 ? go(static_cast<const int32_t*>(ids))
+                                       : go(static_cast<const int64_t*>(ids));
+    });
+  }
   char* w = static_cast<char*>(workspace);
   SortPlan plan = plan_of(tokens, rows);
   plan.items[0] = reinterpret_cast<Item*>(w + l.items[0]);
@@ -786,33 +949,22 @@ extern "C" tbe_status tbe_embed_backward(const void* grad_out, int32_t dtype, in
                         static_cast<int>(tokens), static_cast<int>(rows), static_cast<int>(width),
                         static_cast<int>((width + 7) / 8 * 8), static_cast<int>(piece), scale,
                         accumulate != 0};
-  return for_dtype(dtype, [&](auto t) {
+  return for_types([&](auto t, auto o, auto aligned) {
     using T = decltype(t);
-    const auto go = [&](auto aligned, auto o) {
-      constexpr bool kAligned = decltype(aligned)::value;
-      using O = decltype(o);
-      const int64_t places = (width + kVec<T> - 1) / kVec<T>;
-      const int lg = std::min(log2_up(places), 8);
-      const int per = kMoveThreads >> lg;
-      const dim3 grid(static_cast<unsigned>((pieces + per - 1) / per),
-                      static_cast<unsigned>((places + (1 << lg) - 1) >> lg));
-      const auto kernel = embed_sum_kernel<T, O, kAligned>;
-      const size_t smem = RowsAhead<T, kAligned>::kBytes * kMoveThreads +
-                          ((per + 2) * piece + 2) * sizeof(Item);
-      if (room_for(reinterpret_cast<const void*>(kernel), smem) != cudaSuccess) return TBE_ECUDA;
-      kernel<<<grid, kMoveThreads, smem, s>>>(args, lg);
-      if (pieces < 3) return launched();  // no run is long
-      note_launch();
-      embed_join_kernel<O><<<dim3(static_cast<unsigned>((pieces + kJoinPieces - 1) / kJoinPieces),
-                                  static_cast<unsigned>((width + 4 * kJoinLanes - 1) /
-                                                        (4 * kJoinLanes))),
-                             kJoinLanes * kJoinSegments, 0, s>>>(args);
-      return launched();
-    };
-    const auto to_type = [&](auto aligned) {
-      return out_dtype == dtype ? go(aligned, T{}) : go(aligned, float{});
-    };
-    const bool vec = in.vectors(width, 16) && to.vectors(width, 16);
-    return vec ? to_type(std::true_type{}) : to_type(std::false_type{});
+    using O = decltype(o);
+    constexpr bool kAligned = decltype(aligned)::value;
+    const int64_t places = (width + kVec<T> - 1) / kVec<T>;
+    const int lg = std::min(log2_up(places), 8);
+    const int per = kMoveThreads >> lg;
+    const dim3 grid(static_cast<unsigned>((pieces + per - 1) / per),
+                    static_cast<unsigned>((places + (1 << lg) - 1) >> lg));
+    const size_t smem = RowsAhead<T, kAligned>::kBytes * kMoveThreads +
+                        ((per + 2) * piece + 2) * sizeof(Item);
+    const tbe_status summed = launch(embed_sum_kernel<T, O, kAligned>, grid, kMoveThreads, smem,
+                                     true, s, args, lg);
+    if (summed != TBE_OK || pieces < 3) return summed;  // no run is long
+    const dim3 joins(static_cast<unsigned>((pieces + kJoinPieces - 1) / kJoinPieces),
+                     static_cast<unsigned>((width + 4 * kJoinLanes - 1) / (4 * kJoinLanes)));
+    return launch(embed_join_kernel<O>, joins, kJoinLanes * kJoinSegments, 0, true, s, args);
   });
 }

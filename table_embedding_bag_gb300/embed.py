@@ -99,5 +99,6 @@ def tbe_embed_backward(grad_out, ids, rows, scale=1.0, out=None, out_dtype=None,
     _ok("tbe_embed_backward", lib.tbe_embed_backward(
         grad_out.data_ptr(), _ROW_DT[grad_out.dtype], n, width, gs, ids.data_ptr(),
         _ID_DT[ids.dtype], rows, float(scale), bool(accumulate), out.data_ptr(),
-        _ROW_DT[out.dtype], os_, ws.data_ptr(), ws.numel(), _stream_of(stream, device)))
+        _ROW_DT[out.dtype], os_, None if ws is None else ws.data_ptr(),
+        0 if ws is None else ws.numel(), _stream_of(stream, device)))
     return out

@@ -174,7 +174,8 @@ _sizes = {}  # bytes that a size function gave, by its arguments
 
 
 def _workspace(lib, call, sizes, ws, stream, like):
-    """The scratch of a call whose size function is `call`: ws, checked, or a new one."""
+    """The scratch of a call whose size function is `call`: ws, checked, or a new one (None where
+    the call needs none)."""
     need = _sizes.get((call, sizes))
     if need is None:
         n = ctypes.c_size_t(0)
@@ -183,7 +184,7 @@ def _workspace(lib, call, sizes, ws, stream, like):
             _sizes.clear()
         need = _sizes[call, sizes] = n.value
     if ws is None:
-        return _empty(stream, max(need, 1), torch.uint8, like)
+        return _empty(stream, need, torch.uint8, like) if need else None
     if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.numel() < need:
         raise ValueError(f"ws must be a contiguous uint8 tensor of at least {need} entries")
     if ws.get_device() != like.get_device():
