@@ -279,9 +279,9 @@ __global__ void __launch_bounds__(kSortWarps * 32)
 // the next rows to a ring in shared memory (cp.async) while it adds the row at hand.
 constexpr int kLeastPiece = 8, kMostPiece = 64;
 constexpr int kSumGroups = 152 * 8;  // groups that fill the GPU
-constexpr int kJoinPieces = 8;       // pieces whose ends a CTA looks at
+constexpr int kJoinPieces = 32;       // pieces whose ends a CTA looks at
 constexpr int kJoinSegments = 8;
-constexpr int kJoinLanes = 32;       // vectors of four columns of a CTA
+constexpr int kJoinLanes = 32;        // vectors of four columns of a CTA
 
 struct SumArgs {
   const void* grad_out;
@@ -484,8 +484,7 @@ __global__ void __launch_bounds__(kJoinLanes * kJoinSegments)
   const bool found = run_here < P.rows && row_at(end - 1) == run_here &&
                      (end == P.piece || row_at(end - P.piece - 1) != run_here) &&
                      is_long(P, end, run_here, row_at);
-  // The items were there when the sums began; the sums' parts and rows are now.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  bool waited = false;
   for (unsigned todo = __ballot_sync(kAll, found); todo; todo &= todo - 1) {
     const int64_t piece = piece0 + __ffs(todo) - 1;
     const int run = __shfl_sync(kAll, run_here, __ffs(todo) - 1);
@@ -494,6 +493,9 @@ __global__ void __launch_bounds__(kJoinLanes * kJoinSegments)
       all = __ballot_sync(kAll, row_at((piece + 1 + more + lane) * P.piece) == run);
       more += __popc(all);
     }
+    // The items were there when the sums began; the sums' parts and rows are from here on.
+    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+    waited = true;
     const auto part = [&](int64_t p, int slot) {
       return *reinterpret_cast<const float4*>(P.parts + (p * 2 + slot) * P.part_width + col);
     };
@@ -514,6 +516,7 @@ __global__ void __launch_bounds__(kJoinLanes * kJoinSegments)
       store_sums<O, 4, false>(P, run, col, v);
     }
   }
+  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // the call ends after its sums
 }
 
 // -------------------------------------------------------- gradient, few tokens
