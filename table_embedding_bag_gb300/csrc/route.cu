@@ -179,6 +179,8 @@ template <int L>
 __device__ __noinline__ int order_exactly(int mine, float l, float b, int* room) {
   const int lane = threadIdx.x & 31, first = lane & ~(L - 1);
   const double c = mine >= 0 ? 1.0 / (1.0 + exp(-static_cast<double>(l))) + b : kClosed;
+  room[lane] = -1;  // should ranks collide, which NaN alone could do, no entry is left unset
+  __syncwarp();
   int rank = 0;
   for (int j = 0; j < L; ++j) {
     const double other = __shfl_sync(kAll, c, first + j);
@@ -398,18 +400,19 @@ __global__ void __launch_bounds__(256) route_kernel(const __grid_constant__ Rout
         c[v] = c[v] == kClosed ? kClosed : score_of(c[v], false, scale.top, inverse) + b[v];
     }
   }
-  bool odd = scale.sum != scale.sum && scale.top != kClosed;  // NaN
+  // NaN, or infinities of both signs
+  float all = c[0];
 #pragma unroll
-  for (int v = 0; v < V; ++v) odd |= c[v] != c[v];
-  odd = odd && (count > 0);
+  for (int v = 1; v < V; ++v) all += c[v];
+  const bool odd = (scale.sum != scale.sum && scale.top != kClosed) || (all != all && count > 0);
 
   // Two choices closer than this may be the other way round in exact arithmetic.  In units of
-  // 2^-24 of the row's largest possible score, a score is off by at most 7 with sigmoid
-  // (the exponential's 4 + 1.6 |l| times s (1 - s), the sum's 1 and the reciprocal's 2)
-  // and by 35 with softmax (the exponentials of logit and sum at x below the top, where
-  // exp(x) |x| <= 0.37 and the mean of |x| over the row is at most log 1024, the sum's ten
-  // additions, reciprocal and product); its sum with the bias by half a unit of its own.
-  const float step = P.sigmoid ? 0x1p-20f : 0x1p-17f * inverse;
+  // 2^-24 of the row's largest possible score, a score is off by at most 4.2 with sigmoid
+  // (the exponential's 4 + 1.6 |l| times s (1 - s), 1.1 at most, the sum's 1 and the
+  // reciprocal's 2) and by 35 with softmax (the exponentials of logit and sum at x below the
+  // top, where exp(x) |x| <= 0.37 and the mean of |x| over the row is at most log 1024, the
+  // sum's ten additions, reciprocal and product); its sum with the bias by one unit of itself.
+  const float step = P.sigmoid ? 0x1.1p-21f : 0x1p-17f * inverse;
   bool unsure = row_any<L>(odd), near = false;
 
   if (P.groups > 1) {
@@ -424,11 +427,14 @@ __global__ void __launch_bounds__(256) route_kernel(const __grid_constant__ Rout
       second = fmaxf(fmaxf(second, s), fminf(first, f));
       first = fmaxf(first, f);
     }
-    float worth = first;
+    float worth = first, size_of = first == kClosed ? 0.f : fabsf(first);  // of what it sums
     if (P.group_best > 1 && first != kClosed) {
-      if (P.by_logits) worth = score_of(first, P.sigmoid, scale.top, inverse);
-      if (second != kClosed)
-        worth += P.by_logits ? score_of(second, P.sigmoid, scale.top, inverse) : second;
+      if (P.by_logits) {
+        first = score_of(first, P.sigmoid, scale.top, inverse);
+        if (second != kClosed) second = score_of(second, P.sigmoid, scale.top, inverse);
+      }
+      worth = second != kClosed ? first + second : first;
+      size_of = second != kClosed ? fabsf(first) + fabsf(second) : fabsf(first);
     }
     int rank = 0;
 #pragma unroll 2
@@ -442,8 +448,9 @@ __global__ void __launch_bounds__(256) route_kernel(const __grid_constant__ Rout
       const bool left = worth != kClosed && !open;
       const float last = -row_max<L>(open ? -worth : kClosed);
       const float next = row_max<L>(left ? worth : kClosed);
-      unsure |= next != kClosed &&
-                !(last - next > 2.f * step + 0x1p-21f * fmaxf(fabsf(last), fabsf(next)));
+      const float largest = row_max<L>(size_of);
+      // two sums of two choices, each rounded, and rounded themselves
+      unsure |= next != kClosed && !(last - next > 2.f * step + 0x1p-22f * largest);
     }
     if (!open) {
 #pragma unroll
@@ -468,7 +475,7 @@ __global__ void __launch_bounds__(256) route_kernel(const __grid_constant__ Rout
     const float lp = __shfl_up_sync(kAll, chosen, 1), bp = __shfl_up_sync(kAll, b, 1);
     const float sp = __shfl_up_sync(kAll, s, 1);
     const auto far = [&](float more, float less) {
-      return more - less > step + 0x1p-22f * fmaxf(fabsf(less), fabsf(more));
+      return more - less > step + 0x1p-23f * fmaxf(fabsf(less), fabsf(more));
     };
     near = row_any<L>(place > 0 && place < K && mine >= 0 && !far(sp, s) &&
                       !(lp == chosen && bp == b)) && !unsure;

@@ -170,6 +170,10 @@ def test_choices_that_fp32_does_not_tell_apart():
     check(logits, 8, score="sigmoid", bias=bias, groups=8, top_groups=3, group_best=2)
     big = torch.full((40,), 4096.0, device="cuda")  # swallows the score's last bits in fp32
     check(randn(g, 500, 40), 8, score="sigmoid", bias=big)
+    # choices of both signs, large beside the groups' worth
+    mixed = torch.where(torch.arange(40, device="cuda") % 2 == 0, 300.0, -299.5)
+    check(randn(g, 2000, 40), 6, score="sigmoid", bias=mixed + 1e-5 * randn(g, 40), groups=10,
+          top_groups=3, group_best=2)
     assert s.shape == (2000, 40)
 
 
