@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kSortWarps * 32)
 // What bounds it is how many rows' loads are on their way, so each thread copies its own columns of
 // the next rows to a ring in shared memory (cp.async) while it adds the row at hand.
 constexpr int kLeastPiece = 8, kMostPiece = 64;
-constexpr int kSumGroups = 152 * 8;  // groups that fill the GPU
+constexpr int64_t kSumThreads = 152 * 2048;  // threads that fill the GPU
 constexpr int kJoinPieces = 32;       // pieces whose ends a CTA looks at
 constexpr int kJoinSegments = 8;
 constexpr int kJoinLanes = 32;        // vectors of four columns of a CTA
@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kJoinLanes * kJoinSegments)
 // the one with a row's first token lists the row's tokens in their order and sums them; a
 // CTA's groups of threads take equal parts of a long list, added in their order.  The other
 // CTAs clear the rows of their range that have no token.
-constexpr int kFewTokens = 512;
+constexpr int kFewTokens = 1024;
 constexpr int kFewRows = 32768;  // of a clearing CTA, at most: a bit each in its shared memory
 
 template <typename IdT>
@@ -538,7 +538,7 @@ struct FewArgs {
 template <typename T, typename O, typename IdT, bool kAligned>
 __global__ void __launch_bounds__(kMoveThreads)
     embed_few_kernel(const __grid_constant__ FewArgs<IdT> A, int log_group) {
-  constexpr int V = kVec<T>, kInBatch = 8;
+  constexpr int V = kVec<T>, kInBatch = 16;
   const SumArgs& P = A.sum;
   __shared__ int list[kFewTokens];
   __shared__ unsigned found[kFewTokens / 32];
@@ -680,9 +680,9 @@ SortPlan plan_of(int64_t tokens, int64_t rows) {
 // Places of a piece: few while that leaves the GPU idle, more as the tokens are more, since a
 // long run has a part in each.
 int64_t piece_of(int64_t tokens, int64_t width) {
-  const int64_t groups = (width + 2047) / 2048;  // of a piece, at most
+  const int64_t threads = std::min<int64_t>((width + 7) / 8, 256);  // of a piece, about
   int64_t piece = kLeastPiece;
-  while (piece < kMostPiece && tokens * groups > 2 * piece * kSumGroups) piece *= 2;
+  while (piece < kMostPiece && tokens * threads >= 2 * piece * kSumThreads) piece *= 2;
   return piece;
 }
 

@@ -406,13 +406,14 @@ __global__ void __launch_bounds__(256) route_kernel(const __grid_constant__ Rout
   for (int v = 1; v < V; ++v) all += c[v];
   const bool odd = (scale.sum != scale.sum && scale.top != kClosed) || (all != all && count > 0);
 
-  // Two choices closer than this may be the other way round in exact arithmetic.  In units of
-  // 2^-24 of the row's largest possible score, a score is off by at most 4.2 with sigmoid
-  // (the exponential's 4 + 1.6 |l| times s (1 - s), 1.1 at most, the sum's 1 and the
-  // reciprocal's 2) and by 35 with softmax (the exponentials of logit and sum at x below the
-  // top, where exp(x) |x| <= 0.37 and the mean of |x| over the row is at most log 1024, the
-  // sum's ten additions, reciprocal and product); its sum with the bias by one unit of itself.
-  const float step = P.sigmoid ? 0x1.1p-21f : 0x1p-17f * inverse;
+  // Two choices closer than their errors may be the other way round in exact arithmetic.  In units
+  // of 2^-24, a sigmoid score is off by at most 4.2 (the exponential's 4 + 1.6 |l| times
+  // s (1 - s), 1.1 at most, the sum's 1 and the reciprocal's 2), a softmax score x below the
+  // row's top by 34 + 2 |x| times itself (exponential 4 + 2 |x|, the sum's terms 4 + 2 mean |x|,
+  // where that mean is at most log 1024, its ten additions, reciprocal and product), and so by
+  // 35 times the row's largest; its sum with the bias by one unit of itself.  step: twice the
+  // bound that holds for every expert.
+  const float step = P.sigmoid ? 0x1.1p-21f : 0x1.2p-18f * inverse;
   bool unsure = row_any<L>(odd), near = false;
 
   if (P.groups > 1) {
@@ -471,20 +472,22 @@ __global__ void __launch_bounds__(256) route_kernel(const __grid_constant__ Rout
     // neighbours in the order that fp32 does not tell apart; the same logit and bias tie
     // in any arithmetic
     const float b = mine >= 0 ? P.bias[mine] : 0.f;
-    const float s = mine >= 0 ? score_of(chosen, P.sigmoid, scale.top, inverse) + b : kClosed;
+    const float score = mine >= 0 ? score_of(chosen, P.sigmoid, scale.top, inverse) : 0.f;
+    const float s = mine >= 0 ? score + b : kClosed;
+    const float off = P.sigmoid ? 0x1.1p-22f : score * (34.f + 2.f * (scale.top - chosen)) * 0x1p-24f;
     const float lp = __shfl_up_sync(kAll, chosen, 1), bp = __shfl_up_sync(kAll, b, 1);
-    const float sp = __shfl_up_sync(kAll, s, 1);
-    const auto far = [&](float more, float less) {
-      return more - less > step + 0x1p-23f * fmaxf(fabsf(less), fabsf(more));
+    const float sp = __shfl_up_sync(kAll, s, 1), op = __shfl_up_sync(kAll, off, 1);
+    const auto far = [&](float more, float less, float by) {
+      return more - less > by + 0x1p-23f * fmaxf(fabsf(less), fabsf(more));
     };
-    near = row_any<L>(place > 0 && place < K && mine >= 0 && !far(sp, s) &&
+    near = row_any<L>(place > 0 && place < K && mine >= 0 && !far(sp, s, off + op) &&
                       !(lp == chosen && bp == b)) && !unsure;
     if (__any_sync(kAll, near)) {
       // the candidates suffice where the last that is taken is above all others for certain
       const int edge = (lane & ~(L - 1)) + P.k - 1;
       const float last = __shfl_sync(kAll, s, edge);
       const float next = in_rounds ? __shfl_sync(kAll, s, edge + 1 < 32 ? edge + 1 : 31) : bound;
-      const bool enough = P.sigmoid && (next == kClosed || far(last, next));
+      const bool enough = P.sigmoid && (next == kClosed || far(last, next, step));
       const int sorted = order_exactly<L>(mine, chosen, b, reinterpret_cast<int*>(room));
       if (near && enough) {
         mine = sorted;

@@ -49,7 +49,7 @@ def test_binding_constants_match_the_headers():
 
 EMBED = dict(table=A, dt=F16, rows=100, width=32, ts=32, ids=B, it=I32, tokens=8, scale=1.0, out=C,
              os=32)
-BACK = dict(grad=A, dt=BF16, tokens=640, width=32, gs=32, ids=B, it=I64, rows=100, scale=1.0, acc=0,
+BACK = dict(grad=A, dt=BF16, tokens=2000, width=32, gs=32, ids=B, it=I64, rows=100, scale=1.0, acc=0,
             out=C, ot=BF16, os=32, ws=W, n=BIG)
 NORM = dict(x=A, res=B, w=C, dt=F16, wt=F32, rows=8, width=256, xs=256, rs=256, eps=1e-6, h=D,
             hs=256, y=E, ys=256)
@@ -144,9 +144,9 @@ def test_empty_problems_launch_nothing(lib):
 def test_workspace_sizes(lib):
     assert tbe.tbe_embed_workspace_size(0, 10, 16) == 0
     assert tbe.tbe_embed_workspace_size(100, 1000, 4096) == 0
-    for n in (1000, 131072, 131073, 1 << 24, (1 << 31) - 2000):
+    for n in (2000, 131072, 131073, 1 << 24, (1 << 31) - 2000):
         # the sorted tokens twice, and two parts for each piece of 8 to 64 of them
-        pieces = min(n // 8 + 1, max(2432, n // 64 + 1))
+        pieces = min(n // 8 + 1, max(4864, n // 64 + 1))
         got = tbe.tbe_embed_workspace_size(n, 1000, 4096)
         assert 16 * n < got <= 16 * n + 4096 + (5 << 20) + pieces * 2 * 4096 * 4
     assert tbe.tbe_rms_norm_workspace_size(0, 128) == 0
