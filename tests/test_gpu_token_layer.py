@@ -5,6 +5,10 @@ Tolerance: the 8-bit rows are off by 2^-4 of a value, the weights likewise; each
 over a row's columns averages those errors, so results are compared by their 2-norm: within
 2^-3 of it (both errors at once, four times over).  What does not go through 8 bits is held to
 its own type."""
+import importlib.util
+import math
+import os
+
 import pytest
 import torch
 
@@ -68,3 +72,48 @@ def test_embed_norm_route_experts_and_back():
     assert near(dense, (y64 @ w.double()[0].T).detach())
     (out64 * grad_out.double()).sum().backward()
     assert near(g_table, t64.grad) and near(g_weight, w64.grad)
+
+
+@pytest.fixture(scope="module")
+def example():
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "token_layer.py")
+    spec = importlib.util.spec_from_file_location("token_layer_example", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+def test_the_example_runs(example):
+    losses, norms = example.train(steps=3, tokens=700, rows=300, width=256)
+    assert len(losses) == 3 and all(math.isfinite(v) for v in losses + norms)
+    assert all(v > 0 for v in losses + norms)
+
+
+def test_the_examples_gradients(example):
+    # against automatic differentiation in 64 bits with the choice that was made
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    layer = example.TokenLayer(200, 256, 8, 2, g)
+    ids = torch.randint(-1, 200, (500,), generator=g, device="cuda")
+    position = torch.randn(500, 256, generator=g, device="cuda").bfloat16()
+    grad_out = torch.randn(500, 256, generator=g, device="cuda")
+    out = layer.forward(ids, position)
+    grads = layer.backward(grad_out)
+    w8, scale = layer.experts
+    blocks = scale.double().repeat_interleave(128, 1).repeat_interleave(128, 2)
+    w = w8.double() * blocks[:, :256, :256]
+    table, weight, router = (p.double().requires_grad_() for p in
+                             (layer.table, layer.weight, layer.router))
+    x = torch.where((ids >= 0)[:, None], table[ids.clamp_min(0)] * layer.scale, 0.0)
+    h = x + position.double()
+    y = h / torch.sqrt(h.square().mean(1, keepdim=True) + 1e-6) * weight
+    s = torch.sigmoid(y @ router.T).gather(1, layer.chosen.long())
+    cw = s / s.sum(1, keepdim=True)
+    answers = torch.einsum("nkij,nj->nki", w[layer.chosen.long()], y)
+    want = h + (answers * cw[..., None]).sum(1)
+    near = lambda a, b: float((a.double() - b).norm()) <= 2.0 ** -3 * float(b.norm())
+    assert near(out, want.detach())
+    (want * grad_out.double()).sum().backward()
+    for got, p in zip(grads, (table, weight, router)):
+        assert near(got, p.grad)
