@@ -12,6 +12,7 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kMostGroups = 32;  // a lane each
+constexpr int kGroupRounds = 6;
 
 struct RouteArgs {
   const void* logits;
@@ -23,9 +24,9 @@ struct RouteArgs {
   float scale;
   bool sigmoid, renormalize, wide_ids;
   bool by_logits;  // no bias: the choices' order is that of the logits, which are compared
-  // how a row's lanes share its experts: `group_lanes` consecutive lanes a group (a power of
-  // two), `lane_experts` consecutive experts of it a lane
-  int group_lanes, lane_experts;
+  // how a row's lanes share its experts: `group_lanes` = 2^log_lanes consecutive lanes a group of
+  // `size` experts, `lane_experts` consecutive ones of them a lane
+  int size, group_lanes, log_lanes, lane_experts;
   bool vectors;  // lane_experts is the kernel's V, and all of a lane's experts exist and are aligned
 };
 
@@ -96,7 +97,7 @@ __device__ __forceinline__ float score_of(float l, bool sigmoid, float top, floa
 template <typename T>
 __device__ __noinline__ int choose_exactly(const RouteArgs& P, const T* logits,
                                            unsigned long long* room) {
-  const int lane = threadIdx.x & 31, size = P.experts / P.groups;
+  const int lane = threadIdx.x & 31, size = P.size;
   double top = 0.0, sum = 1.0;
   if (!P.sigmoid) {
     float m = kClosed;
@@ -197,24 +198,27 @@ __device__ __noinline__ int order_exactly(int mine, float l, float b, int* room)
 }
 
 // Weights of the chosen, before the scale: lane j of a row has the j-th expert's logit, `on`
-// where there is one.
-template <int L>
+// where there is one.  kNear: by the approximate functions, off by 4 + 1.6 |x| units of 2^-24.
+template <int L, bool kNear>
 __device__ __forceinline__ float weight_of(float l, bool on, bool sigmoid, bool renormalize,
                                            RowScale r) {
+  const auto power = [](float x) { return kNear ? exp_near(x) : expf(x); };
+  const auto ratio = [](float p, float q) { return kNear ? __fdividef(p, q) : __fdiv_rn(p, q); };
+  const auto logistic = [&](float x) {
+    return kNear ? reciprocal_near(1.f + exp_near(-x)) : __fdiv_rn(1.f, 1.f + expf(-x));
+  };
   if (!renormalize) {
     if (!on) return 0.f;
-    return sigmoid ? __fdiv_rn(1.f, 1.f + expf(-l)) : __fdiv_rn(expf(l - r.top), r.sum);
+    return sigmoid ? logistic(l) : ratio(power(l - r.top), r.sum);
   }
   const float top = row_max<L>(on ? l : kClosed);
   // sigmoid(l) is exp(l) to the last bit where no logit is above -60, and exp(l - top) does not
   // underflow
-  const float p = !on                        ? 0.f
-                  : sigmoid && !(top < -60.f) ? __fdiv_rn(1.f, 1.f + expf(-l))
-                                              : expf(l - top);
+  const float p = !on ? 0.f : sigmoid && !(top < -60.f) ? logistic(l) : power(l - top);
   const float sum = row_sum<L>(p);
   if (!on) return 0.f;
   // a NaN among the row's scores makes every softmax weight one
-  return !sigmoid && r.sum != r.sum ? r.sum : __fdiv_rn(p, sum);
+  return !sigmoid && r.sum != r.sum ? r.sum : ratio(p, sum);
 }
 
 // The K experts with the largest choices, in their order: lane j of a row gets the j-th (-1 for
@@ -305,13 +309,17 @@ __device__ __forceinline__ int choose_by_bound(float (&c)[V], int e0, int K, Can
   const float mine = room.c[lane];
   const int e = lane < all ? room.e[lane] : -1;
   int rank = 0;
-  for (int j = 0; j < all; j += 4) {  // they stand in the order of the experts
+  for (int j = 0; j < all; j += 4) {
     const float4 o = *reinterpret_cast<const float4*>(room.c + j);
-    rank += o.x > mine || (o.x == mine && j < lane);
-    rank += o.y > mine || (o.y == mine && j + 1 < lane);
-    rank += o.z > mine || (o.z == mine && j + 2 < lane);
-    rank += o.w > mine || (o.w == mine && j + 3 < lane);
+    rank += o.x > mine;
+    rank += o.y > mine;
+    rank += o.z > mine;
+    rank += o.w > mine;
   }
+  // Choices that are alike share a rank, and the ranks' sum falls short: they take the order of
+  // the experts, in which they stand.
+  if (static_cast<int>(__reduce_add_sync(kAll, lane < all ? rank : 0)) != all * (all - 1) / 2)
+    for (int j = 0; j < all; ++j) rank += room.c[j] == mine && j < lane;
   __syncwarp();
   if (lane < all) room.e[rank] = e;
   __syncwarp();
@@ -335,7 +343,7 @@ __global__ void __launch_bounds__(256) route_kernel(const __grid_constant__ Rout
   double* room = route_smem + warp * room_of(P.experts);
 
   // this lane's experts: e0 .. e0 + mine - 1, of its group
-  const int size = P.experts / P.groups, group = place / P.group_lanes;
+  const int size = P.size, group = place >> P.log_lanes;
   const int in_group = (place & (P.group_lanes - 1)) * P.lane_experts;
   const int e0 = group * size + in_group;
   int count = size - in_group < P.lane_experts ? size - in_group : P.lane_experts;
@@ -437,18 +445,33 @@ __global__ void __launch_bounds__(256) route_kernel(const __grid_constant__ Rout
       worth = second != kClosed ? first + second : first;
       size_of = second != kClosed ? fabsf(first) + fabsf(second) : fabsf(first);
     }
-    int rank = 0;
-#pragma unroll 2
-    for (int o = P.group_lanes; o < L; o += P.group_lanes) {
-      const float other = __shfl_xor_sync(kAll, worth, o);
-      rank += other > worth || (other == worth && (place ^ o) < place);
+    // The groups worth most, one a round where a round is one reduction (eight instructions,
+    // ranking takes nine for every other group); where two are worth the same, by their ranks.
+    bool open = false, ranked = L < 32 || P.top_groups > kGroupRounds;
+    float last = kClosed, next = kClosed;  // the least worth that is taken, the largest left
+    if (!ranked) {
+      float left = worth;
+      for (int r = 0; r < P.top_groups && !ranked; ++r) {
+        const float best = row_max<L>(left);
+        const bool mine = left == best && best != kClosed;
+        ranked = __popc(__ballot_sync(kAll, mine)) > P.group_lanes;
+        if (mine) left = kClosed, open = true;
+        if (best != kClosed) last = best;
+      }
+      next = row_max<L>(left);
     }
-    const bool open = worth != kClosed && rank < P.top_groups;
+    if (ranked) {
+      int rank = 0;
+#pragma unroll 2
+      for (int o = P.group_lanes; o < L; o += P.group_lanes) {
+        const float other = __shfl_xor_sync(kAll, worth, o);
+        rank += other > worth || (other == worth && (place ^ o) < place);
+      }
+      open = worth != kClosed && rank < P.top_groups;
+      last = -row_max<L>(open ? -worth : kClosed);
+      next = row_max<L>(!open ? worth : kClosed);
+    }
     if (by_score) {
-      // the least worth that is taken and the largest that is left
-      const bool left = worth != kClosed && !open;
-      const float last = -row_max<L>(open ? -worth : kClosed);
-      const float next = row_max<L>(left ? worth : kClosed);
       const float largest = row_max<L>(size_of);
       // two sums of two choices, each rounded, and rounded themselves
       unsure |= next != kClosed && !(last - next > 2.f * step + 0x1p-22f * largest);
@@ -511,7 +534,7 @@ __global__ void __launch_bounds__(256) route_kernel(const __grid_constant__ Rout
     chosen = mine >= 0 ? to_f32(logits[mine]) : 0.f;
   }
   if (place >= P.k) mine = -1;  // the one past the last
-  const float w = weight_of<L>(chosen, mine >= 0, P.sigmoid, P.renormalize, scale);
+  const float w = weight_of<L, true>(chosen, mine >= 0, P.sigmoid, P.renormalize, scale);
   if (place < P.k && live) {
     const int64_t at = token * P.k + place;
     if (P.wide_ids) static_cast<int64_t*>(P.ids)[at] = mine;
@@ -576,7 +599,7 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const __grid_consta
     for (int i = place; i < experts; i += L) sum += expf(to_f32(logits[i]) - scale.top);
     scale.sum = row_sum<L>(sum);
   }
-  const float p = weight_of<L>(l, on, P.sigmoid, P.renormalize, scale);
+  const float p = weight_of<L, false>(l, on, P.sigmoid, P.renormalize, scale);
   const float mean = P.sigmoid && !P.renormalize ? 0.f : row_sum<L>(g * p);
   if (whole)
     fill([&](int i) {  // zeros where every expert is closed
@@ -634,7 +657,9 @@ tbe_status launch_route(RouteArgs args, cudaStream_t s) {
   const int kept = args.by_logits ? args.k : args.k + 1;
   const auto each = [&] { return lanes < slots ? INT32_MAX : (size + lanes / slots - 1) / (lanes / slots); };
   while (lanes < 32 && (lanes < kept || each() > 8)) lanes *= 2;
+  args.size = size;
   args.group_lanes = lanes / slots;
+  for (args.log_lanes = 0; 1 << args.log_lanes < args.group_lanes;) ++args.log_lanes;
   args.lane_experts = each();
   const auto go = [&](auto v, auto l) {
     constexpr int V = decltype(v)::value, L = decltype(l)::value;
@@ -695,7 +720,7 @@ extern "C" tbe_status tbe_expert_route(const void* logits, int32_t dtype, int64_
   const RouteArgs args = {logits, bias, ids, weights, logits_stride, static_cast<int>(tokens),
                           experts, k, groups, top_groups, group_best, scale,
                           score == TBE_SCORE_SIGMOID, renormalize != 0, index_dtype == TBE_DT_I64,
-                          !bias, 0, 0, false};
+                          !bias, 0, 0, 0, 0, false};
   return for_dtype(dtype, [&](auto t) {
     return launch_route<decltype(t)>(args, static_cast<cudaStream_t>(stream));
   });
