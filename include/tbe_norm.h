@@ -65,8 +65,9 @@ tbe_status tbe_rms_norm_workspace_size(int64_t rows, int64_t width, size_t* byte
  *                     + grad_h[r, c])
  *   grad_weight[c] = sum_r grad_y[r, c] * h[r, c] * u[r]
  * grad_x is the gradient of x and of residual alike.  grad_h: the gradient that
- * arrives at h, NULL: none.  grad_weight fp32 [H], summed in fp32, or NULL (workspace is then not used).  h: tbe_rms_norm's, or x where
- * it had no residual.  rows = 0 gives grad_weight zeros. */
+ * arrives at h, NULL: none.  grad_weight fp32 [H], summed in fp32, or NULL (workspace is
+ * then not used).  h: tbe_rms_norm's, or x where it had no residual.  rows = 0 gives
+ * grad_weight zeros. */
 tbe_status tbe_rms_norm_backward(const void* grad_y, const void* h, const void* weight,
                                  const void* grad_h, int32_t dtype, int32_t weight_dtype,
                                  int64_t rows, int64_t width, int64_t grad_y_stride,

@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kMoveThreads)
 constexpr int kDigitBits = 10;  // of a pass, at most
 constexpr int kSortUnroll = 4;
 constexpr int kOneLaunch = 131072;
-constexpr int kTokensPerCta = 1024;   // from which another CTA of the cluster pays (4097: 12.4 us at 2048)
+constexpr int kTokensPerCta = 1024;   // from which another CTA of the cluster pays
 constexpr int kGridCtas = 304;
 constexpr int kGridChunk = 4096;      // items of a CTA of three launches, at least
 
@@ -359,7 +359,9 @@ struct RowsAhead {
                        : "memory");
     }
   }
-  static __device__ __forceinline__ void close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  static __device__ __forceinline__ void close() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
   // All but the last kDeep - 1 rows are there.
   static __device__ __forceinline__ void wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kDeep - 1) : "memory");
@@ -435,7 +437,8 @@ __global__ void __launch_bounds__(kMoveThreads)
     float* parts = P.parts + (piece * 2 + slot) * P.part_width + col;
 #pragma unroll
     for (int i = 0; i < V; i += 4)
-      *reinterpret_cast<float4*>(parts + i) = make_float4(sum[i], sum[i + 1], sum[i + 2], sum[i + 3]);
+      *reinterpret_cast<float4*>(parts + i) =
+          make_float4(sum[i], sum[i + 1], sum[i + 2], sum[i + 3]);
   };
   const auto finish = [&] {  // the run ends here
     if (open) leave(0);
@@ -885,7 +888,8 @@ extern "C" tbe_status tbe_embed_backward(const void* grad_out, int32_t dtype, in
       !check_ids(ids, index_dtype, tokens))
     return TBE_EINVAL;
   const Layout l = layout_of(tokens, width);
-  if (l.bytes && (!workspace || ws_bytes < static_cast<size_t>(l.bytes) || !aligned_to(workspace, 16)))
+  if (l.bytes && (!workspace || ws_bytes < static_cast<size_t>(l.bytes) ||
+                  !aligned_to(workspace, 16)))
     return TBE_EWORKSPACE;
   const Bytes id_run = run_of(ids, tokens * (index_dtype == TBE_DT_I32 ? 4 : 8));
   const Bytes ws = run_of(l.bytes ? workspace : nullptr, l.bytes);

@@ -179,7 +179,9 @@ struct Ahead {
                    : "memory");
     }
   }
-  static __device__ __forceinline__ void close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  static __device__ __forceinline__ void close() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
   // All but the last kDeep - 1 groups are there.
   static __device__ __forceinline__ void wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kDeep - 1) : "memory");
@@ -514,7 +516,8 @@ Shape backward_shape(int64_t rows, int64_t vectors, int most) {
 int64_t ctas_of(const Shape& s, int64_t rows, int bytes, int registers) {
   const int threads = s.threads * s.rows;
   const int regs = 65536 / ((registers + 7) / 8 * 8) / threads;
-  const int fit = std::max(1, std::min({regs, 2048 / threads, kNormShared / (bytes * threads + 1024), 32}));
+  const int fit = std::max(
+      1, std::min({regs, 2048 / threads, kNormShared / (bytes * threads + 1024), 32}));
   return std::min<int64_t>((rows + s.rows - 1) / s.rows, int64_t(152) * fit);
 }
 
@@ -529,7 +532,8 @@ tbe_status launch_norm(void (*kernel)(Args), const Args& args, const Shape& s, i
                        int bytes, void* stream) {
   const int smem = bytes * s.threads * s.rows;
   if (smem > 40 * 1024 &&  // beside what is declared in the kernels
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+          cudaSuccess)
     return TBE_ECUDA;
   kernel<<<static_cast<unsigned>(ctas), dim3(s.threads, s.rows), smem,
            static_cast<cudaStream_t>(stream)>>>(args);
@@ -589,7 +593,8 @@ tbe_status run_norm(const void* x, const void* residual, const void* weight, int
         constexpr int kBytes = kAligned ? Ahead<T, kAligned, NV, kIn>::kBytes : 0;
         const auto kernel = rms_norm_kernel<T, kFp8, kAligned, NV, kIn>;
         static const int registers = registers_of(kernel);
-        const int64_t ctas = kAligned ? ctas_of(s, rows, kBytes, registers) : (rows + s.rows - 1) / s.rows;
+        const int64_t ctas =
+            kAligned ? ctas_of(s, rows, kBytes, registers) : (rows + s.rows - 1) / s.rows;
         st = launch_norm(kernel, args, s, ctas, kBytes, stream);
       });
       return st;
@@ -597,7 +602,9 @@ tbe_status run_norm(const void* x, const void* residual, const void* weight, int
     const auto with = [&](auto in) {
       return go(std::true_type{}, in, forward_shape(rows, width / kVec<T>, kMostUnits<T>));
     };
-    if (!vec) return go(std::false_type{}, Int<2>{}, with_rows(shape_of(rows, width, 4, 32, 8), rows, 256));
+    if (!vec)
+      return go(std::false_type{}, Int<2>{},
+                with_rows(shape_of(rows, width, 4, 32, 8), rows, 256));
     return residual ? with(Int<2>{}) : with(Int<1>{});
   });
 }
@@ -700,7 +707,9 @@ extern "C" tbe_status tbe_rms_norm_backward(const void* grad_y, const void* h, c
       const auto with = [&](auto in) {
         return go(std::true_type{}, in, backward_shape(rows, width / kVec<T>, kMostUnits<T>));
       };
-      if (!vec) return go(std::false_type{}, Int<3>{}, with_rows(shape_of(rows, width, 4, 32, 4), rows, 256));
+      if (!vec)
+        return go(std::false_type{}, Int<3>{},
+                  with_rows(shape_of(rows, width, 4, 32, 4), rows, 256));
       return grad_h ? with(Int<3>{}) : with(Int<2>{});
     });
     if (st != TBE_OK) return st;

@@ -17,7 +17,8 @@ import ctypes
 import torch
 
 __all__ = [
-    "tbe_expert_route", "tbe_expert_route_backward", "tbe_expert_sort", "tbe_expert_dispatch", "tbe_expert_dispatch_fp8", "tbe_expert_combine",
+    "tbe_expert_route", "tbe_expert_route_backward",
+    "tbe_expert_sort", "tbe_expert_dispatch", "tbe_expert_dispatch_fp8", "tbe_expert_combine",
     "tbe_expert_combine_backward", "tbe_expert_dispatch_backward", "tbe_quantize_rows",
     "tbe_quantize_weights", "tbe_expert_product", "TBE_MAX_EXPERTS", "TBE_MAX_CHOSEN",
     "TBE_SCALE_BLOCK",
@@ -46,7 +47,8 @@ def configure(lib):
                                                 P, i64, P, P]
     lib.tbe_quantize_weights.argtypes = [P, i32, i64, i64, i64, P, P, P]
     lib.tbe_expert_product.argtypes = [P, i64, P, P, P, P, i64, i64, i64, i32, P, i32, i64, P, P]
-    for f in ("route", "route_backward", "sort", "dispatch", "dispatch_fp8", "combine", "combine_backward", "product"):
+    for f in ("route", "route_backward", "sort", "dispatch", "dispatch_fp8", "combine",
+              "combine_backward", "product"):
         getattr(lib, f"tbe_expert_{f}").restype = ctypes.c_int
     lib.tbe_quantize_weights.restype = ctypes.c_int
 
