@@ -480,18 +480,18 @@ struct Shape {
   int threads, units, rows;  // of a row, of a thread, of a CTA
 };
 
-// How a row of `units` vectors or elements is shared: `wanted` of them a thread where that
-// leaves at least a warp and at most kNormThreads, `least` to `most` in the end; and rows
-// of a CTA, up to `cta` threads and while there are several CTAs a multiprocessor.
-Shape shape_of(int64_t rows, int64_t units, int least, int most, int wanted) {
-  int threads = 32;
-  while (threads < kNormThreads && threads * wanted < units) threads *= 2;
+// How a row of `units` vectors or elements is shared: about `wanted` of them a thread, in whole
+// warps up to kNormThreads, `least` to `most` in the end; and rows of a CTA, up to `cta` threads
+// and while there are several CTAs a multiprocessor.
+Shape shape_of(int64_t units, int least, int most, int wanted) {
+  const int64_t warps = (units + 32 * wanted - 1) / (32 * wanted);
+  const int threads = static_cast<int>(std::min<int64_t>(warps * 32, kNormThreads));
   int per = least;
   while (per * threads < units && per < most) per *= 2;
   return {threads, per, 1};
 }
 Shape with_rows(Shape s, int64_t rows, int cta) {
-  while (s.rows * s.threads < cta && s.rows * 152 * 4 < rows) s.rows *= 2;
+  while (2 * s.rows * s.threads <= cta && s.rows * 152 * 4 < rows) s.rows *= 2;
   return s;
 }
 
@@ -500,14 +500,14 @@ Shape with_rows(Shape s, int64_t rows, int cta) {
 // Rows of one warp share a CTA of 256 threads; the others' barriers would tie rows to one another
 // (153 us with a row a CTA, 160 with four).
 Shape forward_shape(int64_t rows, int64_t vectors, int most) {
-  const Shape s = shape_of(rows, vectors, 1, most, rows < 152 * 4 ? 1 : 4);
+  const Shape s = shape_of(vectors, 1, most, rows < 152 * 4 ? 1 : 4);
   return with_rows(s, rows, s.threads == 32 ? 256 : s.threads);
 }
 // Backward: two vectors a thread (65536 x 2048 bf16: one 199 us, two 161, four 222), in CTAs of
 // 256 threads for wide rows (128 threads: 172 us), of 64 or 128 for narrow ones (65536 x 1024
 // fp16: 68 us, 256 threads 73; x 256 bf16: 30 and 32).
 Shape backward_shape(int64_t rows, int64_t vectors, int most) {
-  const Shape s = shape_of(rows, vectors, 1, most, 2);
+  const Shape s = shape_of(vectors, 1, most, 2);
   return with_rows(s, rows, s.threads == 32 ? 128 : s.threads == 64 ? 64 : 256);
 }
 
@@ -604,7 +604,7 @@ tbe_status run_norm(const void* x, const void* residual, const void* weight, int
     };
     if (!vec)
       return go(std::false_type{}, Int<2>{},
-                with_rows(shape_of(rows, width, 4, 32, 8), rows, 256));
+                with_rows(shape_of(width, 4, 32, 8), rows, 256));
     return residual ? with(Int<2>{}) : with(Int<1>{});
   });
 }
@@ -709,7 +709,7 @@ extern "C" tbe_status tbe_rms_norm_backward(const void* grad_y, const void* h, c
       };
       if (!vec)
         return go(std::false_type{}, Int<3>{},
-                  with_rows(shape_of(rows, width, 4, 32, 4), rows, 256));
+                  with_rows(shape_of(width, 4, 32, 4), rows, 256));
       return grad_h ? with(Int<3>{}) : with(Int<2>{});
     });
     if (st != TBE_OK) return st;

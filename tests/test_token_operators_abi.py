@@ -144,7 +144,7 @@ def test_empty_problems_launch_nothing(lib):
 def test_workspace_sizes(lib):
     assert tbe.tbe_embed_workspace_size(0, 10, 16) == 0
     assert tbe.tbe_embed_workspace_size(100, 1000, 4096) == 0
-    for n in (2000, 131072, 131073, 1 << 24, (1 << 31) - 2000):
+    for n in (2000, 98304, 98305, 1 << 24, (1 << 31) - 2000):
         # the sorted tokens twice, and two parts for each piece of 8 to 64 of them
         pieces = min(n // 8 + 1, max(4864, n // 64 + 1))
         got = tbe.tbe_embed_workspace_size(n, 1000, 4096)
