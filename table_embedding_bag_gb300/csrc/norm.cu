@@ -156,11 +156,12 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*part)[N]) {
     for (int i = 0; i < N; ++i) v[i] += mine[w][i];
 }
 
-// Rows of each of kIn matrices on their way to this thread, kDeep of them a matrix.
+// Rows of each of kIn matrices on their way to this thread, kDeep of them a matrix.  (Two vectors a
+// thread: two rows ahead; gradients of 65536 x 2048 bf16 156 us, with three 164, four 177.)
 template <typename T, bool kAligned, int NV, int kIn>
 struct Ahead {
   using U = Units<T, kAligned>;
-  static constexpr int kDeep = NV <= 2 ? 4 : NV == 4 ? 2 : 1;
+  static constexpr int kDeep = NV == 1 ? 4 : NV <= 4 ? 2 : 1;
   static constexpr int kBytes = kDeep * kIn * NV * 16;  // of shared memory a thread
   uint4* slots;  // this thread's first; the CTA's threads lie side by side
 
@@ -321,7 +322,7 @@ struct NormGradArgs {
 
 // Each thread keeps its columns' part of grad_weight in registers, and its part of the row
 // too, unless that is so much that registers run out: then both passes over it read the ring
-// (65536 x 2048 bf16 shared by 64 threads: 285 us with the row in registers).  kIn: 3 with a
+// (65536 x 2048 bf16 shared by 64 threads: 222 us, with the row in registers 285).  kIn: 3 with a
 // gradient that arrives at h.
 template <typename T, bool kAligned, int NV, int kIn>
 __global__ void __launch_bounds__(kNormThreads)
@@ -503,12 +504,11 @@ Shape forward_shape(int64_t rows, int64_t vectors, int most) {
   const Shape s = shape_of(vectors, 1, most, rows < 152 * 4 ? 1 : 4);
   return with_rows(s, rows, s.threads == 32 ? 256 : s.threads);
 }
-// Backward: two vectors a thread (65536 x 2048 bf16: one 199 us, two 161, four 222), in CTAs of
-// 256 threads for wide rows (128 threads: 172 us), of 64 or 128 for narrow ones (65536 x 1024
-// fp16: 68 us, 256 threads 73; x 256 bf16: 30 and 32).
+// Backward: two vectors a thread (65536 x 2048 bf16: one 199 us, two 156, four 222), a CTA a row
+// (two rows 159 us, four 165), but of 128 threads for rows of one warp.
 Shape backward_shape(int64_t rows, int64_t vectors, int most) {
   const Shape s = shape_of(vectors, 1, most, 2);
-  return with_rows(s, rows, s.threads == 32 ? 128 : s.threads == 64 ? 64 : 256);
+  return with_rows(s, rows, s.threads == 32 ? 128 : s.threads);
 }
 
 // CTAs of a launch: as many as fit the GPU with `bytes` of shared memory and as many registers a
