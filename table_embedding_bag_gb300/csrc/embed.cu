@@ -347,20 +347,21 @@ struct RowsAhead {
   __device__ __forceinline__ uint4* slot(int stage, int k) const {
     return slots + (stage * kSlots + k) * kMoveThreads;
   }
-  __device__ __forceinline__ void start(int stage, const T* row, int col, int width) const {
+  // at: the thread's first column of a row, `left` columns before its end.
+  __device__ __forceinline__ void start(int stage, const T* at, int left) const {
     if constexpr (kAligned) {
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<unsigned>(
                        __cvta_generic_to_shared(slot(stage, 0)))),
-                   "l"(row + col)
+                   "l"(at)
                    : "memory");
     } else {
-      const T* from = row + col - lead<T>(row + col);
+      const int before = lead<T>(at);
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        if (from + k * V < row + width)
+        if (k * V - before < left)
           asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(static_cast<unsigned>(
                            __cvta_generic_to_shared(slot(stage, k)))),
-                       "l"(from + k * V)
+                       "l"(at - before + k * V)
                        : "memory");
     }
   }
@@ -371,13 +372,13 @@ struct RowsAhead {
   static __device__ __forceinline__ void wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kDeep - 1) : "memory");
   }
-  // The thread's columns; what lies past the row's end is not defined.
-  __device__ __forceinline__ Pack<T, V> read(int stage, const T* row, int col) const {
+  // The thread's columns, which begin `bytes` past a boundary; what lies past the row's end is not
+  // defined.
+  __device__ __forceinline__ Pack<T, V> read(int stage, int bytes) const {
     if constexpr (kAligned) {
       return *reinterpret_cast<const Pack<T, V>*>(slot(stage, 0));
     } else {
-      const uint4 o = cut_row(*slot(stage, 0), *slot(stage, 1),
-                              lead<T>(row + col) * static_cast<int>(sizeof(T)));
+      const uint4 o = cut_row(*slot(stage, 0), *slot(stage, 1), bytes);
       return *reinterpret_cast<const Pack<T, V>*>(&o);
     }
   }
@@ -401,7 +402,6 @@ __global__ void __launch_bounds__(kMoveThreads)
   for (int i = threadIdx.x; i < (groups + 2) * P.piece + 2; i += kMoveThreads)
     window[i] = base + i >= 0 && base + i < P.n ? item_at(P.items, base + i) : Item{P.rows, 0};
   __syncthreads();
-  const auto item = [&](int64_t i) { return window[i - base]; };
   const auto row_at = [&](int64_t i) { return window[i - base].row; };
 
   const int64_t piece = piece0 + (threadIdx.x >> log_group);
@@ -409,70 +409,80 @@ __global__ void __launch_bounds__(kMoveThreads)
   const int64_t first = piece * P.piece;
   if (first >= P.n || col >= P.width) return;
   const int64_t last = first + P.piece < P.n ? first + P.piece : P.n;
-  int run = row_at(first);
-  if (run >= P.rows) return;
-  int skip = -1;      // a row that the piece before sums
-  bool open = false;  // the run has a part before this one
-  if (first > 0 && row_at(first - 1) == run) {
-    open = is_long(P, first, run, row_at);
-    if (!open) skip = run;
+  const Item *at = window + (first - base), *end = window + (last - base);
+  if (at->row >= P.rows) return;
+  bool open = false;  // the first run has a part before this one
+  if (first > 0 && row_at(first - 1) == at->row) {
+    open = is_long(P, first, at->row, row_at);
+    if (!open)  // the piece before sums it
+      for (const int skip = at->row; at < end && at->row == skip;) ++at;
   }
-  const int tail = row_at(last - 1);
+  const int tail = end[-1].row;
   bool leaves = false;  // the last run's part goes on in the next piece
-  int64_t end = last;
-  if (last < P.n && tail < P.rows && row_at(last) == tail) {
+  if (last < P.n && tail < P.rows && end->row == tail) {
     leaves = is_long(P, last, tail, row_at);
-    while (!leaves && end < P.n && row_at(end) == tail) ++end;  // at most a piece on
+    if (!leaves)  // at most a piece on
+      for (const Item* n = window + (P.n - base); end < n && end->row == tail;) ++end;
   }
-  const T* grad = static_cast<const T*>(P.grad_out);
+  while (at < end && end[-1].row >= P.rows) --end;  // tokens without a row come last
+  if (at == end) return;
+
+  const T* grad = static_cast<const T*>(P.grad_out) + col;
   const Ring ring = {embed_ring + threadIdx.x};
-  const auto start = [&](int stage, int64_t i) {
-    if (i < end) {
-      const Item it = item(i);
-      if (it.row < P.rows && it.row != skip)
-        ring.start(stage, grad + it.token * P.grad_stride, col, P.width);
-    }
+  const auto start = [&](int stage, const Item* i) {
+    if (i < end) ring.start(stage, grad + i->token * P.grad_stride, P.width - col);
     ring.close();
   };
 #pragma unroll
-  for (int k = 0; k < Ring::kDeep; ++k) start(k, first + k);
+  for (int k = 0; k < Ring::kDeep; ++k) start(k, at + k);
 
-  float sum[V] = {};
+  float2 sum[V / 2];
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) sum[i] = make_float2(0.f, 0.f);
   const auto leave = [&](int slot) {
     float* parts = P.parts + (piece * 2 + slot) * P.part_width + col;
 #pragma unroll
-    for (int i = 0; i < V; i += 4)
-      *reinterpret_cast<float4*>(parts + i) =
-          make_float4(sum[i], sum[i + 1], sum[i + 2], sum[i + 3]);
+    for (int i = 0; i < V / 2; i += 2)
+      *reinterpret_cast<float4*>(parts + 2 * i) =
+          make_float4(sum[i].x, sum[i].y, sum[i + 1].x, sum[i + 1].y);
   };
-  const auto finish = [&] {  // the run ends here
-    if (open) leave(0);
-    else if (run != skip) store_sums<O, V, kAligned>(P, run, col, sum);
+  const auto finish = [&](int row) {  // the run ends here
+    if (open) {
+      leave(0);
+    } else {
+      float f[V];
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) f[2 * i] = sum[i].x, f[2 * i + 1] = sum[i].y;
+      store_sums<O, V, kAligned>(P, row, col, f);
+    }
     open = false;
   };
-  int stage = 0;
-  for (int64_t i = first; i < end; ++i) {
-    const Item it = item(i);
-    if (it.row >= P.rows) break;  // no more tokens of rows
+  int run = at->row, stage = 0;
+  for (;;) {
+    const Item it = *at;
     if (it.row != run) {
-      finish();
+      finish(run);
       run = it.row;
 #pragma unroll
-      for (int c = 0; c < V; ++c) sum[c] = 0.f;
+      for (int i = 0; i < V / 2; ++i) sum[i] = make_float2(0.f, 0.f);
     }
     ring.wait();
-    if (run != skip) {
-      float f[V];
-      to_floats<T>(ring.read(stage, grad + it.token * P.grad_stride, col), f);
+    float f[V];
+    // a row's distance from a boundary, in arithmetic modulo 2^32
+    const int bytes = static_cast<int>(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(grad)) +
+                                       static_cast<uint32_t>(it.token) *
+                                           static_cast<uint32_t>(P.grad_stride * sizeof(T))) & 15;
+    to_floats<T>(ring.read(stage, bytes), f);
 #pragma unroll
-      for (int c = 0; c < V; ++c) sum[c] += f[c];
-    }
-    start(stage, i + Ring::kDeep);
+    for (int i = 0; i < V / 2; ++i)
+      sum[i] = __fadd2_rn(sum[i], make_float2(f[2 * i], f[2 * i + 1]));
+    start(stage, at + Ring::kDeep);
     stage = stage + 1 == Ring::kDeep ? 0 : stage + 1;
+    if (++at == end) break;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   if (leaves) leave(open ? 0 : 1);
-  else finish();
+  else finish(run);
 }
 
 // Adds the parts of the long runs.  A CTA looks at the ends of kJoinPieces pieces, a lane each,

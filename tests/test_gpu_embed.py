@@ -208,6 +208,52 @@ def test_gradient_of_many_tokens():
         check_gradient(tbe.tbe_embed_backward(grad, ids, rows), grad, ids, rows, 1.0)
 
 
+@pytest.mark.parametrize("lengths", [
+    [8], [16], [24], [9], [7, 8, 9], [1, 15], [15, 1], [64, 65, 130, 1, 2, 17, 8, 8, 16, 7],
+    [3, 1000, 5], [1200], [31, 33, 32]])
+@pytest.mark.parametrize("width", [3, 40, 264])
+def test_gradient_of_runs_that_end_at_every_place(lengths, width):
+    # of the sorted tokens: at the pieces' boundaries, before and behind them
+    ids, row = [], 0
+    while len(ids) < 1500:
+        ids += [row] * lengths[row % len(lengths)]
+        row += 1
+    for lead in (0, 1, 5):
+        g = gen(lead)
+        t = torch.tensor([row + 1] * lead + ids, device="cuda")
+        t = t[torch.randperm(t.numel(), generator=g, device="cuda")]
+        grad = randn(g, t.numel(), width)
+        check_gradient(tbe.tbe_embed_backward(grad, t, row + 2), grad, t, row + 2, 1.0)
+        half = grad.half()
+        check_gradient(tbe.tbe_embed_backward(half, t, row + 2), half, t, row + 2, 1.0)
+
+
+def test_two_gradients_at_once():
+    n, rows, width = 30_000, 900, 128
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    sets = [(make_ids(n, rows, "far", torch.int64, gen(i)), randn(gen(i + 5), n, width))
+            for i in range(2)]
+    want = [tbe.tbe_embed_backward(grad, ids, rows) for ids, grad in sets]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = [tbe.tbe_embed_backward(grad, ids, rows, stream=s)
+               for (ids, grad), s in zip(sets, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_many_gradients_are_added():
+    # past what one cluster sorts, into what an output layer has left
+    n, rows, width = 120_001, 3000, 40
+    g = gen(12)
+    ids, grad = make_ids(n, rows, "far", torch.int32, g), randn(g, n, width).bfloat16()
+    ids[ids == 7] = 8
+    before = randn(g, rows, width)
+    got = before.clone()
+    tbe.tbe_embed_backward(grad, ids, rows, 0.5, out=got, accumulate=True)
+    check_gradient(got, grad, ids, rows, 0.5, before)
+
+
 def test_a_padding_rows_gradient_is_not_used():
     ids = torch.tensor([2, -1, 2, 9], device="cuda")
     grad = torch.ones(4, 16, device="cuda")

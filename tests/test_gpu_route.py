@@ -177,6 +177,23 @@ def test_choices_that_fp32_does_not_tell_apart():
     assert s.shape == (2000, 40)
 
 
+@pytest.mark.parametrize("experts,k", [(16, 3), (24, 7), (100, 8), (256, 8), (600, 15), (1000, 20)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_many_rows_that_need_exact_arithmetic(experts, k, score):
+    # logits that differ in their last bits, so that most rows' choices do
+    g = gen(experts)
+    logits = 1.0 + 2.0 ** -22 * torch.randint(0, 400, (300, experts), generator=g,
+                                              device="cuda").float()
+    bias = torch.full((experts,), 0.125, device="cuda")
+    bias[::3] += 2.0 ** -27
+    for how in (dict(), dict(renormalize=False)):
+        check(logits, k, score=score, bias=bias, **how)
+    groups = 4
+    check(logits, min(k, experts // 2), score=score, bias=bias, groups=groups, top_groups=2,
+          group_best=2)
+    check(logits, min(k, experts // 2), score=score, groups=groups, top_groups=2, group_best=2)
+
+
 def test_extreme_logits():
     logits = torch.full((6, 20), -100.0, device="cuda")
     logits[0, 3] = 100.0
