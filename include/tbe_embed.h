@@ -37,7 +37,7 @@ tbe_status tbe_embed(const void* table, int32_t dtype, int64_t rows, int64_t wid
                      float scale, void* out, int64_t out_stride, void* stream);
 
 /* Scratch of tbe_embed_backward: device memory, 16-byte aligned, any contents; none (bytes 0)
- * for a few hundred tokens. */
+ * up to 1024 tokens. */
 tbe_status tbe_embed_workspace_size(int64_t tokens, int64_t rows, int64_t width, size_t* bytes);
 
 /* grad_out [N, H] of dtype, grad_table [V, H] of out_dtype, which is dtype or TBE_DT_F32.

@@ -332,7 +332,7 @@ __device__ __forceinline__ int choose_by_bound(float (&c)[V], int e0, int K, Can
 // A row's experts are shared by L lanes, V consecutive ones a lane at most; 32 / L rows a warp.
 //
 // Instructions bound it (65536 rows, eight of 256 experts in four of eight groups by sigmoid and
-// bias: 52 us for a floor of 10.5 in bytes; 745 a row, issued in 80 % of the cycles), so reductions
+// bias: 51 us for a floor of 10.5 in bytes; 726 a row, issued in 82 % of the cycles), so reductions
 // are the warp's own (redux), the choice looks over few candidates, and what exact arithmetic
 // would cost is kept for the rows that need it.  Five CTAs a multiprocessor: 54 us with four, 53
 // with six.
