@@ -817,7 +817,11 @@ tbe_status launch(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, 
   return TBE_OK;
 }
 
-// Zeros in a matrix.
+// Zeros in a matrix.  Beside the cluster that sorts, six CTAs a multiprocessor are all resident;
+// more would wait for the cluster's end, with a CTA's whole share still to do (eight: 131 MB and
+// 8192 tokens 39.6 us instead of 34.0, 537 MB and 65536 tokens 177 instead of 154), or at sixteen
+// with less of it, which pays for large results (537 MB 150 us, 1.07 GB 303 and 319 with six; 268 MB
+// 68 and 66).
 tbe_status clear(void* p, int64_t rows, int64_t width, int64_t stride, int bytes, bool beside,
                  cudaStream_t s) {
   int64_t row = width * bytes, pitch = stride * bytes, last = row;
@@ -827,7 +831,8 @@ tbe_status clear(void* p, int64_t rows, int64_t width, int64_t stride, int bytes
     rows = (all + row - 1) / row;
     last = all - (rows - 1) * row;
   }
-  return launch(clear_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(rows, 152 * 8))),
+  const int per_sm = beside && rows * row < (400 << 20) ? 6 : 16;
+  return launch(clear_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(rows, 152 * per_sm))),
                 kMoveThreads, 0, beside, s, static_cast<char*>(p), rows, row, pitch, last, bytes);
 }
 
