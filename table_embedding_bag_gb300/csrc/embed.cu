@@ -62,14 +62,14 @@ __global__ void __launch_bounds__(kMoveThreads)
 // Tokens sorted by row, stably, as items (row, token); tokens without a row get row V, which
 // comes last.  A radix sort from the lowest digit, each pass a counting sort
 // as the experts' (a warp counts its run of the items in its own row of shared memory, the
-// rows are scanned, and the warp walks its run again).  Up to kOneLaunch tokens
-// all passes are one launch of one cluster, beside which the result is cleared; above, three
+// rows are scanned, and the warp walks its run again).  Up to kOneLaunch tokens (kOneCleared where
+// the result is cleared beside it) all passes are one launch of one cluster; above, three
 // launches a pass over the whole GPU.  Both measured, with 100000 rows (two passes), gradients of
-// 256 columns added: 32768 tokens 33 us in one launch and 42 in six, 65536 48 and 53, 131072 81 and
-// 75; of 1024 columns stored: 65536 tokens 95 and 104, 131072 136 and 133, 262144 213 and 191.
+// 256 columns added: 65536 tokens 39 us in one launch and 45 in six, 98304 52 and 51, 131072 66 and
+// 59; of 1024 columns stored: 98304 tokens 97 and 113, 131072 117 and 127, 196608 154 and 151.
 constexpr int kDigitBits = 10;  // of a pass, at most
 constexpr int kSortUnroll = 4;
-constexpr int kOneLaunch = 98304;
+constexpr int kOneLaunch = 98304, kOneCleared = 163840;
 constexpr int kTokensPerCta = 1024;   // another CTA's share (4097 tokens: 10.9 us, with 2048 12.8)
 constexpr int kGridCtas = 304;
 constexpr int kGridChunk = 4096;      // items of a CTA of three launches, at least
@@ -964,7 +964,7 @@ extern "C" tbe_status tbe_embed_backward(const void* grad_out, int32_t dtype, in
   SortPlan plan = plan_of(tokens, rows);
   plan.items[0] = reinterpret_cast<Item*>(w + l.items[0]);
   plan.items[1] = reinterpret_cast<Item*>(w + l.items[1]);
-  const bool in_cluster = tokens <= kOneLaunch;
+  const bool in_cluster = tokens <= (accumulate ? kOneLaunch : kOneCleared);
   const auto sort = [&](auto* p) {
     return in_cluster ? sort_in_cluster(p, plan, s)
                       : sort_in_grid(p, plan, reinterpret_cast<int*>(w + l.totals),
