@@ -265,24 +265,36 @@ struct Candidates {
   int e[32];
 };
 
-// The same for a row of a whole warp with many experts a lane.  The K-th largest of the lanes'
-// largest choices bounds the K-th choice from below, so only choices from there on are
-// candidates, a few more than K; they are moved to shared memory, ranked
-// against one another, a lane each, and put in order: lane j gets the j-th, past K too.  (In
-// rounds every expert chosen costs a look over the lane's V choices.)
-// *bound: no other choice is above it.
-template <int V>
+// Chosen ones up to which rows of L lanes have few enough candidates (of normally distributed choices
+// one row in 30 has more than 16 with 9 of 128 experts, one in 100 more than 8 with 4 of 64).
+__host__ __device__ constexpr int most_by_bound(int L) { return L == 32 ? 16 : L == 16 ? 9 : 4; }
+
+// The same with several experts a lane.  The K-th largest of the lanes' largest choices bounds the
+// K-th choice from below, so only choices from there on are candidates, a few more than K;
+// they are moved to shared memory, ranked against one another, a lane each, and put in
+// order: lane j of a row gets the j-th, past K too.  In rounds every expert chosen costs a look
+// over the lane's V choices (65536 rows of bf16, 8 of 128: 20.9 us, in rounds 31.3; 4 of 64: 9.9 and
+// 11.1).  *bound: no other choice is above it.  -2 throughout where a row
+// has more candidates than lanes.
+template <int V, int L>
 __device__ __forceinline__ int choose_by_bound(float (&c)[V], int e0, int K, Candidates& room,
                                                float* bound) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, place = lane & (L - 1), row = lane & ~(L - 1);
   float left = c[0];
 #pragma unroll
   for (int v = 1; v < V; ++v) left = fmaxf(left, c[v]);
   float least = kClosed;
+  if constexpr (L == 32) {
 #pragma unroll 4
-  for (int r = 0; r < K; ++r) {
-    least = row_max<32>(left);
-    if (left == least) left = kClosed;
+    for (int r = 0; r < K; ++r) {
+      least = row_max<L>(left);
+      if (left == least) left = kClosed;
+    }
+  } else {  // the least of those that fewer than K are above
+    int above = 0;
+#pragma unroll
+    for (int o = 1; o < L; ++o) above += __shfl_xor_sync(kAll, left, o) > left;
+    least = -row_max<L>(above < K ? -left : kClosed);
   }
   *bound = least;
   if (least == kClosed) least = -3.402823466e38f;  // open ones only
@@ -291,15 +303,15 @@ __device__ __forceinline__ int choose_by_bound(float (&c)[V], int e0, int K, Can
   for (int v = 0; v < V; ++v) count += c[v] >= least;
   int upto = count;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
+  for (int o = 1; o < L; o <<= 1) {
     const int y = __shfl_up_sync(kAll, upto, o);
-    if (lane >= o) upto += y;
+    if (place >= o) upto += y;
   }
-  const int all = __shfl_sync(kAll, upto, 31);
-  if (all > 32) return -2;  // many alike, or few lanes open
+  const int all = __shfl_sync(kAll, upto, row + L - 1);
+  if (__any_sync(kAll, all > L)) return -2;  // many alike, or few lanes open
   room.c[lane] = kClosed;
   __syncwarp();
-  int at = upto - count;
+  int at = row + upto - count;
 #pragma unroll
   for (int v = 0; v < V; ++v)
     if (c[v] >= least) {
@@ -308,10 +320,10 @@ __device__ __forceinline__ int choose_by_bound(float (&c)[V], int e0, int K, Can
     }
   __syncwarp();
   const float mine = room.c[lane];
-  const int e = lane < all ? room.e[lane] : -1;
+  const int e = place < all ? room.e[lane] : -1;
   int rank = 0;
-  for (int j = 0; j < all; j += 4) {
-    const float4 o = *reinterpret_cast<const float4*>(room.c + j);
+  for (int j = 0; j < (L == 32 ? all : L); j += 4) {
+    const float4 o = *reinterpret_cast<const float4*>(room.c + row + j);
     rank += o.x > mine;
     rank += o.y > mine;
     rank += o.z > mine;
@@ -319,12 +331,13 @@ __device__ __forceinline__ int choose_by_bound(float (&c)[V], int e0, int K, Can
   }
   // Choices that are alike share a rank, and the ranks' sum falls short: they take the order of
   // the experts, in which they stand.
-  if (static_cast<int>(__reduce_add_sync(kAll, lane < all ? rank : 0)) != all * (all - 1) / 2)
-    for (int j = 0; j < all; ++j) rank += room.c[j] == mine && j < lane;
+  const int expected = place == 0 ? all * (all - 1) / 2 : 0;
+  if (static_cast<int>(__reduce_add_sync(kAll, (place < all ? rank : 0) - expected)) != 0)
+    for (int j = 0; j < all; ++j) rank += room.c[row + j] == mine && j < place;
   __syncwarp();
-  if (lane < all) room.e[rank] = e;
+  if (place < all) room.e[row + rank] = e;
   __syncwarp();
-  const int sorted = lane < all ? room.e[lane] : -1;
+  const int sorted = place < all ? room.e[lane] : -1;
   __syncwarp();
   return sorted;
 }
@@ -336,11 +349,11 @@ __device__ __forceinline__ int choose_by_bound(float (&c)[V], int e0, int K, Can
 // are the warp's own (redux), the choice looks over few candidates, and what exact arithmetic
 // would cost is kept for the rows that need it.  Five CTAs a multiprocessor: 54 us with four, 53
 // with six.
-template <typename T, int V, int L>
+// kCandidates: choose_by_bound, which has a kernel of its own as its registers cost the rounds 5 %.
+template <typename T, int V, int L, bool kCandidates>
 __global__ void __launch_bounds__(256, V <= 8 ? 5 : 1)
     route_kernel(const __grid_constant__ RouteArgs P) {
   constexpr int kRows = 32 / L;
-  constexpr bool kBound = L == 32 && V >= 4;
   extern __shared__ __align__(16) double route_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, place = lane & (L - 1);
   const int64_t token0 = (static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp) * kRows;
@@ -493,9 +506,8 @@ __global__ void __launch_bounds__(256, V <= 8 ? 5 : 1)
   const int K = P.by_logits ? P.k : P.k + 1;
   int mine = -2;  // lane j of the row: the j-th expert
   float bound = kClosed;
-  if constexpr (kBound) {
-    if (K <= 16) mine = choose_by_bound<V>(c, e0, K, *reinterpret_cast<Candidates*>(room), &bound);
-  }
+  if constexpr (kCandidates)
+    mine = choose_by_bound<V, L>(c, e0, K, *reinterpret_cast<Candidates*>(room), &bound);
   const bool in_rounds = mine == -2;
   if (in_rounds) mine = choose_in_rounds<V, L>(c, e0, K);
   float chosen = mine >= 0 ? to_f32(logits[mine]) : 0.f;
@@ -658,7 +670,9 @@ tbe_status check_route(int32_t dtype, int64_t tokens, int32_t experts, int32_t s
 int id_bytes(int32_t index_dtype) { return index_dtype == TBE_DT_I32 ? 4 : 8; }
 
 // How rows are shared: as few lanes as hold the chosen ones (and the next) with at most eight
-// experts each, so that a warp's reductions serve several rows.
+// experts each, so that a warp's reductions serve several rows; but a warp a row where that makes
+// the candidates few (65536 rows: 10 of 128 31 us and 39, 12 32 and 44; sixteen lanes a row for the
+// same reason are slower, 6 of 64 17.3 and 14.7).
 template <typename T>
 tbe_status launch_route(RouteArgs args, cudaStream_t s) {
   const int size = args.experts / args.groups;
@@ -666,23 +680,32 @@ tbe_status launch_route(RouteArgs args, cudaStream_t s) {
   while (slots < args.groups) slots *= 2;
   int lanes = 8;
   const int kept = args.by_logits ? args.k : args.k + 1;
-  const auto each = [&] {  // experts of a lane
-    return lanes < slots ? INT32_MAX : (size + lanes / slots - 1) / (lanes / slots);
+  const auto each = [&](int l) {  // experts of a lane, of l a row
+    return l < slots ? INT32_MAX : (size + l / slots - 1) / (l / slots);
   };
-  while (lanes < 32 && (lanes < kept || each() > 8)) lanes *= 2;
+  while (lanes < 32 && (lanes < kept || each(lanes) > 8 ||
+                        (lanes == 16 && kept > most_by_bound(16) && each(32) > 2)))
+    lanes *= 2;
   args.size = size;
   args.group_lanes = lanes / slots;
   for (args.log_lanes = 0; 1 << args.log_lanes < args.group_lanes;) ++args.log_lanes;
-  args.lane_experts = each();
+  args.lane_experts = each(lanes);
   const auto go = [&](auto v, auto l) {
     constexpr int V = decltype(v)::value, L = decltype(l)::value;
     constexpr int kPart = V * sizeof(T) < 16 ? V : 16 / static_cast<int>(sizeof(T));
     args.vectors = args.lane_experts == V && size % V == 0 && args.stride % kPart == 0 &&
                    aligned_to(args.logits, kPart * sizeof(T)) && aligned_to(args.bias, 16);
     const int warps = args.experts > 512 ? 4 : 8, rows = warps * (32 / L);
-    route_kernel<T, V, L><<<static_cast<unsigned>((args.tokens + int64_t(rows) - 1) / rows),
-                            warps * 32, warps * room_of(args.experts) * sizeof(double), s>>>(args);
-    return launched();
+    const auto run = [&](auto candidates) {
+      route_kernel<T, V, L, decltype(candidates)::value>
+          <<<static_cast<unsigned>((args.tokens + int64_t(rows) - 1) / rows), warps * 32,
+             warps * room_of(args.experts) * sizeof(double), s>>>(args);
+      return launched();
+    };
+    if constexpr (V >= 4) {
+      if (kept <= most_by_bound(L)) return run(std::true_type{});
+    }
+    return run(std::false_type{});
   };
   const auto with = [&](auto l) {
     constexpr int L = decltype(l)::value;

@@ -194,6 +194,25 @@ def test_many_rows_that_need_exact_arithmetic(experts, k, score):
     check(logits, min(k, experts // 2), score=score, groups=groups, top_groups=2, group_best=2)
 
 
+@pytest.mark.parametrize("experts,k", [
+    (32, 4), (40, 3), (64, 4), (64, 8), (96, 9), (128, 8), (128, 9), (100, 12), (128, 16), (256, 8)])
+@pytest.mark.parametrize("how", [HOW[0], HOW[5], HOW[6]])
+def test_rows_with_many_and_few_candidates_side_by_side(experts, k, how):
+    # few values, so that many choices are alike; the largest side by side; most or all closed
+    g = gen(experts * k)
+    logits = torch.randint(-2, 3, (400, experts), generator=g, device="cuda") / 2
+    logits[1::7] += randn(g, experts) * 0.01
+    logits[2::7] = randn(g, logits[2::7].shape[0], experts)
+    logits[3::7, 5:5 + k + 2] += 4.0
+    closed = torch.rand(logits[4::7].shape, generator=g, device="cuda") < 0.97
+    logits[4::7] = torch.where(closed, -math.inf, logits[4::7])
+    logits[5::14] = -math.inf
+    logits[6::7] = 0.25
+    check(logits, k, **with_bias(how, experts, g))
+    if how.get("bias"):
+        check(logits, k, **dict(how, bias=torch.zeros(experts, device="cuda")))
+
+
 def test_extreme_logits():
     logits = torch.full((6, 20), -100.0, device="cuda")
     logits[0, 3] = 100.0
