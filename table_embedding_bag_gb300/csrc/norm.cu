@@ -99,18 +99,29 @@ __device__ __forceinline__ float2 both(float f) { return make_float2(f, f); }
 
 // The thread's part of the weight.  In the rows' type it stays in registers; in fp32 beside
 // 16-bit rows it is read for each row.
-template <typename T, bool kAligned, int NV>
+template <typename T, bool kAligned, int NV, bool kShifted>
 struct Weight {
   using U = Units<T, kAligned>;
   static constexpr int V = U::V;
   Pack<T, V> own[NV];
   const float* wide;
-  int width;
+  int width, lead;
 
-  __device__ __forceinline__ Weight(const void* weight, bool w32, int width_) : width(width_) {
+  // lead: columns of the first unit before the row (kShifted).
+  __device__ __forceinline__ Weight(const void* weight, bool w32, int width_, int lead_)
+      : width(width_), lead(lead_) {
     wide = sizeof(T) == 2 && weight && w32 ? static_cast<const float*>(weight) : nullptr;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      if constexpr (kShifted) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int c = U::col(j) + i - lead;
+          own[j].v[i] = weight && !wide && c >= 0 && c < width ? static_cast<const T*>(weight)[c]
+                                                              : from_f32<T>(1.f);
+        }
+        continue;
+      }
       const bool on = weight && !wide && U::col(j) < width;
       own[j] = load_unit<T, V>(static_cast<const T*>(weight), U::col(j), on);
       if (!on)
@@ -125,7 +136,10 @@ struct Weight {
           const int a = U::col(2 * i), b = U::col(2 * i + 1);
           return make_float2(a < width ? wide[a] : 1.f, b < width ? wide[b] : 1.f);
         } else {
-          const int col = U::col(i / (V / 2)) + i % (V / 2) * 2;
+          const int col = U::col(i / (V / 2)) + i % (V / 2) * 2 - lead;
+          if constexpr (kShifted)
+            return make_float2(col >= 0 && col < width ? wide[col] : 1.f,
+                               col + 1 >= 0 && col + 1 < width ? wide[col + 1] : 1.f);
           return col < width ? *reinterpret_cast<const float2*>(wide + col) : both(1.f);
         }
       }
@@ -168,12 +182,13 @@ struct Ahead {
   __device__ __forceinline__ uint4* slot(int stage, int in, int j) const {
     return slots + ((stage * kIn + in) * NV + j) * (blockDim.x * blockDim.y);
   }
+  // From the boundary `lead` columns before the row up to column `end` from there.
   __device__ __forceinline__ void start(int stage, int in, const void* matrix, int64_t stride,
-                                        int64_t row, int width) const {
-    const T* from = static_cast<const T*>(matrix) + row * stride;
+                                        int64_t row, int lead, int end) const {
+    const T* from = static_cast<const T*>(matrix) + row * stride - lead;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int col = U::col(j), bytes = col < width ? 16 : 0;  // the rest are zeros
+      const int col = U::col(j), bytes = col < end ? 16 : 0;  // the rest are zeros
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(static_cast<unsigned>(
                        __cvta_generic_to_shared(slot(stage, in, j)))),
                    "l"(from + (bytes ? col : 0)), "r"(bytes)
@@ -198,32 +213,72 @@ struct Ahead {
 
 extern __shared__ uint4 norm_ring[];
 
+// The rows that a row of threads walks: `first` of its CTA, its own `row`, then `step` on.  Shifted
+// rows are off 16 bytes, by as much as others are every kVec rows; a CTA's are alike, so `lead`,
+// the columns between the boundary and the row, is the same for all of a thread's
+// rows.  Its vectors begin at the boundary: the first and the last of a row hold other columns, which
+// are zeros here and not stored.
+template <typename T, bool kShifted>
+struct Walk {
+  int64_t first, row, step;
+  int lead, end;  // columns, from the boundary on
+
+  __device__ __forceinline__ Walk(const void* p, int64_t stride, int width) {
+    constexpr int kAlike = kShifted ? kVec<T> : 1;
+    const int y = blockDim.y, b = blockIdx.x;
+    first = b % kAlike + static_cast<int64_t>(b / kAlike) * y * kAlike;
+    row = first + static_cast<int64_t>(threadIdx.y) * kAlike;
+    step = static_cast<int64_t>(gridDim.x / kAlike) * y * kAlike;
+    lead = kShifted ? tbe::lead<T>(static_cast<const T*>(p) + first * stride) : 0;
+    end = lead + width;
+  }
+  __device__ __forceinline__ void next() { first += step, row += step; }
+  // Zeros in a vector's columns outside the row.
+  __device__ __forceinline__ void mask(Pack<T, kVec<T>>& v, int col) const {
+    if (!kShifted || (col >= lead && col + kVec<T> <= end)) return;
+#pragma unroll
+    for (int i = 0; i < kVec<T>; ++i)
+      if (col + i < lead || col + i >= end) v.v[i] = from_f32<T>(0.f);
+  }
+  // `boundary`: the row's start less `lead`.
+  __device__ __forceinline__ void store(T* boundary, int col, const Pack<T, kVec<T>>& v) const {
+    if (!kShifted || (col >= lead && col + kVec<T> <= end)) {
+      store_unit<T, kVec<T>>(boundary, col, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVec<T>; ++i)
+        if (col + i >= lead && col + i < end) boundary[col + i] = v.v[i];
+    }
+  }
+};
+
 // kIn: 2 with a residual; rows off 16 bytes, which are loaded where they are needed, ask for it.
-template <typename T, bool kFp8, bool kAligned, int NV, int kIn>
+template <typename T, bool kFp8, bool kAligned, int NV, int kIn, bool kShifted>
 __global__ void __launch_bounds__(kNormThreads)
     rms_norm_kernel(const __grid_constant__ NormArgs P) {
   using U = Units<T, kAligned>;
   constexpr int V = U::V, kPairs = NV * V / 2;
   using Ring = Ahead<T, kAligned, NV, kIn>;
   __shared__ float parts[2][kNormThreads / 32][1];
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  Walk<T, kShifted> walk(P.x, P.xs, P.width);
+  const int lead = walk.lead, end = walk.end;
   const Ring ring = {norm_ring + threadIdx.y * blockDim.x + threadIdx.x};
   const auto start = [&](int stage, int64_t r) {
     if (r < P.rows) {
-      ring.start(stage, 0, P.x, P.xs, r, P.width);
-      if (kIn == 2) ring.start(stage, 1, P.residual, P.rs, r, P.width);
+      ring.start(stage, 0, P.x, P.xs, r, lead, end);
+      if (kIn == 2) ring.start(stage, 1, P.residual, P.rs, r, lead, end);
     }
     ring.close();
   };
   if constexpr (kAligned) {
 #pragma unroll
-    for (int k = 0; k < Ring::kDeep; ++k) start(k, row + k * step);
+    for (int k = 0; k < Ring::kDeep; ++k) start(k, walk.row + k * walk.step);
   }
-  const Weight<T, kAligned, NV> weight(P.weight, P.w32, P.width);
+  const Weight<T, kAligned, NV, kShifted> weight(P.weight, P.w32, P.width, lead);
   int stage = 0, turn = 0;
   // as many rounds for all rows of the CTA
-  for (int64_t first = row - threadIdx.y; first < P.rows; first += step, row += step, turn ^= 1) {
+  for (; walk.first < P.rows; walk.next(), turn ^= 1) {
+    const int64_t row = walk.row;
     const bool live = row < P.rows;  // the others take part in the barriers
     Pack<T, V> v[NV];                // zeros from `width` on
     if constexpr (kAligned) {
@@ -249,11 +304,18 @@ __global__ void __launch_bounds__(kNormThreads)
       for (int i = 0; i < kPairs; ++i)  // the sum as it is held
         set_pair(v, i, __fadd2_rn(pair_at(v, i), pair_at(b, i)));
       if (P.h && live) {
-        T* h = static_cast<T*>(P.h) + row * P.hs;
+        T* h = static_cast<T*>(P.h) + row * P.hs - lead;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-          if (U::col(j) < P.width) store_unit<T, V>(h, U::col(j), v[j]);
+          if (U::col(j) < end) {
+            if constexpr (kAligned) walk.store(h, U::col(j), v[j]);
+            else store_unit<T, V>(h, U::col(j), v[j]);
+          }
       }
+    }
+    if constexpr (kShifted) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) walk.mask(v[j], U::col(j));
     }
     float2 squares = both(0.f);
 #pragma unroll
@@ -261,18 +323,21 @@ __global__ void __launch_bounds__(kNormThreads)
     float sum[1] = {squares.x + squares.y};
     row_sums(sum, parts[turn]);
     if constexpr (kAligned) {  // all of the row's slots have been read
-      start(stage, row + Ring::kDeep * step);
+      start(stage, row + Ring::kDeep * walk.step);
       stage = stage + 1 == Ring::kDeep ? 0 : stage + 1;
     }
     const float2 u = both(rsqrtf(__fdiv_rn(sum[0], static_cast<float>(P.width)) + P.eps));
     if constexpr (!kFp8) {
-      T* y = static_cast<T*>(P.y) + row * P.ys;
+      T* y = static_cast<T*>(P.y) + row * P.ys - lead;
 #pragma unroll
       for (int i = 0; i < kPairs; ++i)
         set_pair(v, i, __fmul2_rn(__fmul2_rn(pair_at(v, i), u), weight.at(i)));
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if (live && U::col(j) < P.width) store_unit<T, V>(y, U::col(j), v[j]);
+        if (live && U::col(j) < end) {
+          if constexpr (kAligned) walk.store(y, U::col(j), v[j]);
+          else store_unit<T, V>(y, U::col(j), v[j]);
+        }
     } else {
       constexpr int kUnits = kAligned ? 1 : 4;          // units of a thread in a block of 128
       constexpr int kLanes = kAligned ? kBlock / V : 32;  // lanes that share it
@@ -324,7 +389,7 @@ struct NormGradArgs {
 // too, unless that is so much that registers run out: then both passes over it read the ring
 // (65536 x 2048 bf16 shared by 64 threads: 222 us, with the row in registers 285).  kIn: 3 with a
 // gradient that arrives at h.
-template <typename T, bool kAligned, int NV, int kIn>
+template <typename T, bool kAligned, int NV, int kIn, bool kShifted>
 __global__ void __launch_bounds__(kNormThreads)
     rms_norm_backward_kernel(const __grid_constant__ NormGradArgs P) {
   using U = Units<T, kAligned>;
@@ -336,24 +401,25 @@ __global__ void __launch_bounds__(kNormThreads)
   float2 acc[kPairs];
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) acc[i] = both(0.f);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  Walk<T, kShifted> walk(P.h, P.hs, P.width);
+  const int lead = walk.lead, end = walk.end;
   const Ring ring = {norm_ring + threadIdx.y * blockDim.x + threadIdx.x};
   const auto start = [&](int stage, int64_t r) {
     if (r < P.rows) {
-      ring.start(stage, 0, P.h, P.hs, r, P.width);
-      ring.start(stage, 1, P.gy, P.gys, r, P.width);
-      if (kIn == 3) ring.start(stage, 2, P.gh, P.ghs, r, P.width);
+      ring.start(stage, 0, P.h, P.hs, r, lead, end);
+      ring.start(stage, 1, P.gy, P.gys, r, lead, end);
+      if (kIn == 3) ring.start(stage, 2, P.gh, P.ghs, r, lead, end);
     }
     ring.close();
   };
   if constexpr (kAligned) {
 #pragma unroll
-    for (int k = 0; k < Ring::kDeep; ++k) start(k, row + k * step);
+    for (int k = 0; k < Ring::kDeep; ++k) start(k, walk.row + k * walk.step);
   }
-  const Weight<T, kAligned, NV> weight(P.weight, P.w32, P.width);
+  const Weight<T, kAligned, NV, kShifted> weight(P.weight, P.w32, P.width, lead);
   int stage = 0, turn = 0;
-  for (int64_t first = row - threadIdx.y; first < P.rows; first += step, row += step, turn ^= 1) {
+  for (; walk.first < P.rows; walk.next(), turn ^= 1) {
+    const int64_t row = walk.row, step = walk.step;
     const bool live = row < P.rows;
     const T* from[3] = {static_cast<const T*>(P.h) + row * P.hs,
                         static_cast<const T*>(P.gy) + row * P.gys,
@@ -366,7 +432,8 @@ __global__ void __launch_bounds__(kNormThreads)
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           if constexpr (kAligned) held[in][j] = ring.unit(stage, in, j);
-          else
+          if constexpr (kShifted) walk.mask(held[in][j], U::col(j));
+          if constexpr (!kAligned)
             held[in][j] = load_unit<T, V>(from[in], U::col(j),
                                           live && from[in] && U::col(j) < P.width);
         }
@@ -376,6 +443,7 @@ __global__ void __launch_bounds__(kNormThreads)
       for (int k = 0; k < kStep; ++k) {
         if constexpr (kHold) v[k] = held[in][j + k];
         else v[k] = ring.unit(stage, in, j + k);
+        if constexpr (kShifted && !kHold) walk.mask(v[k], U::col(j + k));
       }
     };
     float2 squares = both(0.f), dots = both(0.f);  // of h; of d and h
@@ -402,7 +470,7 @@ __global__ void __launch_bounds__(kNormThreads)
     const float width = static_cast<float>(P.width);
     const float2 u = both(rsqrtf(__fdiv_rn(sum[0], width) + P.eps));
     const float2 mean = both(-__fdiv_rn(sum[1] * u.x, width));
-    T* gx = static_cast<T*>(P.gx) + row * P.gxs;
+    T* gx = static_cast<T*>(P.gx) + row * P.gxs - lead;
 #pragma unroll
     for (int j = 0; j < NV; j += kStep) {
       Pack<T, V> a[kStep], b[kStep], c[kStep];
@@ -420,7 +488,10 @@ __global__ void __launch_bounds__(kNormThreads)
       }
 #pragma unroll
       for (int k = 0; k < kStep; ++k)
-        if (live && U::col(j + k) < P.width) store_unit<T, V>(gx, U::col(j + k), a[k]);
+        if (live && U::col(j + k) < end) {
+          if constexpr (kAligned) walk.store(gx, U::col(j + k), a[k]);
+          else store_unit<T, V>(gx, U::col(j + k), a[k]);
+        }
     }
     if constexpr (kAligned && !kHold) {
       start(used, row + Ring::kDeep * step);
@@ -449,8 +520,13 @@ __global__ void __launch_bounds__(kNormThreads)
       if (U::col(2 * i) < P.width) to[U::col(2 * i)] = acc[i].x;
       if (U::col(2 * i + 1) < P.width) to[U::col(2 * i + 1)] = acc[i].y;
     } else {
-      const int col = U::col(i / (V / 2)) + i % (V / 2) * 2;
-      if (col < P.width) to[col] = acc[i].x, to[col + 1] = acc[i].y;
+      const int col = U::col(i / (V / 2)) + i % (V / 2) * 2 - lead;
+      if constexpr (kShifted) {
+        if (col >= 0 && col < P.width) to[col] = acc[i].x;
+        if (col + 1 >= 0 && col + 1 < P.width) to[col + 1] = acc[i].y;
+      } else if (col < P.width) {
+        to[col] = acc[i].x, to[col + 1] = acc[i].y;
+      }
     }
   }
 }
@@ -526,14 +602,38 @@ Shape backward_shape(int64_t rows, int64_t vectors, int most) {
   return with_rows(s, rows, s.threads == 32 ? 256 : s.threads);
 }
 
+// Whether rows of the matrices are off 16 bytes alike.
+bool alike(const Matrix* m, int n) {
+  const auto off = [](const Matrix& a, const Matrix& b) {
+    const uintptr_t starts = reinterpret_cast<uintptr_t>(a.p) ^ reinterpret_cast<uintptr_t>(b.p);
+    return (starts | (static_cast<uint64_t>(a.stride) - static_cast<uint64_t>(b.stride)) *
+                         static_cast<uint64_t>(a.bytes)) % 16 != 0;
+  };
+  for (int i = 1; i < n; ++i)
+    if (m[i].p && off(m[i], m[0])) return false;
+  return true;
+}
+
+// Whether rows off 16 bytes alike are moved in the vectors of their boundaries (Walk), where those fit
+// the threads: 65536 x 1001 bf16 44 us and by single elements 114, with a residual 93 and 142, gradients
+// 102 and 171.  But up to 128 columns, four elements of a warp's threads, those are faster (100000
+// x 101: 18 us, in vectors 23; x 137: 33 and 23), and for the gradients of few rows, as a thread has
+// more rows one after another in vectors (300 x 1001: 5.6 us and 6.9, 4000: 16.2 and 15.5).
+template <typename T>
+bool in_shifted_vectors(int64_t width) {
+  return width > 128 && (width + 2 * kVec<T> - 2) / kVec<T> <= kMostUnits<T> * kNormThreads;
+}
+constexpr int64_t kShiftedGradRows = 152 * 16;
+
 // CTAs of a launch: as many as fit the GPU with `bytes` of shared memory and as many registers a
-// thread, or fewer.
-int64_t ctas_of(const Shape& s, int64_t rows, int bytes, int registers) {
+// thread, or fewer.  alike: they come in so many kinds (Walk).
+int64_t ctas_of(const Shape& s, int64_t rows, int bytes, int registers, int alike) {
   const int threads = s.threads * s.rows;
   const int regs = 65536 / ((registers + 7) / 8 * 8) / threads;
   const int fit = std::max(
       1, std::min({regs, 2048 / threads, kNormShared / (bytes * threads + 1024), 32}));
-  return std::min<int64_t>((rows + s.rows - 1) / s.rows, int64_t(152) * fit);
+  const int64_t each = (rows + alike - 1) / alike;  // rows of a kind
+  return std::min<int64_t>((each + s.rows - 1) / s.rows * alike, int64_t(152) * fit);
 }
 
 template <typename Args>
@@ -599,28 +699,36 @@ tbe_status run_norm(const void* x, const void* residual, const void* weight, int
                          weight_dtype == TBE_DT_F32, eps};
   return for_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    const auto go = [&](auto aligned, auto in, const Shape& s) {
-      constexpr bool kAligned = decltype(aligned)::value;
+    const auto go = [&](auto aligned, auto shifted, auto in, const Shape& s) {
+      constexpr bool kAligned = decltype(aligned)::value, kShifted = decltype(shifted)::value;
       constexpr int kIn = decltype(in)::value;
       tbe_status st = TBE_OK;
       for_units<kAligned ? 1 : 4, kAligned ? kMostUnits<T> : 32>(s.units, [&](auto n) {
         constexpr int NV = decltype(n)::value;
         constexpr int kBytes = kAligned ? Ahead<T, kAligned, NV, kIn>::kBytes : 0;
-        const auto kernel = rms_norm_kernel<T, kFp8, kAligned, NV, kIn>;
+        const auto kernel = rms_norm_kernel<T, kFp8, kAligned, NV, kIn, kShifted>;
         static const int registers = registers_of(kernel);
-        const int64_t ctas =
-            kAligned ? ctas_of(s, rows, kBytes, registers) : (rows + s.rows - 1) / s.rows;
+        const int64_t ctas = kAligned
+                                 ? ctas_of(s, rows, kBytes, registers, kShifted ? kVec<T> : 1)
+                                 : (rows + s.rows - 1) / s.rows;
         st = launch_norm(kernel, args, s, ctas, kBytes, stream);
       });
       return st;
     };
-    const auto with = [&](auto in) {
-      return go(std::true_type{}, in, forward_shape(rows, width / kVec<T>, kMostUnits<T>));
+    const auto with = [&](auto shifted, auto in) {
+      const int64_t vectors = (width + (vec ? 0 : 2 * kVec<T> - 2)) / kVec<T>;
+      return go(std::true_type{}, shifted, in, forward_shape(rows, vectors, kMostUnits<T>));
     };
+    // (fp32 rows are summed in one order, so that their norm, quantised, is the norm in 8 bits)
+    if constexpr (!kFp8 && sizeof(T) == 2) {
+      const Matrix moved[4] = {in[0], in[1], out[0], out[1]};
+      if (!vec && alike(moved, 4) && in_shifted_vectors<T>(width))
+        return residual ? with(std::true_type{}, Int<2>{}) : with(std::true_type{}, Int<1>{});
+    }
     if (!vec)
-      return go(std::false_type{}, Int<2>{},
+      return go(std::false_type{}, std::false_type{}, Int<2>{},
                 with_rows(shape_of(width, 4, 32, 8), rows, 256));
-    return residual ? with(Int<2>{}) : with(Int<1>{});
+    return residual ? with(std::false_type{}, Int<2>{}) : with(std::false_type{}, Int<1>{});
   });
 }
 
@@ -701,10 +809,10 @@ extern "C" tbe_status tbe_rms_norm_backward(const void* grad_y, const void* h, c
                          weight_dtype == TBE_DT_F32, eps};
     const tbe_status st = for_dtype(dtype, [&](auto t) {
       using T = decltype(t);
-      const auto go = [&](auto aligned, auto in, Shape sh) {
-        constexpr bool kAligned = decltype(aligned)::value;
-        constexpr int kIn = decltype(in)::value;
-        while (sh.rows > rows) sh.rows /= 2;
+      const auto go = [&](auto aligned, auto shifted, auto in, Shape sh) {
+        constexpr bool kAligned = decltype(aligned)::value, kShifted = decltype(shifted)::value;
+        constexpr int kIn = decltype(in)::value, kAlike = kShifted ? kVec<T> : 1;
+        while (sh.rows > 1 && sh.rows * kAlike > rows) sh.rows /= 2;
         tbe_status st = TBE_OK;
         for_units<kAligned ? 1 : 4, kAligned ? kMostUnits<T> : 32>(sh.units, [&](auto n) {
           constexpr int NV = decltype(n)::value;
@@ -713,22 +821,26 @@ extern "C" tbe_status tbe_rms_norm_backward(const void* grad_y, const void* h, c
           constexpr int kBytes = kAligned ? Ahead<T, kAligned, NV, kIn>::kBytes : kSums;
           static_assert(kBytes >= kSums, "");
           // whole groups of rows only, so that the parts are no more than the rows
-          const auto kernel = rms_norm_backward_kernel<T, kAligned, NV, kIn>;
+          const auto kernel = rms_norm_backward_kernel<T, kAligned, NV, kIn, kShifted>;
           static const int registers = registers_of(kernel);
-          const int64_t ctas = std::min({ctas_of(sh, rows, kBytes, registers), rows / sh.rows,
-                                         int64_t(kNormParts)});
+          const int64_t ctas = std::min({ctas_of(sh, rows, kBytes, registers, kAlike),
+                                         rows / (sh.rows * kAlike) * kAlike, int64_t(kNormParts)});
           parts = static_cast<int>(ctas);
           st = launch_norm(kernel, args, sh, ctas, kBytes, s);
         });
         return st;
       };
-      const auto with = [&](auto in) {
-        return go(std::true_type{}, in, backward_shape(rows, width / kVec<T>, kMostUnits<T>));
+      const auto with = [&](auto shifted, auto in) {
+        const int64_t vectors = (width + (vec ? 0 : 2 * kVec<T> - 2)) / kVec<T>;
+        return go(std::true_type{}, shifted, in, backward_shape(rows, vectors, kMostUnits<T>));
       };
+      const Matrix moved[4] = {in[0], in[1], in[2], out};
+      if (!vec && rows >= kShiftedGradRows && alike(moved, 4) && in_shifted_vectors<T>(width))
+        return grad_h ? with(std::true_type{}, Int<3>{}) : with(std::true_type{}, Int<2>{});
       if (!vec)
-        return go(std::false_type{}, Int<3>{},
+        return go(std::false_type{}, std::false_type{}, Int<3>{},
                   with_rows(shape_of(width, 4, 32, 4), rows, 256));
-      return grad_h ? with(Int<3>{}) : with(Int<2>{});
+      return grad_h ? with(std::false_type{}, Int<3>{}) : with(std::false_type{}, Int<2>{});
     });
     if (st != TBE_OK) return st;
   }

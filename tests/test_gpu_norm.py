@@ -194,6 +194,43 @@ def test_strided_rows(dtype, pad, shift):
     assert bool((room == 7).all())
 
 
+@pytest.mark.parametrize("rows,width,pad,shift", [
+    (2437, 137, 0, 0), (2500, 1001, 0, 0), (2439, 1001, 6, 3), (20_001, 261, 3, 7),
+    (2433, 4099, 5, 2), (41, 2051, 13, 5), (3, 1001, 0, 0), (2440, 136, 16, 1)])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("weight", ["own", "fp32", None])
+def test_rows_off_16_bytes_among_nan(rows, width, pad, shift, dtype, weight):
+    # all matrices alike, what lies between the rows not a number
+    _, _, _, _, w = make(1, width, dtype, width, weight)
+    nan = lambda: torch.full((rows * (width + pad) + 64,), float("nan"), dtype=dtype, device="cuda")
+    g = gen(rows)
+
+    def cut(value=None):
+        room = nan()
+        rows_of = room[shift:shift + rows * (width + pad)].view(rows, width + pad)[:, :width]
+        if value is not None:
+            rows_of.copy_(value)
+        return room, rows_of
+
+    x, res, gy, gh = (cut(randn(g, rows, width).to(dtype))[1] for _ in range(4))
+    rooms = [cut() for _ in range(3)]
+    y, h = tbe.tbe_rms_norm(x, w, residual=res, out=rooms[0][1], h=rooms[1][1])
+    assert torch.equal(h, (x.float() + res.float()).to(dtype))
+    near(y, norm64(h, w, 1e-6))
+    near(tbe.tbe_rms_norm(x, w, out=y), norm64(x, w, 1e-6))
+    for given in (None, gh):
+        dx, dw = tbe.tbe_rms_norm_backward(gy, h, w, grad_h=given, grad_x=rooms[2][1])
+        rx, size, rw, total = gradient64(gy, h, w, given, 1e-6)
+        near(dx, rx, size, 2.0 ** -17)
+        assert bool(((dw.double() - rw).abs() <= (2.0 ** -17 + rows * 2.0 ** -24) * total).all())
+        again, dw2 = tbe.tbe_rms_norm_backward(gy, h, w, grad_h=given)  # on other boundaries
+        near(again, rx, size, 2.0 ** -17)
+        assert bool(((dw2.double() - rw).abs() <= (2.0 ** -17 + rows * 2.0 ** -24) * total).all())
+    for room, written in rooms:
+        written.zero_()
+        assert int(room.isnan().sum()) == room.numel() - rows * width
+
+
 def test_without_rows():
     none = torch.zeros(0, 24, device="cuda")
     assert tbe.tbe_rms_norm(none).shape == (0, 24)
