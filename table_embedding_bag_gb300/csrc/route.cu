@@ -308,7 +308,8 @@ __device__ __forceinline__ int choose_by_bound(float (&c)[V], int e0, int K, Can
     if (place >= o) upto += y;
   }
   const int all = __shfl_sync(kAll, upto, row + L - 1);
-  if (__any_sync(kAll, all > L)) return -2;  // many alike, or few lanes open
+  const bool many = L == 32 ? all > L : __any_sync(kAll, all > L);
+  if (many) return -2;  // many alike, or few lanes open
   room.c[lane] = kClosed;
   __syncwarp();
   int at = row + upto - count;
@@ -331,8 +332,10 @@ __device__ __forceinline__ int choose_by_bound(float (&c)[V], int e0, int K, Can
   }
   // Choices that are alike share a rank, and the ranks' sum falls short: they take the order of
   // the experts, in which they stand.
-  const int expected = place == 0 ? all * (all - 1) / 2 : 0;
-  if (static_cast<int>(__reduce_add_sync(kAll, (place < all ? rank : 0) - expected)) != 0)
+  const int ranks = all * (all - 1) / 2;  // of a row without
+  const int short_of = L == 32 ? 0 : place == 0 ? ranks : 0;
+  if (static_cast<int>(__reduce_add_sync(kAll, (place < all ? rank : 0) - short_of)) !=
+      (L == 32 ? ranks : 0))
     for (int j = 0; j < all; ++j) rank += room.c[row + j] == mine && j < place;
   __syncwarp();
   if (place < all) room.e[row + rank] = e;
@@ -345,7 +348,7 @@ __device__ __forceinline__ int choose_by_bound(float (&c)[V], int e0, int K, Can
 // A row's experts are shared by L lanes, V consecutive ones a lane at most; 32 / L rows a warp.
 //
 // Instructions bound it (65536 rows, eight of 256 experts in four of eight groups by sigmoid and
-// bias: 51 us for a floor of 10.5 in bytes; 726 a row, issued in 82 % of the cycles), so reductions
+// bias: 51 us for a floor of 10.5 in bytes; 732 a row, issued in 85 % of the cycles), so reductions
 // are the warp's own (redux), the choice looks over few candidates, and what exact arithmetic
 // would cost is kept for the rows that need it.  Five CTAs a multiprocessor: 54 us with four, 53
 // with six.
