@@ -208,6 +208,37 @@ def test_gradient_of_many_tokens():
         check_gradient(tbe.tbe_embed_backward(grad, ids, rows), grad, ids, rows, 1.0)
 
 
+@pytest.mark.parametrize("n", [98_304, 98_305, 163_840, 163_841])
+def test_gradient_around_the_limits_of_one_launch(n):
+    rows, width = 40_000, 24
+    g = gen(n)
+    ids, grad = make_ids(n, rows, "far", torch.int64, g), randn(g, n, width).half()
+    check_gradient(tbe.tbe_embed_backward(grad, ids, rows, 0.5), grad, ids, rows, 0.5)
+    before = randn(g, rows, width)
+    got = before.clone()
+    tbe.tbe_embed_backward(grad, ids, rows, 0.5, out=got, accumulate=True)
+    check_gradient(got, grad, ids, rows, 0.5, before)
+
+
+@pytest.mark.parametrize("rows,width,pad", [
+    (110_000, 2000, 0), (52_000, 2048, 8), (60_001, 4097, 3)])
+def test_gradient_into_large_results(rows, width, pad):
+    # cleared in more CTAs above 400 MB; rows side by side and apart
+    n = 3000
+    g = gen(rows)
+    room = torch.full((rows, width + pad), 7.0, dtype=torch.bfloat16, device="cuda")
+    ids = make_ids(n, rows, "far", torch.int64, g)
+    grad = torch.randint(-8, 9, (n, width), generator=g, device="cuda").bfloat16()
+    got = tbe.tbe_embed_backward(grad, ids, rows, out=room[:, :width])
+    kept = ids[(ids >= 0) & (ids < rows)]
+    some = kept.unique()
+    for row in some[:20].tolist():
+        assert torch.equal(got[row], grad[ids == row].sum(0, dtype=torch.float32).bfloat16())
+    others = torch.ones(rows, dtype=torch.bool, device="cuda")
+    others[some] = False
+    assert not bool(got[others].any()) and bool((room[:, width:] == 7).all())
+
+
 @pytest.mark.parametrize("lengths", [
     [8], [16], [24], [9], [7, 8, 9], [1, 15], [15, 1], [64, 65, 130, 1, 2, 17, 8, 8, 16, 7],
     [3, 1000, 5], [1200], [31, 33, 32]])
