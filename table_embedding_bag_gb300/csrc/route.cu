@@ -91,6 +91,12 @@ __device__ __forceinline__ float score_of(float l, bool sigmoid, float top, floa
   return sigmoid ? reciprocal_near(1.f + exp_near(-l)) : exp_near(l - top) * inverse;
 }
 
+// Score and bias, the same wherever it is formed.
+__device__ __forceinline__ float choice_of(float l, float b, bool sigmoid, float top,
+                                           float inverse) {
+  return sigmoid ? score_of(l, true, 0.f, 0.f) + b : fmaf(exp_near(l - top), inverse, b);
+}
+
 // A row's choice again in 64 bits, by the whole warp: few rows need it (see `step` below), but
 // the last of them ends the launch.  room: the row's choices as integers in their order, 0 where
 // an expert is closed.  Returns lane j's expert, -1 for none.
@@ -425,11 +431,11 @@ __global__ void __launch_bounds__(256, V <= 8 ? 5 : 1)
     if (P.sigmoid) {
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        c[v] = c[v] == kClosed ? kClosed : score_of(c[v], true, 0.f, 0.f) + b[v];
+        c[v] = c[v] == kClosed ? kClosed : choice_of(c[v], b[v], true, 0.f, 0.f);
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        c[v] = c[v] == kClosed ? kClosed : score_of(c[v], false, scale.top, inverse) + b[v];
+        c[v] = c[v] == kClosed ? kClosed : choice_of(c[v], b[v], false, scale.top, inverse);
     }
   }
   // NaN, or infinities of both signs
@@ -519,7 +525,7 @@ __global__ void __launch_bounds__(256, V <= 8 ? 5 : 1)
     // in any arithmetic
     const float b = mine >= 0 ? P.bias[mine] : 0.f;
     const float score = mine >= 0 ? score_of(chosen, P.sigmoid, scale.top, inverse) : 0.f;
-    const float s = mine >= 0 ? score + b : kClosed;
+    const float s = mine >= 0 ? choice_of(chosen, b, P.sigmoid, scale.top, inverse) : kClosed;
     const float off =
         P.sigmoid ? 0x1.1p-22f : score * (34.f + 2.f * (scale.top - chosen)) * 0x1p-24f;
     const float lp = __shfl_up_sync(kAll, chosen, 1), bp = __shfl_up_sync(kAll, b, 1);
@@ -527,7 +533,10 @@ __global__ void __launch_bounds__(256, V <= 8 ? 5 : 1)
     const auto far = [&](float more, float less, float by) {
       return more - less > by + 0x1p-23f * fmaxf(fabsf(less), fabsf(more));
     };
-    near = row_any<L>(place > 0 && place < K && mine >= 0 && !far(sp, s, off + op) &&
+    // The one past the last that is taken stands for all that are left, which are no larger here
+    // but may be off by more than it is: by half a step at most.
+    const float by = place == P.k ? op + 0.5f * step : op + off;
+    near = row_any<L>(place > 0 && place < K && mine >= 0 && !far(sp, s, by) &&
                       !(lp == chosen && bp == b)) && !unsure;
     if (__any_sync(kAll, near)) {
       // the candidates suffice where the last that is taken is above all others for certain

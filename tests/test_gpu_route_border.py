@@ -1,0 +1,48 @@
+"""Routing where fp32 does not tell the last expert that is chosen from one behind it, on the
+GPU, against the plain 64-bit form of test_gpu_route.py.
+
+Rows have one close pair, at the border, so that nothing else in them asks for exact
+arithmetic."""
+import math
+
+import pytest
+import torch
+
+from .test_gpu_route import check, gen, route64
+
+pytestmark = pytest.mark.gpu
+
+# experts and chosen ones of rows of 8, 16 and 32 lanes, in rounds and by candidates
+SIZES = [(16, 1), (16, 5), (24, 3), (33, 2), (64, 3), (64, 7), (100, 1), (128, 6), (128, 8), (96, 12),
+         (256, 1), (256, 2), (256, 8), (600, 4), (1000, 8)]
+
+
+@pytest.mark.parametrize("experts,k", SIZES)
+@pytest.mark.parametrize("place", ["first", "middle", "last"])
+def test_a_likely_expert_of_low_bias_behind_unlikely_ones(experts, k, place):
+    # Softmax.  One expert has nearly all of the score, whose error is that of the row's sum, and
+    # with its bias it comes to what the k-th choice and the next one come to, whose scores, and
+    # so whose errors, are next to nothing.
+    rows, g = 4000, gen(experts + k)
+    base = -17 + 11 * torch.rand(experts, generator=g, device="cuda", dtype=torch.float64)
+    likely = {"first": 0, "middle": experts // 2, "last": experts - 1}[place]
+    others = [e for e in range(experts) if e != likely]
+    chosen, close = others[:k - 1], others[k - 1:k + 1]
+    rest = torch.tensor(others[k + 1:], device="cuda")
+    base[rest] += math.log(0.065) - torch.logsumexp(base[rest], 0)
+    base[chosen], base[close], base[likely] = -20.0, -25.0, 0.0
+    logits = base.expand(rows, -1).clone()
+    # moves the likely expert's score by a few of its errors, either way
+    shift = 8e-6 * torch.rand(rows, 1, generator=g, device="cuda", dtype=torch.float64) - 4e-6
+    logits[:, rest] += shift
+    logits = logits.float()
+    bias = torch.full((experts,), -2.0, dtype=torch.float64, device="cuda")
+    bias[chosen] = 2.0 - 0.1 * torch.arange(k - 1, dtype=torch.float64, device="cuda")
+    bias[close] = torch.tensor([2.0 ** -6, 2.0 ** -6 - 3 * 2.0 ** -30], dtype=torch.float64, device="cuda")
+    bias[likely] = 2.0 ** -6 - torch.softmax(base.float().double(), 0)[likely]
+    bias = bias.float()
+    want, _ = route64(logits, k, bias=bias)
+    assert bool((want[:, -1] == likely).any()) and bool((want[:, -1] == close[0]).any())
+    assert bias[close[0]] > bias[close[1]]
+    check(logits, k, bias=bias)
+    check(logits, k, bias=bias, renormalize=False)
