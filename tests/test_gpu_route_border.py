@@ -20,26 +20,26 @@ SIZES = [(16, 1), (16, 5), (24, 3), (33, 2), (64, 3), (64, 7), (100, 1), (128, 6
 @pytest.mark.parametrize("experts,k", SIZES)
 @pytest.mark.parametrize("place", ["first", "middle", "last"])
 def test_a_likely_expert_of_low_bias_behind_unlikely_ones(experts, k, place):
-    # Softmax.  One expert has nearly all of the score, whose error is that of the row's sum, and
-    # with its bias it comes to what the k-th choice and the next one come to, whose scores, and
-    # so whose errors, are next to nothing.
+    # Softmax.  One expert has much of the score, with the error of the row's sum, and with its bias
+    # it comes to what the k-th choice and the next one come to, whose scores, and so whose
+    # errors, are next to nothing.
     rows, g = 4000, gen(experts + k)
-    base = -17 + 11 * torch.rand(experts, generator=g, device="cuda", dtype=torch.float64)
     likely = {"first": 0, "middle": experts // 2, "last": experts - 1}[place]
     others = [e for e in range(experts) if e != likely]
     chosen, close = others[:k - 1], others[k - 1:k + 1]
     rest = torch.tensor(others[k + 1:], device="cuda")
-    base[rest] += math.log(0.065) - torch.logsumexp(base[rest], 0)
-    base[chosen], base[close], base[likely] = -20.0, -25.0, 0.0
-    logits = base.expand(rows, -1).clone()
-    # moves the likely expert's score by a few of its errors, either way
-    shift = 8e-6 * torch.rand(rows, 1, generator=g, device="cuda", dtype=torch.float64) - 4e-6
-    logits[:, rest] += shift
-    logits = logits.float()
+    # The rest have 0.8 of the likely one's score, shared at random, so that each row's sum is
+    # rounded in its own way; and a little more or less, which moves the likely one's by a few of
+    # its errors.
+    l = 3 * torch.rand(rows, experts, generator=g, device="cuda", dtype=torch.float64)
+    l[:, rest] += math.log(0.8) - torch.logsumexp(l[:, rest], 1, keepdim=True)
+    l[:, rest] += 2e-6 * torch.rand(rows, 1, generator=g, device="cuda", dtype=torch.float64) - 1e-6
+    l[:, chosen], l[:, close], l[:, likely] = -20.0, -25.0, 0.0
+    logits = l.float()
     bias = torch.full((experts,), -2.0, dtype=torch.float64, device="cuda")
     bias[chosen] = 2.0 - 0.1 * torch.arange(k - 1, dtype=torch.float64, device="cuda")
     bias[close] = torch.tensor([2.0 ** -6, 2.0 ** -6 - 3 * 2.0 ** -30], dtype=torch.float64, device="cuda")
-    bias[likely] = 2.0 ** -6 - torch.softmax(base.float().double(), 0)[likely]
+    bias[likely] = 2.0 ** -6 - 1 / 1.8
     bias = bias.float()
     want, _ = route64(logits, k, bias=bias)
     assert bool((want[:, -1] == likely).any()) and bool((want[:, -1] == close[0]).any())
