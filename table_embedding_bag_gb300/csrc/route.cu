@@ -180,6 +180,21 @@ __device__ __noinline__ int choose_exactly(const RouteArgs& P, const T* logits,
   return mine;
 }
 
+// Whether a row of L lanes has an expert whose choice may be the one of logit l and bias b, which
+// is `last`, without being the same logit and bias.  by: what the errors of both come to at most.
+template <typename T, int L>
+__device__ __noinline__ bool others_near(const RouteArgs& P, const T* logits, float l, float b,
+                                         float last, float by, float top, float inverse) {
+  bool found = false;
+  for (int e = threadIdx.x & (L - 1); e < P.experts; e += L) {
+    const float le = to_f32(logits[e]), be = P.bias[e];
+    const float s = le == kClosed ? kClosed : choice_of(le, be, P.sigmoid, top, inverse);
+    found |= s != kClosed && !(le == l && be == b) &&
+             !(fabsf(last - s) > by + 0x1p-23f * fmaxf(fabsf(last), fabsf(s)));
+  }
+  return row_any<L>(found);
+}
+
 // The candidates of rows of L lanes, lane j with expert `mine` (-1: none) of logit l and bias b,
 // put in the order of their sigmoid choices in 64 bits.  room: 32 entries.
 template <int L>
@@ -521,8 +536,8 @@ __global__ void __launch_bounds__(256, V <= 8 ? 5 : 1)
   if (in_rounds) mine = choose_in_rounds<V, L>(c, e0, K);
   float chosen = mine >= 0 ? to_f32(logits[mine]) : 0.f;
   if (!P.by_logits) {
-    // neighbours in the order that fp32 does not tell apart; the same logit and bias tie
-    // in any arithmetic
+    // neighbours in the order that fp32 does not tell apart; the same logit and bias tie in any
+    // arithmetic
     const float b = mine >= 0 ? P.bias[mine] : 0.f;
     const float score = mine >= 0 ? score_of(chosen, P.sigmoid, scale.top, inverse) : 0.f;
     const float s = mine >= 0 ? choice_of(chosen, b, P.sigmoid, scale.top, inverse) : kClosed;
@@ -536,8 +551,19 @@ __global__ void __launch_bounds__(256, V <= 8 ? 5 : 1)
     // The one past the last that is taken stands for all that are left, which are no larger here
     // but may be off by more than it is: by half a step at most.
     const float by = place == P.k ? op + 0.5f * step : op + off;
-    near = row_any<L>(place > 0 && place < K && mine >= 0 && !far(sp, s, by) &&
-                      !(lp == chosen && bp == b)) && !unsure;
+    const bool close = place > 0 && place < K && mine >= 0 && !far(sp, s, by);
+    const bool alike = lp == chosen && bp == b;
+    near = row_any<L>(close && !alike) && !unsure;
+    // Where the last that is taken and the one past it are alike, that one does not stand for those
+    // behind it.
+    const bool hidden = close && alike && place == P.k;
+    if (__any_sync(kAll, hidden)) {
+      const int edge = (lane & ~(L - 1)) + P.k;
+      const float l = __shfl_sync(kAll, chosen, edge), bias = __shfl_sync(kAll, b, edge);
+      const float last = __shfl_sync(kAll, s, edge), width = __shfl_sync(kAll, by, edge);
+      const bool others = others_near<T, L>(P, logits, l, bias, last, width, scale.top, inverse);
+      near |= row_any<L>(hidden) && others && !unsure;
+    }
     if (__any_sync(kAll, near)) {
       // the candidates suffice where the last that is taken is above all others for certain
       const int edge = (lane & ~(L - 1)) + P.k - 1;

@@ -46,3 +46,52 @@ def test_a_likely_expert_of_low_bias_behind_unlikely_ones(experts, k, place):
     assert bias[close[0]] > bias[close[1]]
     check(logits, k, bias=bias)
     check(logits, k, bias=bias, renormalize=False)
+
+
+@pytest.mark.parametrize("experts,k", SIZES)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("kinds", [1, 2, 3])
+def test_experts_alike_at_the_border(experts, k, score, kinds):
+    # The k-th choice and the next one have the same logit and bias, and behind them stand
+    # choices that fp32 holds to be the same, or next to it, and that are larger.  Biases below a
+    # half whose sums with the score are above it, where fp32's steps are twice as wide.
+    rows, g = 3000, gen(experts * k + kinds)
+    low = 0.5 - 2.0 ** -23
+    kind = torch.randint(0, kinds, (experts,), generator=g, device="cuda")
+    bias = torch.tensor([low, low + 2.0 ** -25, low - 2.0 ** -24], device="cuda")[kind]
+    alike = torch.tensor([0.0, 0.0, 1.25 * 2.0 ** -22], device="cuda")[kind]
+    assert kinds == 1 or bias.unique().numel() > 1
+    # by chance some are chosen for certain, some are alike and the others far behind
+    chance = torch.rand(rows, experts, generator=g, device="cuda")
+    sure = max(k - 2, 0) / experts
+    logits = torch.where(chance < sure + 4 / experts, alike, -4.0)
+    certain = 4 + 0.125 * torch.arange(experts, device="cuda") % 8
+    logits = torch.where(chance < sure, certain, logits)
+    check(logits, k, score=score, bias=bias)
+    if kinds < 3:
+        check(logits.bfloat16(), k, score=score, bias=bias)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts", [3, 64, 128, 256])
+def test_an_expert_behind_two_alike(score, experts):
+    # the smallest case: of the first three the last is ahead, by less than fp32 holds
+    logits = torch.full((5, experts), -30.0, device="cuda")
+    logits[:, :3] = 0.0
+    bias = torch.zeros(experts, device="cuda")
+    bias[:3] = 0.5 - 2.0 ** -23
+    bias[2] += 2.0 ** -25
+    assert check(logits, 1, score=score, bias=bias)[0].tolist() == [[2]] * 5
+    assert check(logits, 2, score=score, bias=bias)[0].tolist() == [[2, 0]] * 5
+
+
+@pytest.mark.parametrize("experts,k", SIZES)
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_coarse_logits_with_stepped_biases(experts, k, dtype):
+    # as a rule of balance leaves them: biases that rose and fell by one step a time
+    g = gen(experts - k)
+    logits = (0.5 * torch.randn(2000, experts, generator=g, device="cuda")).to(dtype)
+    steps = torch.randint(-3, 4, (experts,), generator=g, device="cuda")
+    for score in ("softmax", "sigmoid"):
+        check(logits, k, score=score, bias=1e-3 * steps.float())
+        check(logits, k, score=score, bias=2.0 ** -24 * steps.float())
