@@ -541,8 +541,9 @@ __global__ void __launch_bounds__(256, V <= 8 ? 5 : 1)
     const float b = mine >= 0 ? P.bias[mine] : 0.f;
     const float score = mine >= 0 ? score_of(chosen, P.sigmoid, scale.top, inverse) : 0.f;
     const float s = mine >= 0 ? choice_of(chosen, b, P.sigmoid, scale.top, inverse) : kClosed;
-    const float off =
-        P.sigmoid ? 0x1.1p-22f : score * (34.f + 2.f * (scale.top - chosen)) * 0x1p-24f;
+    // (softmax: and by what the exponential drops below 2^-126)
+    const float off = P.sigmoid ? 0x1.1p-22f
+                                : fmaf(score * 0x1p-24f, 34.f + 2.f * (scale.top - chosen), 0x1p-125f);
     const float lp = __shfl_up_sync(kAll, chosen, 1), bp = __shfl_up_sync(kAll, b, 1);
     const float sp = __shfl_up_sync(kAll, s, 1), op = __shfl_up_sync(kAll, off, 1);
     const auto far = [&](float more, float less, float by) {

@@ -95,3 +95,20 @@ def test_coarse_logits_with_stepped_biases(experts, k, dtype):
     for score in ("softmax", "sigmoid"):
         check(logits, k, score=score, bias=1e-3 * steps.float())
         check(logits, k, score=score, bias=2.0 ** -24 * steps.float())
+
+
+@pytest.mark.parametrize("experts", [12, 64, 128, 256])
+def test_scores_at_the_end_of_fp32(experts):
+    # softmax scores around 2^-126, one of which an approximate exponential may hold to be zero,
+    # with biases that are as small
+    end = 126 * math.log(2.0)
+    for places in (1, 2, 3):
+        logits = torch.full((15, experts), -math.inf, device="cuda")
+        logits[:, 0] = 0.0
+        first = -end + 2.0 ** -17 * (torch.arange(15, device="cuda") - 7).double()
+        logits[:, 5] = first.float()
+        logits[:, 7] = logits[:, 5] - places * 2.0 ** -17
+        bias = torch.zeros(experts, dtype=torch.float64, device="cuda")
+        bias[7] = (places + 0.5) * 2.0 ** -143  # a half more than what the score is less
+        for k in (1, 2, 3):
+            check(logits, k, bias=bias.float())
