@@ -218,28 +218,30 @@ __device__ __noinline__ int order_exactly(int mine, float l, float b, int* room)
   return mine;
 }
 
+// sigmoid(x), to fp32's end at both sides.
+__device__ __forceinline__ float logistic(float x) {
+  const float e = expf(-fabsf(x));
+  return __fdiv_rn(x < 0.f ? e : 1.f, 1.f + e);
+}
+
 // Weights of the chosen, before the scale: lane j of a row has the j-th expert's logit, `on`
-// where there is one.  kNear: by the approximate functions, off by 4 + 1.6 |x| units of 2^-24.
-template <int L, bool kNear>
+// where there is one.  By expf and rounded divisions, in both directions: an expert is chosen by
+// approximate scores only where their errors do not matter, but its weight is a result.
+template <int L>
 __device__ __forceinline__ float weight_of(float l, bool on, bool sigmoid, bool renormalize,
                                            RowScale r) {
-  const auto power = [](float x) { return kNear ? exp_near(x) : expf(x); };
-  const auto ratio = [](float p, float q) { return kNear ? __fdividef(p, q) : __fdiv_rn(p, q); };
-  const auto logistic = [&](float x) {
-    return kNear ? reciprocal_near(1.f + exp_near(-x)) : __fdiv_rn(1.f, 1.f + expf(-x));
-  };
   if (!renormalize) {
     if (!on) return 0.f;
-    return sigmoid ? logistic(l) : ratio(power(l - r.top), r.sum);
+    return sigmoid ? logistic(l) : __fdiv_rn(expf(l - r.top), r.sum);
   }
   const float top = row_max<L>(on ? l : kClosed);
   // sigmoid(l) is exp(l) to the last bit where no logit is above -60, and exp(l - top) does not
   // underflow
-  const float p = !on ? 0.f : sigmoid && !(top < -60.f) ? logistic(l) : power(l - top);
+  const float p = !on ? 0.f : sigmoid && !(top < -60.f) ? logistic(l) : expf(l - top);
   const float sum = row_sum<L>(p);
   if (!on) return 0.f;
   // a NaN among the row's scores makes every softmax weight one
-  return !sigmoid && r.sum != r.sum ? r.sum : ratio(p, sum);
+  return !sigmoid && r.sum != r.sum ? r.sum : __fdiv_rn(p, sum);
 }
 
 // The K experts with the largest choices, in their order: lane j of a row gets the j-th (-1 for
@@ -419,7 +421,8 @@ __global__ void __launch_bounds__(256, V <= 8 ? 5 : 1)
     scale.top = row_max<L>(top);
     float part[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) part[v] = exp_near(c[v] - scale.top);
+    for (int v = 0; v < V; ++v)  // of weights, not only of choices, where they are not renormalised
+      part[v] = P.renormalize ? exp_near(c[v] - scale.top) : expf(c[v] - scale.top);
 #pragma unroll
     for (int o = V / 2; o; o >>= 1)
 #pragma unroll
@@ -594,7 +597,7 @@ __global__ void __launch_bounds__(256, V <= 8 ? 5 : 1)
     chosen = mine >= 0 ? to_f32(logits[mine]) : 0.f;
   }
   if (place >= P.k) mine = -1;  // the one past the last
-  const float w = weight_of<L, true>(chosen, mine >= 0, P.sigmoid, P.renormalize, scale);
+  const float w = weight_of<L>(chosen, mine >= 0, P.sigmoid, P.renormalize, scale);
   if (place < P.k && live) {
     const int64_t at = token * P.k + place;
     if (P.wide_ids) static_cast<int64_t*>(P.ids)[at] = mine;
@@ -661,7 +664,7 @@ __global__ void __launch_bounds__(256)
     for (int i = place; i < experts; i += L) sum += expf(to_f32(logits[i]) - scale.top);
     scale.sum = row_sum<L>(sum);
   }
-  const float p = weight_of<L, false>(l, on, P.sigmoid, P.renormalize, scale);
+  const float p = weight_of<L>(l, on, P.sigmoid, P.renormalize, scale);
   const float mean = P.sigmoid && !P.renormalize ? 0.f : row_sum<L>(g * p);
   if (whole)
     fill([&](int i) {  // zeros where every expert is closed
@@ -687,7 +690,7 @@ __global__ void __launch_bounds__(256)
   } else {
     // as many times the mean as the expert is named
     d = p * (of_score - static_cast<float>(__popc(same)) * mean);
-    if (P.sigmoid) d *= __fdiv_rn(1.f, 1.f + expf(l));  // 1 - sigmoid(l)
+    if (P.sigmoid) d *= logistic(-l);  // 1 - sigmoid(l)
   }
   __syncwarp();
   if (on && first) grad[e] = from_f32<T>(d);
