@@ -646,8 +646,11 @@ template <typename Args>
 tbe_status launch_norm(void (*kernel)(Args), const Args& args, const Shape& s, int64_t ctas,
                        int bytes, void* stream) {
   const int smem = bytes * s.threads * s.rows;
-  if (smem > 40 * 1024 &&  // beside what is declared in the kernels
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+  // What is asked for is the kernel's and not the launch's: as much for every launch of it, so that
+  // none takes from another, which a second host thread may be about to make or a graph holds.
+  const int most = bytes * kNormThreads;
+  if (most > 40 * 1024 &&  // beside what is declared in the kernels
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) !=
           cudaSuccess)
     return TBE_ECUDA;
   kernel<<<static_cast<unsigned>(ctas), dim3(s.threads, s.rows), smem,
