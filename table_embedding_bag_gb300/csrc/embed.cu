@@ -736,11 +736,14 @@ bool check_ids(const void* ids, int32_t dtype, int64_t tokens) {
   return !tokens || (ids && aligned_to(ids, dtype == TBE_DT_I32 ? 4 : 8));
 }
 
-cudaError_t room_for(const void* kernel, size_t smem) {
-  return smem <= 40 * 1024 ? cudaSuccess  // beside what is declared in the kernels
+// Room for a kernel's launches in shared memory; most: of the largest of them.  It belongs to the
+// kernel, so a launch that asked for its own size could take from another, which a second host
+// thread may be about to make or a graph holds.
+cudaError_t room_for(const void* kernel, size_t most) {
+  return most <= 40 * 1024 ? cudaSuccess  // beside what is declared in the kernels
                            : cudaFuncSetAttribute(kernel,
                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                  static_cast<int>(smem));
+                                                  static_cast<int>(most));
 }
 
 template <typename IdT>
@@ -796,12 +799,12 @@ tbe_status sort_in_grid(const IdT* ids, const SortPlan& plan, int* totals, int* 
   return st;
 }
 
-// A launch; with `beside` it may begin before the kernel ahead of it ends, and waits for that one's
-// results itself.
+// A launch with `smem` bytes of the `most` that the kernel is ever launched with; with `beside` it
+// may begin before the kernel ahead of it ends, and waits for that one's results itself.
 template <typename... Args>
-tbe_status launch(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, bool beside,
-                  cudaStream_t s, std::common_type_t<Args>... args) {
-  if (room_for(reinterpret_cast<const void*>(kernel), smem) != cudaSuccess) return TBE_ECUDA;
+tbe_status launch(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, size_t most,
+                  bool beside, cudaStream_t s, std::common_type_t<Args>... args) {
+  if (room_for(reinterpret_cast<const void*>(kernel), most) != cudaSuccess) return TBE_ECUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
@@ -833,7 +836,8 @@ tbe_status clear(void* p, int64_t rows, int64_t width, int64_t stride, int bytes
   }
   const int per_sm = beside && rows * row < (400 << 20) ? 6 : 16;
   return launch(clear_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(rows, 152 * per_sm))),
-                kMoveThreads, 0, beside, s, static_cast<char*>(p), rows, row, pitch, last, bytes);
+                kMoveThreads, 0, 0, beside, s, static_cast<char*>(p), rows, row, pitch, last,
+                bytes);
 }
 
 }  // namespace
@@ -953,8 +957,9 @@ extern "C" tbe_status tbe_embed_backward(const void* grad_out, int32_t dtype, in
         const int64_t ranges = accumulate ? 0 : (rows + few.range - 1) / few.range;
         const dim3 grid(static_cast<unsigned>(tokens + (ranges + slices - 1) / slices),
                         static_cast<unsigned>(slices));
-        return launch(embed_few_kernel<T, O, IdT, kAligned>, grid, kMoveThreads,
-                      kMoveThreads * kVec<T> * sizeof(float), false, s, few, lg);
+        constexpr size_t kSums = kMoveThreads * kVec<T> * sizeof(float);
+        return launch(embed_few_kernel<T, O, IdT, kAligned>, grid, kMoveThreads, kSums, kSums, false,
+                      s, few, lg);
       };
       return index_dtype == TBE_DT_I32 ? go(static_cast<const int32_t*>(ids))
                                        : go(static_cast<const int64_t*>(ids));
@@ -996,13 +1001,14 @@ extern "C" tbe_status tbe_embed_backward(const void* grad_out, int32_t dtype, in
     const int per = kMoveThreads >> lg;
     const dim3 grid(static_cast<unsigned>((pieces + per - 1) / per),
                     static_cast<unsigned>((places + (1 << lg) - 1) >> lg));
-    const size_t smem = RowsAhead<T, kAligned>::kBytes * kMoveThreads +
-                        ((per + 2) * piece + 2) * sizeof(Item);
+    constexpr size_t kRing = RowsAhead<T, kAligned>::kBytes * kMoveThreads;
+    const size_t smem = kRing + ((per + 2) * piece + 2) * sizeof(Item);
+    constexpr size_t kMostSmem = kRing + ((kMoveThreads + 2) * kMostPiece + 2) * sizeof(Item);
     const tbe_status summed = launch(embed_sum_kernel<T, O, kAligned>, grid, kMoveThreads, smem,
-                                     true, s, args, lg);
+                                     kMostSmem, true, s, args, lg);
     if (summed != TBE_OK || pieces < 3) return summed;  // no run is long
     const dim3 joins(static_cast<unsigned>((pieces + join - 1) / join),
                      static_cast<unsigned>(slices));
-    return launch(embed_join_kernel<O>, joins, kJoinLanes * kJoinSegments, 0, true, s, args);
+    return launch(embed_join_kernel<O>, joins, kJoinLanes * kJoinSegments, 0, 0, true, s, args);
   });
 }

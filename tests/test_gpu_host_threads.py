@@ -11,7 +11,7 @@ import table_embedding_bag_gb300 as tbe
 pytestmark = pytest.mark.gpu
 
 
-BF16 = 4
+BF16, I64 = 4, 3
 
 
 def at_once(calls, rounds=12000):
@@ -67,8 +67,20 @@ def norm(width):
     return call, y, want, (x, res, h)
 
 
+def embedding_gradient(width):
+    # 41 and 49 KB: a ring, and the items of as many pieces as a CTA has groups of threads
+    n, rows = 2000, 300
+    grad, ids = randn(n, width).bfloat16(), torch.arange(n, device="cuda") * 7919 % rows
+    out = torch.empty(rows, width, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(tbe.tbe_embed_workspace_size(n, rows, width), dtype=torch.uint8, device="cuda")
+    want = tbe.tbe_embed_backward(grad, ids, rows)
+    call = bound("tbe_embed_backward", grad.data_ptr(), BF16, n, width, width, ids.data_ptr(), I64,
+                 rows, 1.0, 0, out.data_ptr(), BF16, width, ws.data_ptr(), ws.numel())
+    return call, out, want, (grad, ids, ws)
+
+
 @pytest.mark.parametrize("make,widths", [
-    (norm_gradient, (8192, 6144)), (norm, (16384, 8192))])
+    (norm_gradient, (8192, 6144)), (norm, (16384, 8192)), (embedding_gradient, (8, 16))])
 def test_calls_of_two_sizes_at_once(make, widths):
     made = [make(w) for w in widths]
     assert at_once([m[0] for m in made]) == {tbe.TBE_OK}
@@ -76,7 +88,7 @@ def test_calls_of_two_sizes_at_once(make, widths):
 
 
 @pytest.mark.parametrize("make,large,small", [
-    (norm_gradient, 8192, 6144), (norm, 16384, 8192)])
+    (norm_gradient, 8192, 6144), (norm, 16384, 8192), (embedding_gradient, 8, 16)])
 def test_a_graph_outlives_smaller_calls(make, large, small):
     big, little = make(large), make(small)
     stream = torch.cuda.Stream()
