@@ -767,7 +767,7 @@ tbe_status sort_in_cluster(const IdT* ids, const SortPlan& plan, cudaStream_t s)
       (ctas > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed,
                                         1) != cudaSuccess) ||
       cudaLaunchKernelEx(&cfg, kernel, ids, plan) != cudaSuccess)
-    return TBE_ECUDA;
+    return refused();
   return launched();
 }
 
@@ -780,7 +780,7 @@ tbe_status sort_pass(const Source& from, const SortPlan& plan, int p, int* total
   const size_t most = static_cast<size_t>(kSortWarps + 1) * 4 << kDigitBits;
   if (room_for(reinterpret_cast<const void*>(token_count_kernel<Source>), most) != cudaSuccess ||
       room_for(reinterpret_cast<const void*>(token_place_kernel<Source>), most) != cudaSuccess)
-    return TBE_ECUDA;
+    return refused();
   token_count_kernel<Source><<<ctas, kSortWarps * 32, smem, s>>>(from, plan.n, d, totals);
   note_launch();
   token_scan_kernel<<<(buckets + 7) / 8, 256, 0, s>>>(totals, ctas, buckets, sums);
@@ -804,7 +804,7 @@ tbe_status sort_in_grid(const IdT* ids, const SortPlan& plan, int* totals, int* 
 template <typename... Args>
 tbe_status launch(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, size_t most,
                   bool beside, cudaStream_t s, std::common_type_t<Args>... args) {
-  if (room_for(reinterpret_cast<const void*>(kernel), most) != cudaSuccess) return TBE_ECUDA;
+  if (room_for(reinterpret_cast<const void*>(kernel), most) != cudaSuccess) return refused();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
@@ -815,7 +815,7 @@ tbe_status launch(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = beside ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return TBE_ECUDA;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return refused();
   note_launch();
   return TBE_OK;
 }

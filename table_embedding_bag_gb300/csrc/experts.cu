@@ -598,14 +598,14 @@ extern "C" tbe_status tbe_expert_sort(const void* ids, int32_t index_dtype, int6
     if (!room_for(kernel) ||
         (ctas > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed,
                                           1) != cudaSuccess))
-      return TBE_ECUDA;
+      return refused();
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.numAttrs = ctas > 1 ? 1 : 0;
     if (cudaLaunchKernelEx(&cfg, kernel, p, n, experts, offsets, source, position) != cudaSuccess)
-      return TBE_ECUDA;
+      return refused();
     return launched();
   };
   const auto three_launches = [&](auto* p) {
@@ -613,7 +613,7 @@ extern "C" tbe_status tbe_expert_sort(const void* ids, int32_t index_dtype, int6
     const int ctas = n / kSortGridChunk < kSortGridCtas ? n / kSortGridChunk : kSortGridCtas;
     const auto count = expert_count_kernel<IdT>;
     const auto rank = expert_rank_kernel<IdT>;
-    if (!room_for(count) || !room_for(rank)) return TBE_ECUDA;
+    if (!room_for(count) || !room_for(rank)) return refused();
     const int scan_ctas = experts < 256 ? 1 : kScanCtas;
     const int share = (experts + scan_ctas) / scan_ctas;  // of the E + 1 buckets
     int segments = 1;
@@ -621,7 +621,7 @@ extern "C" tbe_status tbe_expert_sort(const void* ids, int32_t index_dtype, int6
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.numAttrs = 0;
     if (cudaLaunchKernelEx(&cfg, count, p, n, experts, position) != cudaSuccess)
-      return TBE_ECUDA;
+      return refused();
     note_launch();
     // the next two begin while the launch before them ends (griddepcontrol.wait)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -634,13 +634,13 @@ extern "C" tbe_status tbe_expert_sort(const void* ids, int32_t index_dtype, int6
     cfg.dynamicSmemBytes = 0;
     if (cudaLaunchKernelEx(&cfg, expert_scan_kernel, n, experts, ctas, share, segments, offsets,
                            position) != cudaSuccess)
-      return TBE_ECUDA;
+      return refused();
     cfg.numAttrs = 1;
     note_launch();
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.dynamicSmemBytes = smem;
     if (cudaLaunchKernelEx(&cfg, rank, p, n, experts, source, position) != cudaSuccess)
-      return TBE_ECUDA;
+      return refused();
     return launched();
   };
   const auto go = [&](auto* p) { return n <= kSortOneLaunch ? one_launch(p) : three_launches(p); };

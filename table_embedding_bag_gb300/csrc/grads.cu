@@ -294,7 +294,7 @@ tbe_status launch_after(void (*kernel)(Args...), int ctas, cudaStream_t s,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return TBE_ECUDA;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return refused();
   note_launch();
   return TBE_OK;
 }

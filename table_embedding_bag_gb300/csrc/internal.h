@@ -14,6 +14,13 @@ struct WsLayout;
 // Counts one kernel launch (read back by tbe_kernel_launches).
 void note_launch();
 
+// The status of a call whose runtime call failed.  Takes the error off the host thread, where the
+// next call would find it, which asks for the last error after its launch.
+inline tbe_status refused() {
+  cudaGetLastError();
+  return TBE_ECUDA;
+}
+
 // Kernel probe (tbe_probe_set): events around launches of the selected kernel.
 void probe_begin(uint32_t kernel, cudaStream_t s);
 void probe_end(uint32_t kernel, cudaStream_t s);

@@ -96,7 +96,7 @@ extern "C" tbe_status tbe_backward_rowwise_adagrad_noalloc(
                                            (mean ? TBE_WS_MEAN : 0u), /*allow_hot=*/false);
   if (W.total > TBE_NOALLOC_SCRATCH_BYTES) return TBE_ETOO_LARGE;
   char* scratch = scratch_ptr();
-  if (!scratch) return TBE_ECUDA;
+  if (!scratch) return refused();
   const Launch L{d, n, static_cast<cudaStream_t>(stream), sm_count()};
   // Each call stands alone: the hot-row set is cleared (the path is off, so
   // nothing reads it, but no stale set is kept), and everything else the
@@ -105,19 +105,19 @@ extern "C" tbe_status tbe_backward_rowwise_adagrad_noalloc(
   // because bounds reporting is not offered here.
   if (cudaMemsetAsync(scratch + W.hot_n(W.hot_next), 0, static_cast<size_t>(d->T) * sizeof(uint32_t),
                       L.s) != cudaSuccess)
-    return TBE_ECUDA;
+    return refused();
   cudaError_t e = launch_preprocess(L, W, scratch, indices, offsets, per_sample_weights, false);
-  if (e != cudaSuccess) return TBE_ECUDA;
+  if (e != cudaSuccess) return refused();
   if (mean) {
     float* inv_len = reinterpret_cast<float*>(scratch + W.inv_len);
     float* scaled = reinterpret_cast<float*>(scratch + W.grad_mean);
     e = launch_mean_factors(L, offsets, inv_len);
-    if (e != cudaSuccess) return TBE_ECUDA;
+    if (e != cudaSuccess) return refused();
     e = launch_scale_grad(L, grad_out, inv_len, scaled);
-    if (e != cudaSuccess) return TBE_ECUDA;
+    if (e != cudaSuccess) return refused();
     grad_out = scaled;
   }
   e = launch_update(L, W, scratch, grad_out, weights, momentum, lr, eps,
                     (flags & TBE_F_LONG_TWO_LAUNCH) != 0, elementwise);
-  return e == cudaSuccess ? TBE_OK : TBE_ECUDA;
+  return e == cudaSuccess ? TBE_OK : refused();
 }

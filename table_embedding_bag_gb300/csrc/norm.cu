@@ -639,7 +639,9 @@ int64_t ctas_of(const Shape& s, int64_t rows, int bytes, int registers, int alik
 template <typename Args>
 int registers_of(void (*kernel)(Args)) {
   cudaFuncAttributes a;
-  return cudaFuncGetAttributes(&a, kernel) == cudaSuccess ? a.numRegs : 128;
+  if (cudaFuncGetAttributes(&a, kernel) == cudaSuccess) return a.numRegs;
+  cudaGetLastError();
+  return 128;
 }
 
 template <typename Args>
@@ -652,7 +654,7 @@ tbe_status launch_norm(void (*kernel)(Args), const Args& args, const Shape& s, i
   if (most > 40 * 1024 &&  // beside what is declared in the kernels
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) !=
           cudaSuccess)
-    return TBE_ECUDA;
+    return refused();
   kernel<<<static_cast<unsigned>(ctas), dim3(s.threads, s.rows), smem,
            static_cast<cudaStream_t>(stream)>>>(args);
   return launched();

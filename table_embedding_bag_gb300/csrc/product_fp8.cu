@@ -1227,7 +1227,7 @@ extern "C" tbe_status tbe_expert_product(const uint8_t* a, int64_t a_stride, con
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return TBE_ECUDA;
+    return refused();
   ProductArgs P;
   P.a_scale = a_scale;
   P.w_scale = w_scale;
@@ -1246,9 +1246,9 @@ extern "C" tbe_status tbe_expert_product(const uint8_t* a, int64_t a_stride, con
   CUtensorMap a_map, a_part_map;
   if (!make_map(&a_map, a, 1, rows, k, a_stride, kTileM) ||
       !make_map(&a_part_map, a, 1, rows, k, a_stride, kRowBox))
-    return TBE_ECUDA;
+    return refused();
   CUtensorMap out_map = a_map;  // not used unless P.tma_out
-  if (P.tma_out && !make_map(&out_map, out, ob, rows, n, out_stride * ob, 32)) return TBE_ECUDA;
+  if (P.tma_out && !make_map(&out_map, out, ob, rows, n, out_stride * ob, 32)) return refused();
   const auto launch = [&](auto t, auto tile_n, auto share, int cluster) -> tbe_status {
     using T = decltype(t);
     constexpr int kTileN = decltype(tile_n)::value;
@@ -1257,12 +1257,12 @@ extern "C" tbe_status tbe_expert_product(const uint8_t* a, int64_t a_stride, con
     P.n_tiles = static_cast<int>((n + kTileN - 1) / kTileN);
     CUtensorMap w_map;
     if (!make_map(&w_map, w, 1, static_cast<int64_t>(experts) * n, k, k, Shape::kWRows))
-      return TBE_ECUDA;
+      return refused();
     const auto kernel = product_kernel<T, kTileN, kShare>;
     constexpr int kSmem = Shape::kSmem;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
         cudaSuccess)
-      return TBE_ECUDA;
+      return refused();
     P.row_tiles = static_cast<int>(most_row_tiles(rows, experts, Shape::kTileRows));
     const int64_t most = static_cast<int64_t>(P.row_tiles) * P.n_tiles;
     if (most > INT32_MAX / 8) return TBE_EUNSUPPORTED;  // the kernel counts tiles in 32 bits
@@ -1283,7 +1283,7 @@ extern "C" tbe_status tbe_expert_product(const uint8_t* a, int64_t a_stride, con
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, kernel, a_map, a_part_map, w_map, out_map, P) != cudaSuccess)
-      return TBE_ECUDA;
+      return refused();
     return launched();
   };
   using Narrow = std::integral_constant<int, 128>;

@@ -253,7 +253,7 @@ int device_sms() {
   return sms[dev];
 }
 
-tbe_status from_cuda(cudaError_t e) { return e == cudaSuccess ? TBE_OK : TBE_ECUDA; }
+tbe_status from_cuda(cudaError_t e) { return e == cudaSuccess ? TBE_OK : refused(); }
 
 // Offsets check / repair shared by every entry point.  Returns the offsets
 // pointer the kernels should read.
@@ -266,7 +266,7 @@ tbe_status run_checks(const Launch& L, const WsLayout& W, char* ws, const void* 
   const bool repair = (flags & TBE_F_REPAIR_OFFSETS) != 0;
   cudaError_t e = launch_check_offsets(L, offsets, repair, ws + W.offsets_fix,
                                        reinterpret_cast<int64_t*>(ws + W.fix_scratch), *status);
-  if (e != cudaSuccess) return TBE_ECUDA;
+  if (e != cudaSuccess) return refused();
   if (repair) *offsets_eff = ws + W.offsets_fix;
   return TBE_OK;
 }
@@ -439,7 +439,7 @@ tbe_status tbe_read_status(void* workspace, void* stream, int32_t* status_bits) 
     e = cudaMemcpyAsync(&v, workspace, sizeof(int32_t), cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e == cudaSuccess) e = cudaMemsetAsync(workspace, 0, sizeof(int32_t), s);
-  if (e != cudaSuccess) return TBE_ECUDA;
+  if (e != cudaSuccess) return refused();
   *status_bits = v;
   return TBE_OK;
 }
@@ -462,9 +462,9 @@ tbe_status tbe_probe_read(uint32_t* launches, float* total_ms) {
   float sum = 0.f;
   for (int i = 0; i < tbe::g_probe_used; ++i) {
     float ms = 0.f;
-    if (cudaEventSynchronize(tbe::g_probe_ev[i][1]) != cudaSuccess) return TBE_ECUDA;
+    if (cudaEventSynchronize(tbe::g_probe_ev[i][1]) != cudaSuccess) return refused();
     if (cudaEventElapsedTime(&ms, tbe::g_probe_ev[i][0], tbe::g_probe_ev[i][1]) != cudaSuccess)
-      return TBE_ECUDA;
+      return refused();
     sum += ms;
   }
   *launches = static_cast<uint32_t>(tbe::g_probe_used);
