@@ -35,6 +35,8 @@
 //    (exact) as the bags' partial sums.
 // On an mbarrier time-out the CTA records TBE_ERR_TIMEOUT, drains its MMAs
 // (bounded), frees its tensor memory and stops.
+#include <mutex>
+
 #include "common.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
@@ -615,6 +617,75 @@ __global__ void __launch_bounds__(kBThreads, 1)
   if (warp == 0) tmem_dealloc(tmem, 2 * tmem_cols);
 }
 
+// A call's byte-tile launch: one CTA per SM, as many ring stages as shared memory holds, the
+// transpose buffer when at least two stages fit beside it.
+struct BytesShape {
+  bool xpose;
+  int stages;
+  size_t smem;
+};
+BytesShape bytes_shape(int n_max, size_t optin) {
+  BytesShape b;
+  b.xpose = fwd_bytes_smem_bytes(n_max, 2, true) <= optin;
+  b.stages = kBMaxStages;
+  while (b.stages > 1 && fwd_bytes_smem_bytes(n_max, b.stages, b.xpose) > optin) --b.stages;
+  b.smem = fwd_bytes_smem_bytes(n_max, b.stages, b.xpose);
+  return b;
+}
+
+// The current device's shared memory, per CTA and per SM, and the kernels' set-up there, made by
+// the first call: each kernel may use as much as its largest launch does.  That belongs to the
+// kernel, so a call that asked for its own size could take from another host thread's.
+struct HotLimits {
+  size_t optin, per_sm;
+};
+cudaError_t hot_limits(HotLimits* out) {
+  static std::mutex mu;
+  static HotLimits made[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  const std::lock_guard<std::mutex> lk(mu);
+  if (!made[dev].optin) {
+    int optin = 0, per_sm = 0;
+    e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e != cudaSuccess) return e;
+    e = cudaDeviceGetAttribute(&per_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
+    if (e != cudaSuccess) return e;
+    for (const void* k : {reinterpret_cast<const void*>(forward_hot_kernel<true>),
+                          reinterpret_cast<const void*>(forward_hot_kernel<false>)}) {
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(fwd_hot_smem_bytes(kHotMaxD)));
+      if (e != cudaSuccess) return e;
+      // all of the unified L1 / shared storage as shared memory, so that two
+      // CTAs fit when the operands allow
+      e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+      if (e != cudaSuccess) return e;
+    }
+    size_t most[2] = {};  // without the transpose buffer and with it
+    for (int n = 16; n <= kHotMaxD; n += 16) {
+      const BytesShape b = bytes_shape(n, static_cast<size_t>(optin));
+      if (b.smem > most[b.xpose]) most[b.xpose] = b.smem;
+    }
+    const void* bytes[2][2] = {{reinterpret_cast<const void*>(forward_bytes_kernel<false, true>),
+                                reinterpret_cast<const void*>(forward_bytes_kernel<false, false>)},
+                               {reinterpret_cast<const void*>(forward_bytes_kernel<true, true>),
+                                reinterpret_cast<const void*>(forward_bytes_kernel<true, false>)}};
+    for (int x = 0; x < 2; ++x)
+      for (const void* k : bytes[x]) {
+        if (!most[x]) continue;
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(most[x]));
+        if (e != cudaSuccess) return e;
+      }
+    made[dev] = {static_cast<size_t>(optin), static_cast<size_t>(per_sm)};
+  }
+  *out = made[dev];
+  return cudaSuccess;
+}
+
 }  // namespace
 
 cudaError_t launch_forward_hot(const Launch& L, const WsLayout& W, char* ws, const void* weights,
@@ -646,75 +717,29 @@ cudaError_t launch_forward_hot(const Launch& L, const WsLayout& W, char* ws, con
     const size_t smem = fwd_hot_smem_bytes(a.n_max);
 
     const bool bf16 = d->weights_dtype == TBE_DT_BF16;
-    const int ti = bf16 ? 1 : 0;  // weight type: index of the per-type attribute caches
-    const void* hot_k = bf16 ? reinterpret_cast<const void*>(forward_hot_kernel<true>)
-                             : reinterpret_cast<const void*>(forward_hot_kernel<false>);
-    static size_t attr_bytes[64][2] = {};
-    static int ctas_per_sm[64][2] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    HotLimits limits;
+    cudaError_t e = hot_limits(&limits);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (attr_bytes[dev][ti] != smem) {
-      e = cudaFuncSetAttribute(hot_k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(smem));
-      if (e != cudaSuccess) return e;
-      // all of the unified L1 / shared storage as shared memory, so that two
-      // CTAs fit when the operands allow
-      e = cudaFuncSetAttribute(hot_k, cudaFuncAttributePreferredSharedMemoryCarveout,
-                               cudaSharedmemCarveoutMaxShared);
-      if (e != cudaSuccess) return e;
-      int smem_per_sm = 0;
-      e = cudaDeviceGetAttribute(&smem_per_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
-      if (e != cudaSuccess) return e;
-      // 1 KB of each CTA's shared memory is reserved by the driver
-      int per_sm = static_cast<int>(static_cast<size_t>(smem_per_sm) / (smem + 1024));
-      if (per_sm > 2) per_sm = 2;
-      ctas_per_sm[dev][ti] = per_sm < 1 ? 1 : per_sm;
-      attr_bytes[dev][ti] = smem;
-    }
+    // 1 KB of each CTA's shared memory is reserved by the driver
+    int per_sm = static_cast<int>(limits.per_sm / (smem + 1024));
+    if (per_sm > 2) per_sm = 2;
+    if (per_sm < 1) per_sm = 1;
     // resident CTAs x tensor-memory columns must fit the SM's 512
-    int per_sm = ctas_per_sm[dev][ti];
     if (per_sm * static_cast<int>(tmem_cols) > 512) per_sm = static_cast<int>(512 / tmem_cols);
     const int64_t tiles = static_cast<int64_t>(d->T) * ((d->B + kFM - 1) / kFM);
     int64_t grid = static_cast<int64_t>(per_sm) * L.num_sms;
     if (grid > tiles) grid = tiles;
     if (grid < 1) grid = 1;
 
-    // byte tiles: one CTA per SM, as many ring stages as shared memory holds
-    // (the transpose buffer when at least two stages fit beside it)
-    static size_t bytes_attr[64][2] = {};
-    static int bytes_stages[64][2] = {};
-    static int bytes_nmax[64][2] = {};
-    static bool bytes_xpose[64][2] = {};
-    if (bytes_nmax[dev][ti] != a.n_max) {
-      int optin = 0;
-      e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-      if (e != cudaSuccess) return e;
-      const bool xpose = fwd_bytes_smem_bytes(a.n_max, 2, true) <= static_cast<size_t>(optin);
-      int stages = kBMaxStages;
-      while (stages > 1 && fwd_bytes_smem_bytes(a.n_max, stages, xpose) > static_cast<size_t>(optin))
-        --stages;
-      const size_t bsmem = fwd_bytes_smem_bytes(a.n_max, stages, xpose);
-      const void* k = xpose ? (bf16 ? reinterpret_cast<const void*>(forward_bytes_kernel<true, true>)
-                                    : reinterpret_cast<const void*>(forward_bytes_kernel<true, false>))
-                            : (bf16 ? reinterpret_cast<const void*>(forward_bytes_kernel<false, true>)
-                                    : reinterpret_cast<const void*>(forward_bytes_kernel<false, false>));
-      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bsmem));
-      if (e != cudaSuccess) return e;
-      bytes_attr[dev][ti] = bsmem;
-      bytes_stages[dev][ti] = stages;
-      bytes_xpose[dev][ti] = xpose;
-      bytes_nmax[dev][ti] = a.n_max;
-    }
+    const BytesShape bytes = bytes_shape(a.n_max, limits.optin);
     int64_t bgrid = L.num_sms < tiles ? L.num_sms : tiles;
     if (bgrid < 1) bgrid = 1;
     // both kernels together are the hot part of the forward
     probe_begin(TBE_PROBE_FORWARD_HOT, L.s);
     const unsigned bg = static_cast<unsigned>(bgrid);
-    const size_t bs = bytes_attr[dev][ti];
-    const int st = bytes_stages[dev][ti];
-    if (bytes_xpose[dev][ti]) {
+    const size_t bs = bytes.smem;
+    const int st = bytes.stages;
+    if (bytes.xpose) {
       if (bf16) forward_bytes_kernel<true, true><<<bg, kBThreads, bs, L.s>>>(a, tmem_cols, st);
       else forward_bytes_kernel<true, false><<<bg, kBThreads, bs, L.s>>>(a, tmem_cols, st);
     } else {

@@ -29,6 +29,8 @@
 // hot_part[t][p][slot][c] and restarted.  The finishing kernel sums the
 // partitions in order.  Every mbarrier wait is bounded (time-out:
 // TBE_ERR_TIMEOUT in the status word, drain, free).
+#include <mutex>
+
 #include "common.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
@@ -590,34 +592,45 @@ __global__ void __launch_bounds__(kGThreads, 2) hot_grad_bytes_kernel(HotGradArg
   if (warp == 0) tmem_dealloc(tmem, tmem_cols);
 }
 
+// The kernels' set-up on the current device, made by the first call: each may use as much shared
+// memory as its largest launch does.  That belongs to the kernel, so a call that asked for its own
+// size could take from another host thread's.
+cudaError_t prepare_hot_grad() {
+  static std::mutex mu;
+  static bool made[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  const std::lock_guard<std::mutex> lk(mu);
+  if (made[dev]) return cudaSuccess;
+  const struct {
+    const void* kernel;
+    size_t most;
+  } kernels[] = {
+      {reinterpret_cast<const void*>(hot_grad_tc_kernel<false>), hot_grad_smem_bytes(2)},
+      {reinterpret_cast<const void*>(hot_grad_tc_kernel<true>), hot_grad_smem_bytes(2)},
+      {reinterpret_cast<const void*>(hot_grad_bytes_kernel), hot_grad_bytes_smem_bytes(2)}};
+  for (const auto& k : kernels) {
+    e = cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(k.most));
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(k.kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+  }
+  made[dev] = true;
+  return cudaSuccess;
+}
+
 }  // namespace
 
 cudaError_t launch_hot_grad(const Launch& L, const WsLayout& W, char* ws, const float* grad_out) {
   const int max_mtiles = L.d->max_D > kGM ? 2 : 1;
   const size_t smem = hot_grad_smem_bytes(max_mtiles);
   const size_t bsmem = hot_grad_bytes_smem_bytes(max_mtiles);
-  static size_t attr_bytes[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  cudaError_t e = prepare_hot_grad();
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (attr_bytes[dev] != smem) {
-    for (const void* k : {reinterpret_cast<const void*>(hot_grad_tc_kernel<false>),
-                          reinterpret_cast<const void*>(hot_grad_tc_kernel<true>)}) {
-      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-      if (e != cudaSuccess) return e;
-      e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout,
-                               cudaSharedmemCarveoutMaxShared);
-      if (e != cudaSuccess) return e;
-    }
-    e = cudaFuncSetAttribute(hot_grad_bytes_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(bsmem));
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(hot_grad_bytes_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             cudaSharedmemCarveoutMaxShared);
-    if (e != cudaSuccess) return e;
-    attr_bytes[dev] = smem;
-  }
   HotGradArgs a;
   a.grad_out = grad_out;
   a.D_offsets = L.d->D_offsets;
