@@ -9,8 +9,8 @@
  *
  * R rows of H columns, 1 <= H <= TBE_MAX_NORM_WIDTH.  The norm is of the sum as
  * it is held in the rows' type, so that the gradients, which read h, belong to it.
- * Squares, sums and products are fp32 (a square above 2^128 overflows: u = 0); each
- * result is rounded once.  A row of zeros with eps = 0 follows the formula (NaN).
+ * Squares, sums and products are fp32 (a square above 2^128 overflows: u = 0; one below
+ * 2^-149 is lost, which shows where eps is no larger); each result is rounded once.  A row of zeros with eps = 0 follows the formula (NaN).
  *
  * Matrices are row-major with a row stride in elements (at least the row's columns);
  * their columns are contiguous.  dtype (x, residual, h, y and the gradients of rows) is
@@ -48,7 +48,10 @@ tbe_status tbe_rms_norm(const void* x, const void* residual, const void* weight,
 /* The norm quantised to e4m3 with one scale for each 128 columns of a row, as
  * tbe_expert_product takes it (the arithmetic of tbe_quantize_weights in
  * tbe_experts.h, on the unrounded fp32 products h * u * weight):
- * q [R, H] one byte a value, scale [R, ceil(H / 128)] fp32 (contiguous). */
+ * q [R, H] one byte a value, scale [R, ceil(H / 128)] fp32 (contiguous).
+ * It is for products of all rows with one expert.  Experts that a router chooses take
+ * rows sorted by expert, which no call here makes of 8-bit rows, and the router itself needs y:
+ * there take tbe_rms_norm, and tbe_expert_dispatch_fp8 quantises the rows on their way. */
 tbe_status tbe_rms_norm_fp8(const void* x, const void* residual, const void* weight,
                             int32_t dtype, int32_t weight_dtype, int64_t rows, int64_t width,
                             int64_t x_stride, int64_t residual_stride, float eps, void* h,

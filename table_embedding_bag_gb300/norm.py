@@ -1,5 +1,6 @@
 """Binding of the root-mean-square norm (include/tbe_norm.h): with the residual's
-addition, in the rows' type or in 8 bits for tbe_expert_product, and its gradients.
+addition, in the rows' type or in 8 bits for a tbe_expert_product of all rows with one
+expert, and its gradients.
 
 As in the rest of the package the functions only check and marshal their
 arguments; outputs that are not given are allocated on the stream the call runs on,
@@ -88,7 +89,8 @@ def tbe_rms_norm(x, weight=None, residual=None, eps=1e-6, out=None, h=None, stre
 def tbe_rms_norm_fp8(x, weight=None, residual=None, eps=1e-6, out=None, scale=None, h=None,
                      stream=None):
     """tbe_rms_norm with the result quantised to e4m3, one fp32 scale for each 128 columns, as
-    tbe_expert_product takes it: (q, scale), or (q, scale, h) with a residual."""
+    tbe_expert_product takes it of one expert for all rows: (q, scale), or (q, scale, h) with a
+    residual.  Routed experts take their rows from tbe_rms_norm by tbe_expert_dispatch_fp8."""
     device, xs, w, wt, rs, h, hs = _inputs(x, weight, residual, h, stream)
     rows, width = x.shape
     out, qs, scale = _fp8_out(stream, device, x, rows, out, scale)
