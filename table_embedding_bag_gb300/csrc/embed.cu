@@ -1006,7 +1006,7 @@ extern "C" tbe_status tbe_embed_backward(const void* grad_out, int32_t dtype, in
     constexpr size_t kMostSmem = kRing + ((kMoveThreads + 2) * kMostPiece + 2) * sizeof(Item);
     const tbe_status summed = launch(embed_sum_kernel<T, O, kAligned>, grid, kMoveThreads, smem,
                                      kMostSmem, true, s, args, lg);
-    if (summed != TBE_OK || pieces < 3) return summed;  // no run is long
+    if (summed != TBE_OK) return summed;
     const dim3 joins(static_cast<unsigned>((pieces + join - 1) / join),
                      static_cast<unsigned>(slices));
     return launch(embed_join_kernel<O>, joins, kJoinLanes * kJoinSegments, 0, 0, true, s, args);
