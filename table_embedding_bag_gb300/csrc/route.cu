@@ -296,8 +296,8 @@ __host__ __device__ constexpr int most_by_bound(int L) { return L == 32 ? 16 : L
 // K-th choice from below, so only choices from there on are candidates, a few more than K;
 // they are moved to shared memory, ranked against one another, a lane each, and put in
 // order: lane j of a row gets the j-th, past K too.  In rounds every expert chosen costs a look
-// over the lane's V choices (65536 rows of bf16, 8 of 128: 20.9 us, in rounds 31.3; 4 of 64: 9.9 and
-// 11.1).  *bound: no other choice is above it.  -2 throughout where a row
+// over the lane's V choices (65536 rows of bf16, 8 of 128: 21.6 us, in rounds 31.8; 4 of 64: 10.4 and
+// 11.6; 8 of 256 by sigmoid and bias 43.9 and 77).  *bound: no other choice is above it.  -2 throughout where a row
 // has more candidates than lanes.
 template <int V, int L>
 __device__ __forceinline__ int choose_by_bound(float (&c)[V], int e0, int K, Candidates& room,
@@ -371,10 +371,11 @@ __device__ __forceinline__ int choose_by_bound(float (&c)[V], int e0, int K, Can
 // A row's experts are shared by L lanes, V consecutive ones a lane at most; 32 / L rows a warp.
 //
 // Instructions bound it (65536 rows, eight of 256 experts in four of eight groups by sigmoid and
-// bias: 51 us for a floor of 10.5 in bytes; 732 a row, issued in 85 % of the cycles), so reductions
+// bias: 53 us for a floor of 10.5 in bytes; 769 a row, issued in 85 % of the cycles), so reductions
 // are the warp's own (redux), the choice looks over few candidates, and what exact arithmetic
-// would cost is kept for the rows that need it.  Five CTAs a multiprocessor: 54 us with four, 53
-// with six.
+// would cost is kept for the rows that need it.  Five CTAs a multiprocessor: 53.6 us, with four
+// 56.5, with six 55.6; in sixteen other forms, of 8 to 32 lanes a row, five are within 5 % of the best
+// of the three, though at 48 registers those of 8 and 16 lanes spill 36 to 68 bytes.
 // kCandidates: choose_by_bound, which has a kernel of its own as its registers cost the rounds 5 %.
 template <typename T, int V, int L, bool kCandidates>
 __global__ void __launch_bounds__(256, V <= 8 ? 5 : 1)
