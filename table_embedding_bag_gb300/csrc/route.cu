@@ -235,9 +235,9 @@ __device__ __forceinline__ float weight_of(float l, bool on, bool sigmoid, bool 
     return sigmoid ? logistic(l) : __fdiv_rn(expf(l - r.top), r.sum);
   }
   const float top = row_max<L>(on ? l : kClosed);
-  // sigmoid(l) is exp(l) to the last bit where no logit is above -60, and exp(l - top) does not
-  // underflow
-  const float p = !on ? 0.f : sigmoid && !(top < -60.f) ? logistic(l) : expf(l - top);
+  // sigmoid(l) is exp(l) to a quarter of the last bit where no logit is above -18, and exp(l - top)
+  // does not underflow
+  const float p = !on ? 0.f : sigmoid && !(top < -18.f) ? logistic(l) : expf(l - top);
   const float sum = row_sum<L>(p);
   if (!on) return 0.f;
   // a NaN among the row's scores makes every softmax weight one

@@ -66,3 +66,27 @@ def test_sigmoid_weights(dtype):
     ids, w = tbe.tbe_expert_route(far, 6, score="sigmoid", scale=1.0)
     s = torch.softmax(torch.nn.functional.logsigmoid(far.double().gather(1, ids.long())), 1)
     assert bool(((w.double() - s).abs() <= (2 * 10 + 5 + 1) * U * s).all())
+
+
+@pytest.mark.parametrize("top", [-18, -19, -30, -59, -60, -61, -90])
+def test_sigmoid_weights_whose_scores_underflow(top):
+    # the ratio of two scores of which fp32 holds the smaller one badly or not at all
+    logits = torch.full((90, 8), float(top), device="cuda")
+    logits[:, 3] = top - torch.arange(90, device="cuda").float()
+    if top == -18:  # the scores themselves are taken: to e^-87
+        logits = logits[:60]
+    how = dict(score="sigmoid", scale=1.0)
+    ids, w = tbe.tbe_expert_route(logits, 8, **how)
+    l = logits.double().gather(1, ids.long())
+    s = torch.softmax(torch.nn.functional.logsigmoid(l), 1)
+    # the scores' own off by a quarter of a unit more than exponentials, a normal result
+    bound = (2 * 10 + 5 + 1) * U * s + 2.0 ** -126
+    assert bool(((w.double() - s).abs() <= bound).all())
+    # its gradient by differences of logarithms: d w_j / d l_i = w_j (1 - s_i) (i == j) - w_j w_i (1 - s_i)
+    gw = torch.ones_like(w)
+    gw[:, -1] = 3.0
+    got = tbe.tbe_expert_route_backward(gw, logits, ids, **how).gather(1, ids.long())
+    one = 1 / (1 + torch.exp(l))
+    ref = s * one * (gw.double() - (gw.double() * s).sum(1, keepdim=True))
+    size = s * (gw.double() + (gw.double() * s).sum(1, keepdim=True))
+    assert bool(((got.double() - ref).abs() <= 2.0 ** -18 * size + 2.0 ** -126).all())
