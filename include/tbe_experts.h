@@ -56,9 +56,9 @@ enum { TBE_SCORE_SOFTMAX = 1, TBE_SCORE_SIGMOID = 2 };
  * wherever 64 bits tell the c apart: where fp32 does not, it is made again in 64 bits.
  * Without a bias the experts' logits themselves are compared.  The bias only chooses: weights
  * are of s, in fp32 by exponentials to two units in the last place and rounded divisions, in
- * tbe_expert_route_backward too.  NaN ranks above everything, so a token with a NaN logit shows it in its
- * weights; softmax of +inf is NaN as the formula gives, and a row that is closed
- * throughout has ids -1.
+ * tbe_expert_route_backward too.  NaN ranks above everything, so a token with a NaN logit
+ * shows it in its weights; softmax of +inf is NaN as the formula gives, and a row that is
+ * closed throughout has ids -1.
  * logits have a row stride in elements; ids and weights are contiguous.
  * Errors: TBE_EINVAL (sizes: k > top_groups * E / G, E not a multiple of G, ...; a scale that is
  * not finite), TBE_EUNSUPPORTED (types, E > TBE_MAX_EXPERTS, k > TBE_MAX_CHOSEN, G > 32,

@@ -10,7 +10,8 @@
  * R rows of H columns, 1 <= H <= TBE_MAX_NORM_WIDTH.  The norm is of the sum as
  * it is held in the rows' type, so that the gradients, which read h, belong to it.
  * Squares, sums and products are fp32 (a square above 2^128 overflows: u = 0; one below
- * 2^-149 is lost, which shows where eps is no larger); each result is rounded once.  A row of zeros with eps = 0 follows the formula (NaN).
+ * 2^-149 is lost, which shows where eps is no larger); each result is rounded once.  A row
+ * of zeros with eps = 0 follows the formula (NaN).
  *
  * Matrices are row-major with a row stride in elements (at least the row's columns);
  * their columns are contiguous.  dtype (x, residual, h, y and the gradients of rows) is

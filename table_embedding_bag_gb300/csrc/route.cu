@@ -297,8 +297,8 @@ __host__ __device__ constexpr int most_by_bound(int L) { return L == 32 ? 16 : L
 // they are moved to shared memory, ranked against one another, a lane each, and put in
 // order: lane j of a row gets the j-th, past K too.  In rounds every expert chosen costs a look
 // over the lane's V choices (65536 rows of bf16, 8 of 128: 21.6 us, in rounds 31.8; 4 of 64: 10.4 and
-// 11.6; 8 of 256 by sigmoid and bias 43.9 and 77).  *bound: no other choice is above it.  -2 throughout where a row
-// has more candidates than lanes.
+// 11.6; 8 of 256 by sigmoid and bias, fp32: 43.9 and 77).  *bound: no other choice is above it.
+// -2 throughout where a row has more candidates than lanes.
 template <int V, int L>
 __device__ __forceinline__ int choose_by_bound(float (&c)[V], int e0, int K, Candidates& room,
                                                float* bound) {
@@ -546,8 +546,9 @@ __global__ void __launch_bounds__(256, V <= 8 ? 5 : 1)
     const float score = mine >= 0 ? score_of(chosen, P.sigmoid, scale.top, inverse) : 0.f;
     const float s = mine >= 0 ? choice_of(chosen, b, P.sigmoid, scale.top, inverse) : kClosed;
     // (softmax: and by what the exponential drops below 2^-126)
-    const float off = P.sigmoid ? 0x1.1p-22f
-                                : fmaf(score * 0x1p-24f, 34.f + 2.f * (scale.top - chosen), 0x1p-125f);
+    const float below = scale.top - chosen;
+    const float off =
+        P.sigmoid ? 0x1.1p-22f : fmaf(score * 0x1p-24f, 34.f + 2.f * below, 0x1p-125f);
     const float lp = __shfl_up_sync(kAll, chosen, 1), bp = __shfl_up_sync(kAll, b, 1);
     const float sp = __shfl_up_sync(kAll, s, 1), op = __shfl_up_sync(kAll, off, 1);
     const auto far = [&](float more, float less, float by) {
